@@ -17,13 +17,21 @@ Names follow the C ABI:
   and k and the store of k and v into the paged cache, ahead of decode
 * ``paged_prefill_plan(...)`` / ``paged_prefill_attn(...)``: attention for
   requests of any query length over a host-made work list
+
+and of ``include/paged_step.h``, the calls around them in a serving step:
+
+* ``paged_decode_attn_sinks(...)``, ``paged_prefill_plan_sinks(...)`` /
+  ``paged_prefill_attn_sinks(...)``: a sliding window whose first tokens
+  stay visible
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
+import struct
 from typing import Optional
 
 import torch
@@ -45,6 +53,7 @@ COUNTERS_PER_PAIR = 16  # PD_COUNTERS_PER_PAIR
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "paged_decode.h")
+STEP_HEADER = os.path.join(os.path.dirname(HEADER), "paged_step.h")
 
 
 class PagedDecodeError(RuntimeError):
@@ -156,13 +165,28 @@ def lib():
         L.paged_prefill_attn.argtypes = [T] * 7 + [ctypes.POINTER(PdPrefillPlanInfo), T] + \
             [i32] * 5 + [f32, i32, ctypes.POINTER(PdScratch), vp]
         L.paged_prefill_attn.restype = i32
+        # (paged_step.h: packed descriptors, passed as bytes)
+        L.paged_decode_attn_sinks.argtypes = [vp] * 7 + [i32] * 7 + [
+            f32, i32, ctypes.POINTER(PdScratch), vp, ctypes.POINTER(PdOptions)]
+        L.paged_decode_attn_sinks.restype = i32
+        L.paged_decode_plan_sinks.argtypes = [i32] * 10 + [ctypes.POINTER(PdScratch),
+                                                           ctypes.POINTER(PdOptions),
+                                                           ctypes.POINTER(PdPlan)]
+        L.paged_decode_plan_sinks.restype = i32
+        L.paged_prefill_plan_sinks.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, i64,
+                                               ctypes.POINTER(PdPrefillPlanInfo)]
+        L.paged_prefill_plan_sinks.restype = i32
+        L.paged_prefill_attn_sinks.argtypes = [vp] * 7 + [ctypes.POINTER(PdPrefillPlanInfo), vp] + \
+            [i32] * 6 + [f32, i32, ctypes.POINTER(PdScratch), vp]
+        L.paged_prefill_attn_sinks.restype = i32
         _lib = L
     return _lib
 
 
-def declared_symbols() -> list:
-    """Function names the public header declares."""
-    text = open(HEADER).read()
+def declared_symbols(header: str = HEADER) -> list:
+    """Function names a public header declares (paged_decode.h, or
+    ``STEP_HEADER``)."""
+    text = open(header).read()
     return re.findall(r"PD_API\s+[\w\s\*]*?\b(paged_\w+)\s*\(", text)
 
 
@@ -186,6 +210,59 @@ def tensor_desc(t: torch.Tensor) -> PdTensor:
         d.shape[i] = t.shape[i]
         d.stride[i] = t.stride(i)
     return d
+
+
+_DESC = [struct.Struct("Pii%dq%dx%dq%dx" % (n, 8 * (4 - n), n, 8 * (4 - n))) for n in range(5)]
+assert _DESC[4].size == ctypes.sizeof(PdTensor)
+
+
+def _packed(t: Optional[torch.Tensor]) -> Optional[bytes]:
+    """The bytes of ``tensor_desc(t)`` (None: no tensor).  A step makes some
+    dozens of these, and packing takes a third of the time of filling a
+    ctypes structure (0.8 against 2.4 us)."""
+    if t is None:
+        return None
+    n = t.dim()
+    if n > 4:
+        return bytes(tensor_desc(t))
+    return _DESC[n].pack(t.data_ptr(), _DTYPES.get(t.dtype, 99), n, *t.shape, *t.stride())
+
+
+_NO_DEVICE = contextlib.nullcontext()
+
+
+def _launch_on(tensors, stream):
+    """(context, stream handle) of a launch on the tensors' device, whichever
+    is current, or None when they are not on one CUDA device.  Without any
+    CUDA device the library is left to report that."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            return None
+    if dev.type != "cuda":
+        return None if torch.cuda.is_available() else (_NO_DEVICE, 0)
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if dev.index == torch.cuda.current_device():
+        return _NO_DEVICE, handle
+    return torch.cuda.device(dev), handle
+
+
+def _step_call(name, tensors, args, stream, check):
+    """A call of paged_step.h: ``args(packed tensors, stream handle)`` gives
+    the C arguments.  Tensors on several devices, or on none that the library
+    runs on, are PD_EINVAL."""
+    where = _launch_on(tensors, stream)
+    if where is None:
+        rc = -1
+    else:
+        with where[0]:
+            rc = getattr(lib(), name)(*args([_packed(t) for t in tensors], where[1]))
+    if check and rc != PD_OK:
+        raise PagedDecodeError(rc, name)
+    return rc
 
 
 def options(**kw) -> PdOptions:
@@ -322,6 +399,43 @@ def paged_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_size, page_size,
     return plan.as_dict()
 
 
+def paged_decode_attn_sinks(q, k_cache, v_cache, block_table, seq_lens, out, num_q_heads,
+                            num_kv_heads, head_size, page_size, max_query_len, window, sinks,
+                            scale, layout, scratch: Optional[Scratch] = None, query_start=None,
+                            stream=None, opts: Optional[PdOptions] = None,
+                            check: bool = True) -> int:
+    """The decode call over a sliding window beside which the first ``sinks``
+    tokens of every sequence stay visible (see paged_step.h);
+    ``query_start`` as in ``paged_decode_attn_varlen``, or None for
+    ``max_query_len`` query tokens per sequence."""
+    sp = ctypes.byref(scratch.desc) if scratch is not None else None
+    op = ctypes.byref(opts) if opts is not None else None
+    return _step_call(
+        "paged_decode_attn_sinks",
+        (q, k_cache, v_cache, block_table, seq_lens, query_start, out),
+        lambda t, st: (*t, int(num_q_heads), int(num_kv_heads), int(head_size), int(page_size),
+                       int(max_query_len), int(window), int(sinks), float(scale), int(layout), sp,
+                       st, op),
+        stream, check)
+
+
+def paged_decode_plan_sinks(num_seqs, num_q_heads, num_kv_heads, head_size, page_size,
+                            max_query_len, window, sinks, block_table_width, num_sms,
+                            scratch: Optional[Scratch] = None, opts: Optional[PdOptions] = None,
+                            scratch_desc: Optional[PdScratch] = None) -> dict:
+    """The launch plan of ``paged_decode_attn_sinks`` (host only)."""
+    plan = PdPlan()
+    sd = scratch.desc if scratch is not None else scratch_desc
+    rc = lib().paged_decode_plan_sinks(num_seqs, num_q_heads, num_kv_heads, head_size, page_size,
+                                       max_query_len, window, sinks, block_table_width, num_sms,
+                                       ctypes.byref(sd) if sd is not None else None,
+                                       ctypes.byref(opts) if opts is not None else None,
+                                       ctypes.byref(plan))
+    if rc != PD_OK:
+        raise PagedDecodeError(rc, "paged_decode_plan_sinks")
+    return plan.as_dict()
+
+
 def paged_rope_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache,
                            v_cache, num_q_heads, num_kv_heads, head_size, rot_dim, page_size,
                            layout, is_neox=True, stream=None, check: bool = True) -> int:
@@ -350,31 +464,44 @@ def rope_case(case, q_out=None, stream=None):
     return q_out
 
 
+def _prefill_plan(what, query_start, seq_lens, args):
+    """(items int32 [n, 8] as a CPU tensor, info) of a prefill planner of the
+    library: a size query, then the items."""
+    qs = torch.as_tensor(query_start, dtype=torch.int32).contiguous()
+    sl = torch.as_tensor(seq_lens, dtype=torch.int32).contiguous()
+    S = int(sl.shape[0])
+    if qs.shape[0] != S + 1:
+        raise PagedDecodeError(-1, what)
+    info = PdPrefillPlanInfo()
+    call = getattr(lib(), what)
+    rc = call(qs.data_ptr(), sl.data_ptr(), S, *args, None, 0, ctypes.byref(info))
+    if rc != PD_OK:
+        raise PagedDecodeError(rc, what)
+    items = torch.zeros((int(info.num_items), 8), dtype=torch.int32)
+    rc = call(qs.data_ptr(), sl.data_ptr(), S, *args,
+              items.data_ptr() if items.numel() else None, int(info.num_items),
+              ctypes.byref(info))
+    if rc != PD_OK:
+        raise PagedDecodeError(rc, what)
+    return items, info
+
+
 def paged_prefill_plan(query_start, seq_lens, num_q_heads, num_kv_heads, head_size, window,
                        num_sms=0):
     """The work list of a prefill launch for this head size, made on the host
     (see the C header): returns (items int32 [n, 8] as a CPU tensor,
     PdPrefillPlanInfo)."""
-    qs = torch.as_tensor(query_start, dtype=torch.int32).contiguous()
-    sl = torch.as_tensor(seq_lens, dtype=torch.int32).contiguous()
-    S = int(sl.shape[0])
-    if qs.shape[0] != S + 1:
-        raise PagedDecodeError(-1, "paged_prefill_plan")
-    info = PdPrefillPlanInfo()
-    L = lib()
-    rc = L.paged_prefill_plan(qs.data_ptr(), sl.data_ptr(), S, int(num_q_heads),
-                              int(num_kv_heads), int(head_size), int(window), int(num_sms), None,
-                              0, ctypes.byref(info))
-    if rc != PD_OK:
-        raise PagedDecodeError(rc, "paged_prefill_plan")
-    items = torch.zeros((int(info.num_items), 8), dtype=torch.int32)
-    rc = L.paged_prefill_plan(qs.data_ptr(), sl.data_ptr(), S, int(num_q_heads),
-                              int(num_kv_heads), int(head_size), int(window), int(num_sms),
-                              items.data_ptr() if items.numel() else None, int(info.num_items),
-                              ctypes.byref(info))
-    if rc != PD_OK:
-        raise PagedDecodeError(rc, "paged_prefill_plan")
-    return items, info
+    return _prefill_plan("paged_prefill_plan", query_start, seq_lens,
+                         (int(num_q_heads), int(num_kv_heads), int(head_size), int(window),
+                          int(num_sms)))
+
+
+def paged_prefill_plan_sinks(query_start, seq_lens, num_q_heads, num_kv_heads, head_size, window,
+                             sinks, num_sms=0):
+    """The work list of ``paged_prefill_attn_sinks``."""
+    return _prefill_plan("paged_prefill_plan_sinks", query_start, seq_lens,
+                         (int(num_q_heads), int(num_kv_heads), int(head_size), int(window),
+                          int(sinks), int(num_sms)))
 
 
 def paged_prefill_scratch_bytes(num_kv_heads, head_size, num_sms) -> int:
@@ -407,6 +534,23 @@ def paged_prefill_attn(q, k_cache, v_cache, block_table, seq_lens, query_start, 
     if check and rc != PD_OK:
         raise PagedDecodeError(rc, "paged_prefill_attn")
     return rc
+
+
+def paged_prefill_attn_sinks(q, k_cache, v_cache, block_table, seq_lens, query_start, work, info,
+                             out, num_q_heads, num_kv_heads, head_size, page_size, window, sinks,
+                             scale, layout, scratch: Optional["Scratch"] = None, stream=None,
+                             check: bool = True) -> int:
+    """The prefill call over a sliding window beside which the first
+    ``sinks`` tokens stay visible (``work`` and ``info`` from
+    ``paged_prefill_plan_sinks``)."""
+    sp = ctypes.byref(scratch.desc) if scratch is not None else None
+    return _step_call(
+        "paged_prefill_attn_sinks",
+        (q, k_cache, v_cache, block_table, seq_lens, query_start, work, out),
+        lambda t, st: (*t[:7], ctypes.byref(info), t[7], int(num_q_heads), int(num_kv_heads),
+                       int(head_size), int(page_size), int(window), int(sinks), float(scale),
+                       int(layout), sp, st),
+        stream, check)
 
 
 def prefill_case(case, out=None, scratch=None, stream=None, num_sms=0, plan=None):

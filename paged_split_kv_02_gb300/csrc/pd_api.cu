@@ -186,12 +186,12 @@ struct PlanOut {
   int nt, kg, ns;
 };
 
-int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int bt_width, int num_sms,
-              const pd_scratch *scratch, const pd_options *opts, pd_plan *plan) {
+int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks, int bt_width,
+              int num_sms, const pd_scratch *scratch, const pd_options *opts, pd_plan *plan) {
   pd_options o{};
   if (opts) o = *opts;
   if (S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || P <= 0 || P % kBlockKeys != 0 ||
-      window < 0 || bt_width < 1 || num_sms <= 0)
+      window < 0 || sinks < 0 || bt_width < 1 || num_sms <= 0)
     return PD_EINVAL;
   if (D != 64 && D != 128 && D != 256 && D != 512) return PD_EHEAD;
   if (M < 1 || M > 8) return PD_EQLEN;
@@ -203,6 +203,8 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int bt_wi
   if (o.mergers < 0 || (o.mergers & (o.mergers - 1)) != 0) return PD_EINVAL;
   const bool tc = o.path == 3, dot = o.path == 2;
   if ((tc || dot) && D > 256) return PD_EINVAL;
+  if (window == 0) sinks = 0;  // every key is visible
+  if ((tc || dot) && sinks > 0) return PD_EINVAL;  // built for mma.sync
   if ((tc || dot) && o.cluster > 1) return PD_EINVAL;
   const int G = Hq / Hkv, R = G * M;
   // One sequence: at most 16 packed rows per CTA.  Every n-tile warp of a
@@ -252,7 +254,9 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int bt_wi
 
   // KV blocks (16 keys) a (sequence, kv head, row group) can span at most.
   int64_t nb_max = cdiv((int64_t)bt_width * P, kBlockKeys);
-  if (window > 0) nb_max = std::min<int64_t>(nb_max, cdiv(window + M - 1, kBlockKeys) + 1);
+  if (window > 0)
+    nb_max = std::min<int64_t>(
+        nb_max, cdiv((int64_t)window + M - 1, kBlockKeys) + 1 + cdiv(sinks, kBlockKeys));
   const int64_t units = (int64_t)S * Hkv * rg;
   const int64_t target = o.max_ctas_hint > 0 ? o.max_ctas_hint : num_sms;
   // a segment reads at least one and a half stages (~10 segments of 1k keys
@@ -437,14 +441,14 @@ int element_dtype_ok(const pd_tensor *t, int want) { return t->dtype == want; }
 int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,
               const pd_tensor *block_table, const pd_tensor *seq_lens,
               const pd_tensor *query_start, pd_tensor *out, int num_q_heads, int num_kv_heads,
-              int head_size, int page_size, int max_query_len, int window, float scale,
+              int head_size, int page_size, int max_query_len, int window, int sinks, float scale,
               int layout, pd_scratch *scratch, void *stream, const pd_options *opts) {
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out) return PD_EINVAL;
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return PD_EINVAL;
   if (head_size != 64 && head_size != 128 && head_size != 256 && head_size != 512) return PD_EHEAD;
   if (max_query_len < 1 || max_query_len > 8) return PD_EQLEN;
   if (page_size <= 0 || page_size % kBlockKeys != 0) return PD_EINVAL;
-  if (window < 0 || !std::isfinite(scale)) return PD_EINVAL;
+  if (window < 0 || sinks < 0 || !std::isfinite(scale)) return PD_EINVAL;
   if (layout != PD_NHD && layout != PD_HND) return PD_EINVAL;
   if (seq_lens->ndim != 1 || !seq_lens->data || seq_lens->stride[0] != 1) return PD_EINVAL;
   if (!element_dtype_ok(seq_lens, PD_I32) || !element_dtype_ok(block_table, PD_I32)) return PD_EDTYPE;
@@ -482,7 +486,7 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
   if ((rc = device_info(&dev)) != PD_OK) return rc;
   pd_plan plan;
   rc = make_plan((int)S, num_q_heads, num_kv_heads, head_size, page_size, max_query_len, window,
-                 (int)block_table->shape[1], dev.num_sms, scratch, opts, &plan);
+                 sinks, (int)block_table->shape[1], dev.num_sms, scratch, opts, &plan);
   if (rc != PD_OK) return rc;
   if (query_start && plan.path == 3) return PD_EINVAL;  // not built for variable lengths
 
@@ -511,6 +515,7 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
   p.M = max_query_len;
   p.P = page_size;
   p.window = window;
+  p.sinks = window > 0 ? sinks : 0;
   p.layout = layout;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.R = plan.rows;
@@ -575,6 +580,23 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
 }
 
 }  // namespace
+
+int attn_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,
+              const pd_tensor *block_table, const pd_tensor *seq_lens,
+              const pd_tensor *query_start, pd_tensor *out, int num_q_heads, int num_kv_heads,
+              int head_size, int page_size, int max_query_len, int window, int sinks, float scale,
+              int layout, pd_scratch *scratch, void *stream, const pd_options *opts) {
+  return attn_impl(q, k_cache, v_cache, block_table, seq_lens, query_start, out, num_q_heads,
+                   num_kv_heads, head_size, page_size, max_query_len, window, sinks, scale, layout,
+                   scratch, stream, opts);
+}
+
+int attn_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_size, int page_size,
+              int max_query_len, int window, int sinks, int block_table_width, int num_sms,
+              const pd_scratch *scratch, const pd_options *opts, pd_plan *plan) {
+  return make_plan(num_seqs, num_q_heads, num_kv_heads, head_size, page_size, max_query_len,
+                   window, sinks, block_table_width, num_sms, scratch, opts, plan);
+}
 
 int device_check(int *num_sms, unsigned int **status) {
   DeviceInfo d;
@@ -651,7 +673,7 @@ int paged_decode_attn(const pd_tensor *q, const pd_tensor *k_cache, const pd_ten
                       int max_query_len, int window, float scale, int layout,
                       pd_scratch *scratch, void *stream) {
   return attn_impl(q, k_cache, v_cache, block_table, seq_lens, nullptr, out, num_q_heads,
-                   num_kv_heads, head_size, page_size, max_query_len, window, scale, layout,
+                   num_kv_heads, head_size, page_size, max_query_len, window, 0, scale, layout,
                    scratch, stream, nullptr);
 }
 
@@ -661,7 +683,7 @@ int paged_decode_attn_opts(const pd_tensor *q, const pd_tensor *k_cache, const p
                            int max_query_len, int window, float scale, int layout,
                            pd_scratch *scratch, void *stream, const pd_options *opts) {
   return attn_impl(q, k_cache, v_cache, block_table, seq_lens, nullptr, out, num_q_heads,
-                   num_kv_heads, head_size, page_size, max_query_len, window, scale, layout,
+                   num_kv_heads, head_size, page_size, max_query_len, window, 0, scale, layout,
                    scratch, stream, opts);
 }
 
@@ -674,7 +696,7 @@ int paged_decode_attn_varlen(const pd_tensor *q, const pd_tensor *k_cache,
                              const pd_options *opts) {
   if (!query_start) return PD_EINVAL;
   return attn_impl(q, k_cache, v_cache, block_table, seq_lens, query_start, out, num_q_heads,
-                   num_kv_heads, head_size, page_size, max_query_len, window, scale, layout,
+                   num_kv_heads, head_size, page_size, max_query_len, window, 0, scale, layout,
                    scratch, stream, opts);
 }
 
@@ -684,7 +706,7 @@ int paged_decode_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_
                       pd_plan *plan) {
   if (!plan) return PD_EINVAL;
   return make_plan(num_seqs, num_q_heads, num_kv_heads, head_size, page_size, max_query_len,
-                   window, block_table_width, num_sms, scratch, opts, plan);
+                   window, 0, block_table_width, num_sms, scratch, opts, plan);
 }
 
 int paged_decode_device_status(unsigned int *status, int reset, void *stream) {

@@ -76,6 +76,9 @@ struct Params {
   // split tiles and partial slots (per kv head) the scratch holds
   const int32_t *work;
   int pf_groups, pf_slots;
+  // keys at the start of a sequence that stay visible beside the window;
+  // > 0 (then window > 0 too) selects the kernel instances built for it
+  int sinks;
 };
 
 struct Launch {
@@ -179,8 +182,30 @@ inline int64_t epilogue_floats(int D, int NT, int KG, int CS, int ncl_max) {
 // rows on the M side, 16 rows per warp (prefill tiles, D <= 128), 5 =
 // tcgen05 prefill tiles of 128 rows with Q, S, P and O in tensor memory
 // (D = 128)
+// (p.sinks > 0: the instances for a window with sinks, paths 1, 4 and 5)
 cudaError_t launch_mma(int D, bool bf16, int path, const CUtensorMap &tk, const CUtensorMap &tv,
                        const Params &p, const Launch &l, cudaStream_t stream);
+
+// The calls behind the public entry points, with the sinks beside the window
+// (0: none; the entry points without sinks).
+int attn_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,
+              const pd_tensor *block_table, const pd_tensor *seq_lens,
+              const pd_tensor *query_start, pd_tensor *out, int num_q_heads, int num_kv_heads,
+              int head_size, int page_size, int max_query_len, int window, int sinks, float scale,
+              int layout, pd_scratch *scratch, void *stream, const pd_options *opts);
+int attn_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_size, int page_size,
+              int max_query_len, int window, int sinks, int block_table_width, int num_sms,
+              const pd_scratch *scratch, const pd_options *opts, pd_plan *plan);
+int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int num_seqs,
+                      int num_q_heads, int num_kv_heads, int head_size, int window, int sinks,
+                      int num_sms, pd_prefill_item *items, int64_t capacity,
+                      pd_prefill_plan_info *info);
+int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,
+                 const pd_tensor *block_table, const pd_tensor *seq_lens,
+                 const pd_tensor *query_start, const pd_tensor *work,
+                 const pd_prefill_plan_info *info, pd_tensor *out, int num_q_heads,
+                 int num_kv_heads, int head_size, int page_size, int window, int sinks,
+                 float scale, int layout, pd_scratch *scratch, void *stream);
 
 // The current device, checked (an sm_103 part): its SM count and the
 // device status word.  Returns a pd_status.

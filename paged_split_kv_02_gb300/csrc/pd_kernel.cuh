@@ -140,7 +140,7 @@ __device__ __forceinline__ float exp2_or_zero(float x, float m) {
   return sfu_exp2(x - m);
 }
 
-template <int D, bool BF16, bool TC, bool DOT, bool RM, bool TP>
+template <int D, bool BF16, bool TC, bool DOT, bool RM, bool TP, bool SINK>
 __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThreads, 1)
     pd_decode_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ Params p) {
@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
   static_assert(!TP || D == 128, "the tensor-memory prefill consumer serves head size 128");
   static_assert(!RM || D <= 128, "the rows-on-M consumer keeps Q and O of 16 rows in registers");
   static_assert(!DOT || D <= 256, "the warp dot-product consumer serves head sizes up to 256");
+  static_assert(!SINK || (!TC && !DOT), "sinks are built for the mma.sync and prefill consumers");
   using tag = std::integral_constant<bool, BF16>;
   using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
   constexpr int NBOX = D / 64;                  // 128-byte boxes across the head dim
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
   const int spec_b0 = seg * p.seg_blocks;
   const int32_t *bt_row = p.block_table + (int64_t)s * p.bt_stride;
   const int bt_blocks = p.bt_width * bpp;
-  const bool spec_on = warp == NC && p.window == 0 && !prefill;
+  const bool spec_on = !SINK && warp == NC && p.window == 0 && !prefill;
   if (spec_on) {
 #pragma unroll
     for (int k = 0; k < kSpec / 32; ++k) {
@@ -351,8 +352,29 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
     u_lo = p.window ? max(0, n0 - p.window) : 0;
     v_lo = p.window ? max(0, n1 - p.window) : 0;
   }
-  const int b_first = u_lo / kBlockKeys;
-  const int nb = u_hi > u_lo ? (u_hi + kBlockKeys - 1) / kBlockKeys - b_first : 0;
+  int b_first = u_lo / kBlockKeys;
+  int nb = u_hi > u_lo ? (u_hi + kBlockKeys - 1) / kBlockKeys - b_first : 0;
+  // SINK: the blocks of the first p.sinks keys, then those from the union's
+  // window start, counted as one run of nb blocks: block i of the run is the
+  // sequence's block i, and from block sk_nb on block i + sk_gap (the blocks
+  // between, which no row sees, are left out; their pages are never read)
+  int sk_nb = 0, sk_gap = 0;
+  if constexpr (SINK) {
+    sk_nb = (min(p.sinks, u_hi) + kBlockKeys - 1) / kBlockKeys;
+    sk_gap = max(0, b_first - sk_nb);
+    if (nb > 0) nb += b_first - sk_gap;
+    b_first = 0;
+  }
+  auto seq_block = [&](int i) -> int { return SINK && i >= sk_nb ? i + sk_gap : i; };
+  // does a row with the keys [lo, hi) see key k (its window and the sinks);
+  // does every row of the CTA see the 16 keys from key0
+  auto sees = [&](int k, int lo, int hi) -> bool {
+    return k < hi && (k >= lo || (SINK && k < p.sinks));
+  };
+  auto all_see = [&](int key0) -> bool {
+    return key0 + kBlockKeys <= v_hi &&
+           (key0 >= v_lo || (SINK && key0 + kBlockKeys <= p.sinks));
+  };
   // blocks per segment: the plan's, unless the sequence is longer than
   // planned; a prefill tile's segments are its work items' (every one of
   // them arrives at the merge, an empty one with an empty partial)
@@ -424,7 +446,8 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
         i0 = kSpec;
       }
       for (int i = i0 + lane; i < n; i += 32)
-        pids[i] = __ldg(bt_row + (lg_bpp >= 0 ? (my_b0 + base + i) >> lg_bpp : (my_b0 + base + i) / bpp));
+        pids[i] = __ldg(bt_row + (lg_bpp >= 0 ? seq_block(my_b0 + base + i) >> lg_bpp
+                                              : seq_block(my_b0 + base + i) / bpp));
       __syncwarp();
     };
     if (my_nb > 0) load_pids(0);
@@ -438,7 +461,8 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
         pid_base = j * TB;
         load_pids(pid_base);
       }
-      if (!waited && (my_b0 + j * TB + min(TB, my_nb - j * TB)) * kBlockKeys > fresh) {
+      if (!waited &&
+          (seq_block(my_b0 + j * TB + min(TB, my_nb - j * TB) - 1) + 1) * kBlockKeys > fresh) {
         grid_dependency_wait();
         waited = true;
       }
@@ -464,7 +488,7 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
         // so that one box's keys are consecutive 128-byte rows (one MMA
         // descriptor spans the stage)
         const int b = lane / NBOX, x = lane - b * NBOX;
-        const int blk = my_b0 + j * TB + b;
+        const int blk = seq_block(my_b0 + j * TB + b);
         const int key_in_page = (lg_bpp >= 0 ? blk & (bpp - 1) : blk % bpp) * kBlockKeys;
         int phys = pids[j * TB + b - pid_base];
         if ((unsigned)phys >= (unsigned)p.num_pool_blocks) {
@@ -478,7 +502,7 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
         // one copy per 16-key block of K or V (all D/64 swizzle rows at once;
         // the tensor-memory consumers: V only)
         const int kv = (TP || TC) ? 1 : lane >= nbt, b = (TP || TC) ? lane - nbt * NBOX : lane - kv * nbt;
-        const int blk = my_b0 + j * TB + b;
+        const int blk = seq_block(my_b0 + j * TB + b);
         const int key_in_page = (lg_bpp >= 0 ? blk & (bpp - 1) : blk % bpp) * kBlockKeys;
         int phys = pids[j * TB + b - pid_base];
         if ((unsigned)phys >= (unsigned)p.num_pool_blocks) {
@@ -666,10 +690,20 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
         const int nbt = min(TB, my_nb - j * TB);
         const int key_t0 = (my_b0 + j * TB) * kBlockKeys;
         const int slot = j % NS;
+        // first key of the stage's block b
+        auto block_key = [&](int b) -> int {
+          return SINK ? seq_block(my_b0 + j * TB + b) * kBlockKeys : key_t0 + b * kBlockKeys;
+        };
         // every row of the CTA sees every key of the stage: no mask, and the
         // scale is applied inside the exponent (rows past the requests'
         // tokens have Q = 0, finite scores, and are never stored)
-        const bool fast = nbt == TB && key_t0 >= v_lo && key_t0 + SC <= v_hi;
+        bool fast = nbt == TB;
+        if constexpr (SINK) {
+#pragma unroll
+          for (int b = 0; b < TB; ++b) fast = fast && all_see(block_key(b));
+        } else {
+          fast = fast && key_t0 >= v_lo && key_t0 + SC <= v_hi;
+        }
         const float sl2 = p.scale_log2;
         // the largest scaled score of an unmasked stage: the largest (scale
         // >= 0) or smallest raw score, eight independent chains
@@ -731,9 +765,9 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
             for (int u = 0; u < 8; ++u) a[u] = -INFINITY;
 #pragma unroll
             for (int c = 0; c < SC; ++c) {
-              const int k = key_t0 + c;
+              const int k = block_key(c >> 4) + (c & 15);
               float x = __uint_as_float(sr[c]) * sl2;
-              if (!live || !(c < nbt * kBlockKeys && k >= lo && k < hi)) x = -INFINITY;
+              if (!live || !(c < nbt * kBlockKeys && sees(k, lo, hi))) x = -INFINITY;
               sr[c] = __float_as_uint(x);
               a[c & 7] = fmaxf(a[c & 7], x);
             }
@@ -816,11 +850,11 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
         // zero V of keys no row sees (outside the union, stale or NaN slots);
         // each tile does it before its own PV MMAs (the other tile's writes
         // are the same zeros)
-        if (!(nbt == TB && key_t0 >= u_lo && key_t0 + SC <= u_hi)) {
+        if (SINK ? !fast : !(nbt == TB && key_t0 >= u_lo && key_t0 + SC <= u_hi)) {
           unsigned char *vb = ring + slot * STAGE + TB * BLOCK_BYTES;
           for (int c = 32 * (warp & 3) + lane; c < nbt * kBlockKeys; c += 128) {
-            const int k = key_t0 + c;
-            if (k < u_lo || k >= u_hi) {
+            const int k = block_key(c >> 4) + (c & 15);
+            if (!sees(k, u_lo, u_hi)) {
 #pragma unroll 1
               for (int x = 0; x < NBOX * 8; ++x)
                 *reinterpret_cast<uint4 *>(vb + (c >> 4) * BLOCK_BYTES + (x >> 3) * 2048 +
@@ -1343,12 +1377,14 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
       float mxa = -INFINITY, mxb = -INFINITY;
 #pragma unroll
       for (int kn = 0; kn < KN; ++kn) {
-        const int k0 = key_t0 + kn * 8 + 2 * tq;
+        const int k0 = (SINK ? seq_block(my_b0 + j * TB + (kn >> 1)) * kBlockKeys + (kn & 1) * 8
+                             : key_t0 + kn * 8) +
+                       2 * tq;
         const bool blk = (kn >> 1) < nbt;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int k = k0 + (e & 1);
-          const bool ok = blk && ((e < 2) ? (k >= lo_a && k < hi_a) : (k >= lo_b && k < hi_b));
+          const bool ok = blk && ((e < 2) ? sees(k, lo_a, hi_a) : sees(k, lo_b, hi_b));
           sc[kn][e] = ok ? sc[kn][e] * p.scale_log2 : -INFINITY;
         }
         mxa = fmaxf(mxa, fmaxf(sc[kn][0], sc[kn][1]));
@@ -1396,15 +1432,16 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
           pa[1] = pack2(pv[0][2], pv[0][3], tag{});
           pa[2] = pack2(pv[1][0], pv[1][1], tag{});
           pa[3] = pack2(pv[1][2], pv[1][3], tag{});
-          const int key0 = key_t0 + kb * kBlockKeys;
+          const int key0 = SINK ? seq_block(my_b0 + j * TB + kb) * kBlockKeys
+                                : key_t0 + kb * kBlockKeys;
           const bool vmask = !(key0 >= u_lo && key0 + kBlockKeys <= u_hi);
           uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
           if (vmask) {
             const int ke = key0 + 2 * tq;
-            mlo = ((ke >= u_lo && ke < u_hi) ? 0x0000ffffu : 0u) |
-                  ((ke + 1 >= u_lo && ke + 1 < u_hi) ? 0xffff0000u : 0u);
-            mhi = ((ke + 8 >= u_lo && ke + 8 < u_hi) ? 0x0000ffffu : 0u) |
-                  ((ke + 9 >= u_lo && ke + 9 < u_hi) ? 0xffff0000u : 0u);
+            mlo = (sees(ke, u_lo, u_hi) ? 0x0000ffffu : 0u) |
+                  (sees(ke + 1, u_lo, u_hi) ? 0xffff0000u : 0u);
+            mhi = (sees(ke + 8, u_lo, u_hi) ? 0x0000ffffu : 0u) |
+                  (sees(ke + 9, u_lo, u_hi) ? 0xffff0000u : 0u);
           }
           const int jm = lane >> 3, kk = (jm & 1) * 8 + (lane & 7);  // key of the block
           const uint32_t vb = vbase + kb * BLOCK_BYTES + kk * 128;
@@ -1551,18 +1588,18 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
       float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        const int key0 = key_t0 + b * kBlockKeys;
+        const int key0 = SINK ? seq_block(my_b0 + j * TB + b) * kBlockKeys : key_t0 + b * kBlockKeys;
         if (b >= nbt) {
           sc[b][0] = sc[b][1] = sc[b][2] = sc[b][3] = -INFINITY;
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[b][e] *= p.scale_log2;
-          if (!(key0 >= v_lo && key0 + kBlockKeys <= v_hi)) {
+          if (!all_see(key0)) {
             const int ka = key0 + (lane >> 2), kb = ka + 8;
-            if (!(ka >= lo0 && ka < hi0)) sc[b][0] = -INFINITY;
-            if (!(ka >= lo1 && ka < hi1)) sc[b][1] = -INFINITY;
-            if (!(kb >= lo0 && kb < hi0)) sc[b][2] = -INFINITY;
-            if (!(kb >= lo1 && kb < hi1)) sc[b][3] = -INFINITY;
+            if (!sees(ka, lo0, hi0)) sc[b][0] = -INFINITY;
+            if (!sees(ka, lo1, hi1)) sc[b][1] = -INFINITY;
+            if (!sees(kb, lo0, hi0)) sc[b][2] = -INFINITY;
+            if (!sees(kb, lo1, hi1)) sc[b][3] = -INFINITY;
           }
         }
         mx0 = fmaxf(mx0, fmaxf(sc[b][0], sc[b][2]));
@@ -1601,16 +1638,17 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
           l1 += p1 + p3;
           const uint32_t pb0 = movmatrix_trans(pack2(p0, p1, tag{}));
           const uint32_t pb1 = movmatrix_trans(pack2(p2, p3, tag{}));
-          const int key0 = key_t0 + b * kBlockKeys;
+          const int key0 = SINK ? seq_block(my_b0 + j * TB + b) * kBlockKeys
+                                : key_t0 + b * kBlockKeys;
           const bool vmask = !(key0 >= u_lo && key0 + kBlockKeys <= u_hi);
           uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
           if (vmask) {
             // zero V of keys outside every row's range (stale or NaN slots)
             const int ke = key0 + 2 * (lane & 3);
-            mlo = ((ke >= u_lo && ke < u_hi) ? 0x0000ffffu : 0u) |
-                  ((ke + 1 >= u_lo && ke + 1 < u_hi) ? 0xffff0000u : 0u);
-            mhi = ((ke + 8 >= u_lo && ke + 8 < u_hi) ? 0x0000ffffu : 0u) |
-                  ((ke + 9 >= u_lo && ke + 9 < u_hi) ? 0xffff0000u : 0u);
+            mlo = (sees(ke, u_lo, u_hi) ? 0x0000ffffu : 0u) |
+                  (sees(ke + 1, u_lo, u_hi) ? 0xffff0000u : 0u);
+            mhi = (sees(ke + 8, u_lo, u_hi) ? 0x0000ffffu : 0u) |
+                  (sees(ke + 9, u_lo, u_hi) ? 0xffff0000u : 0u);
           }
           const uint32_t vb = vbase + b * BLOCK_BYTES;
 #pragma unroll
@@ -2534,10 +2572,11 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
   }
 }
 
-template <int D, bool BF16, bool TC, bool DOT = false, bool RM = false, bool TP = false>
+template <int D, bool BF16, bool TC, bool DOT = false, bool RM = false, bool TP = false,
+          bool SINK = false>
 cudaError_t launch_mma_t(const CUtensorMap &tk, const CUtensorMap &tv, const Params &p,
                          const Launch &l, cudaStream_t stream) {
-  auto kern = pd_decode_mma<D, BF16, TC, DOT, RM, TP>;
+  auto kern = pd_decode_mma<D, BF16, TC, DOT, RM, TP, SINK>;
   // largest dynamic shared memory opted into so far, per device
   static int configured_smem[64] = {};
   int dev = 0;

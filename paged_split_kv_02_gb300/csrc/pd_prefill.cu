@@ -40,11 +40,12 @@ struct Tile {
   int32_t nseg;
 };
 
-// The plan shared by paged_prefill_plan and paged_prefill_attn's checks.
+// The tiles of a plan and their segments.
 int plan_tiles(const int32_t *query_start, const int32_t *seq_lens, int S, int Hq, int Hkv,
-               int rows, int window, int target, std::vector<Tile> *tiles,
+               int rows, int window, int sinks, int target, std::vector<Tile> *tiles,
                pd_prefill_plan_info *info) {
-  if (S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || window < 0 || target <= 0 || rows <= 0)
+  if (S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || window < 0 || sinks < 0 || target <= 0 ||
+      rows <= 0)
     return PD_EINVAL;
   if (S > 0 && (!query_start || !seq_lens)) return PD_EINVAL;
   const int G = Hq / Hkv;
@@ -67,7 +68,9 @@ int plan_tiles(const int32_t *query_start, const int32_t *seq_lens, int S, int H
       const int64_t key_end = context + last + 1;
       const int64_t key_begin =
           window ? std::max<int64_t>(0, context + first - window + 1) / kBlockKeys * kBlockKeys : 0;
-      const int64_t blocks = cdiv(key_end - key_begin, kBlockKeys);
+      // (with sinks, their blocks before the window's first one too)
+      const int64_t blocks = cdiv(key_end - key_begin, kBlockKeys) +
+                             std::min(cdiv(sinks, kBlockKeys), key_begin / kBlockKeys);
       tiles->push_back({s, (int32_t)t, blocks, 1});
       total += blocks;
     }
@@ -148,16 +151,11 @@ int prefill_shape(int D, PrefillShape *sh) {
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 }  // namespace
-}  // namespace pd
 
-using namespace pd;
-
-extern "C" {
-
-PD_API int paged_prefill_plan(const int32_t *query_start, const int32_t *seq_lens, int num_seqs,
-                              int num_q_heads, int num_kv_heads, int head_size, int window,
-                              int num_sms, pd_prefill_item *items, int64_t capacity,
-                              pd_prefill_plan_info *info) {
+int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int num_seqs,
+                      int num_q_heads, int num_kv_heads, int head_size, int window, int sinks,
+                      int num_sms, pd_prefill_item *items, int64_t capacity,
+                      pd_prefill_plan_info *info) {
   if (!info) return PD_EINVAL;
   if (!head_size_ok(head_size)) return PD_EHEAD;
   if (num_sms <= 0) {
@@ -166,7 +164,7 @@ PD_API int paged_prefill_plan(const int32_t *query_start, const int32_t *seq_len
   }
   std::vector<Tile> tiles;
   int rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads,
-                      tile_rows_for(head_size), window, num_sms, &tiles, info);
+                      tile_rows_for(head_size), window, sinks, num_sms, &tiles, info);
   if (rc != PD_OK) return rc;
   if (!items) return PD_OK;  // a size query
   if (capacity < info->num_items) return PD_EINVAL;
@@ -192,34 +190,20 @@ PD_API int paged_prefill_plan(const int32_t *query_start, const int32_t *seq_len
   return PD_OK;
 }
 
-PD_API size_t paged_prefill_scratch_bytes(int num_kv_heads, int head_size, int num_sms) {
-  if (num_kv_heads <= 0 || num_sms <= 0) return 0;
-  if (!head_size_ok(head_size)) return 0;
-  const int rows = tile_rows_for(head_size);
-  // counters of paged_decode_scratch_init(.., max_num_seqs = num_sms,
-  // num_kv_heads = 1, ..) and partials of 2 x num_sms slots: a plan splits
-  // fewer than num_sms tiles x kv heads into fewer than 2 x num_sms
-  // segments x kv heads
-  const int64_t counters = round256((int64_t)num_sms * PD_COUNTERS_PER_PAIR * 4);
-  const int64_t slots = 2LL * num_sms;
-  const int64_t acc = round256(slots * rows * head_size * 4);
-  const int64_t ml = round256(slots * rows * 2 * 4);
-  return (size_t)(counters + acc + ml);
-}
-
-PD_API int paged_prefill_attn(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,
-                              const pd_tensor *block_table, const pd_tensor *seq_lens,
-                              const pd_tensor *query_start, const pd_tensor *work,
-                              const pd_prefill_plan_info *info, pd_tensor *out, int num_q_heads,
-                              int num_kv_heads, int head_size, int page_size, int window,
-                              float scale, int layout, pd_scratch *scratch, void *stream) {
+int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,
+                 const pd_tensor *block_table, const pd_tensor *seq_lens,
+                 const pd_tensor *query_start, const pd_tensor *work,
+                 const pd_prefill_plan_info *info, pd_tensor *out, int num_q_heads,
+                 int num_kv_heads, int head_size, int page_size, int window, int sinks,
+                 float scale, int layout, pd_scratch *scratch, void *stream) {
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !query_start || !work ||
       !info || !out)
     return PD_EINVAL;
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return PD_EINVAL;
   if (!head_size_ok(head_size)) return PD_EHEAD;
   const int rows = tile_rows_for(head_size);
-  if (page_size <= 0 || page_size % kBlockKeys != 0 || window < 0 || !std::isfinite(scale))
+  if (page_size <= 0 || page_size % kBlockKeys != 0 || window < 0 || sinks < 0 ||
+      !std::isfinite(scale))
     return PD_EINVAL;
   if (layout != PD_NHD && layout != PD_HND) return PD_EINVAL;
   if (seq_lens->ndim != 1 || !seq_lens->data || seq_lens->stride[0] != 1) return PD_EINVAL;
@@ -308,6 +292,7 @@ PD_API int paged_prefill_attn(const pd_tensor *q, const pd_tensor *k_cache, cons
   p.M = 1 << 30;  // a request's query length is not bounded here
   p.P = page_size;
   p.window = window;
+  p.sinks = window > 0 ? sinks : 0;
   p.layout = layout;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.R = 1 << 30;
@@ -344,6 +329,46 @@ PD_API int paged_prefill_attn(const pd_tensor *q, const pd_tensor *k_cache, cons
     return PD_ECUDA;
   }
   return PD_OK;
+}
+
+}  // namespace pd
+
+using namespace pd;
+
+extern "C" {
+
+PD_API int paged_prefill_plan(const int32_t *query_start, const int32_t *seq_lens, int num_seqs,
+                              int num_q_heads, int num_kv_heads, int head_size, int window,
+                              int num_sms, pd_prefill_item *items, int64_t capacity,
+                              pd_prefill_plan_info *info) {
+  return prefill_plan_call(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                           window, 0, num_sms, items, capacity, info);
+}
+
+PD_API size_t paged_prefill_scratch_bytes(int num_kv_heads, int head_size, int num_sms) {
+  if (num_kv_heads <= 0 || num_sms <= 0) return 0;
+  if (!head_size_ok(head_size)) return 0;
+  const int rows = tile_rows_for(head_size);
+  // counters of paged_decode_scratch_init(.., max_num_seqs = num_sms,
+  // num_kv_heads = 1, ..) and partials of 2 x num_sms slots: a plan splits
+  // fewer than num_sms tiles x kv heads into fewer than 2 x num_sms
+  // segments x kv heads
+  const int64_t counters = round256((int64_t)num_sms * PD_COUNTERS_PER_PAIR * 4);
+  const int64_t slots = 2LL * num_sms;
+  const int64_t acc = round256(slots * rows * head_size * 4);
+  const int64_t ml = round256(slots * rows * 2 * 4);
+  return (size_t)(counters + acc + ml);
+}
+
+PD_API int paged_prefill_attn(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,
+                              const pd_tensor *block_table, const pd_tensor *seq_lens,
+                              const pd_tensor *query_start, const pd_tensor *work,
+                              const pd_prefill_plan_info *info, pd_tensor *out, int num_q_heads,
+                              int num_kv_heads, int head_size, int page_size, int window,
+                              float scale, int layout, pd_scratch *scratch, void *stream) {
+  return prefill_call(q, k_cache, v_cache, block_table, seq_lens, query_start, work, info, out,
+                      num_q_heads, num_kv_heads, head_size, page_size, window, 0, scale, layout,
+                      scratch, stream);
 }
 
 }  // extern "C"

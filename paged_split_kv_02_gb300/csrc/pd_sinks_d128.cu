@@ -1,0 +1,16 @@
+// Window with sinks, head size 128: decode (mma.sync) and tensor-memory prefill tiles.
+#include "pd_kernel.cuh"
+
+namespace pd {
+
+cudaError_t launch_sinks_d128(bool bf16, int path, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const Params &p, const Launch &l, cudaStream_t stream) {
+  if (path == 5)
+    return bf16 ? launch_mma_t<128, true, false, false, false, true, true>(tk, tv, p, l, stream)
+                : launch_mma_t<128, false, false, false, false, true, true>(tk, tv, p, l, stream);
+  if (path != 1) return cudaErrorInvalidValue;
+  return bf16 ? launch_mma_t<128, true, false, false, false, false, true>(tk, tv, p, l, stream)
+              : launch_mma_t<128, false, false, false, false, false, true>(tk, tv, p, l, stream);
+}
+
+}  // namespace pd

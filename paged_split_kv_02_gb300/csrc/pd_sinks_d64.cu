@@ -1,0 +1,16 @@
+// Window with sinks, head size 64: decode (mma.sync) and prefill tiles with the rows on the M side.
+#include "pd_kernel.cuh"
+
+namespace pd {
+
+cudaError_t launch_sinks_d64(bool bf16, int path, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const Params &p, const Launch &l, cudaStream_t stream) {
+  if (path == 4)
+    return bf16 ? launch_mma_t<64, true, false, false, true, false, true>(tk, tv, p, l, stream)
+                : launch_mma_t<64, false, false, false, true, false, true>(tk, tv, p, l, stream);
+  if (path != 1) return cudaErrorInvalidValue;
+  return bf16 ? launch_mma_t<64, true, false, false, false, false, true>(tk, tv, p, l, stream)
+              : launch_mma_t<64, false, false, false, false, false, true>(tk, tv, p, l, stream);
+}
+
+}  // namespace pd

@@ -1,0 +1,171 @@
+"""Attention over a window with sinks on the CPU: exported symbols, refusals
+(checked on the host before any launch), the launch plans, and the oracle's
+pins."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_split_kv_02_gb300 as pd
+from oracle import sinks as O
+from paged_split_kv_02_gb300 import workloads as W
+from step_cases import hide
+
+PASSES = -8  # a call that passes every check reaches the missing device
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if torch.cuda.is_available():
+        pytest.skip("host tensors: for machines without a GPU")
+    pd.build()
+    oracle.build()
+
+
+def test_exports_every_declared_symbol():
+    names = pd.declared_symbols(pd.STEP_HEADER)
+    assert {"paged_decode_attn_sinks", "paged_decode_plan_sinks", "paged_prefill_plan_sinks",
+            "paged_prefill_attn_sinks"} <= set(names)
+    for n in names:
+        assert hasattr(pd.lib(), n), n
+
+
+def test_packed_descriptors_are_the_structures():
+    for t in (torch.zeros(3), torch.zeros(4, 5)[:, 1:3],
+              torch.zeros(2, 3, 4, 6, dtype=torch.int32)[..., ::2],
+              torch.zeros(2, 1, 4, dtype=torch.bfloat16).transpose(0, 2), torch.zeros(1, 1, 1, 1, 2),
+              torch.zeros(())):
+        assert pd._packed(t) == bytes(pd.tensor_desc(t))
+    assert pd._packed(None) is None
+
+
+def _attn(**kw):
+    c = W.make_case("refuse", seed=1, dtype=torch.bfloat16, head_size=128, num_q_heads=8,
+                    num_kv_heads=2, page_size=16, max_query_len=2, seq_lens=[100, 40], window=32)
+    a = dict(q=c.q, k=c.k_cache, v=c.v_cache, bt=c.block_table, sl=c.seq_lens,
+             out=torch.empty_like(c.q), Hq=8, Hkv=2, D=128, P=16, M=2, window=32, sinks=4, scale=0.1,
+             layout=W.HND, qs=None, opts=None)
+    a.update(kw)
+    return pd.paged_decode_attn_sinks(a["q"], a["k"], a["v"], a["bt"], a["sl"], a["out"], a["Hq"],
+                                      a["Hkv"], a["D"], a["P"], a["M"], a["window"], a["sinks"],
+                                      a["scale"], a["layout"], None, query_start=a["qs"],
+                                      opts=a["opts"], check=False)
+
+
+def test_decode_sinks_refusals():
+    q = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
+    assert _attn() == PASSES
+    assert _attn(qs=torch.tensor([0, 2, 3], dtype=torch.int32)) == PASSES
+    for kw, rc in [(dict(sinks=-1), -1), (dict(window=-1), -1), (dict(sinks=-1, window=0), -1),
+                   (dict(scale=float("nan")), -1), (dict(D=96), -3), (dict(M=9), -4), (dict(M=0), -4),
+                   (dict(P=24), -1), (dict(Hq=7), -1), (dict(layout=2), -1), (dict(q=q[:3]), -1),
+                   (dict(q=q.float()), -2), (dict(q=q.half()), -2), (dict(bt=torch.zeros(2, 7)), -2),
+                   (dict(bt=torch.zeros(3, 7, dtype=torch.int32)), -1),
+                   (dict(qs=torch.zeros(2, dtype=torch.int32)), -1), (dict(qs=torch.zeros(3)), -2)]:
+        assert _attn(**kw) == rc, kw
+    with pytest.raises(pd.PagedDecodeError):
+        pd.paged_decode_attn_sinks(q, q, q, q, q, q, 8, 2, 128, 16, 2, 32, 4, 0.1, W.HND)
+
+
+def test_plan_sinks():
+    def plan(window, sinks, width=2048, S=1, **kw):
+        sd = pd.PdScratch()
+        sd.data, sd.bytes = 1 << 30, pd.paged_decode_scratch_bytes(S, 32, 8, 128, 4, 256)
+        sd.counter_slots = S * 8 * pd.COUNTERS_PER_PAIR
+        return pd.paged_decode_plan_sinks(S, 32, 8, 128, 16, 4, window, sinks, width, 152,
+                                          scratch_desc=sd, opts=pd.options(**kw) if kw else None)
+    for S in (1, 7, 64):
+        for window in (1, 100, 4096, 2 ** 31 - 1):
+            for sinks in (0, 1, 16, 500, 2 ** 31 - 1):
+                p = plan(window, sinks, S=S)
+                # the segments cover the blocks of the window, a partial one
+                # at its start, and the sinks, or the whole table
+                need = min(2048, -(-(window + 3) // 16) + 1 + -(-sinks // 16))
+                assert p["seg_blocks"] * p["max_segments"] >= need
+                assert p["path"] == 1 and p["smem_bytes"] <= 232448
+    assert (pd.paged_decode_plan_sinks(1, 32, 8, 128, 16, 4, 512, 0, 2048, 152)
+            == pd.paged_decode_plan(1, 32, 8, 128, 16, 4, 512, 2048, 152))
+    # without a window every key is visible, whatever the sinks
+    assert plan(0, 9) == plan(0, 0)
+    assert plan(0, 9, path=3)["path"] == 3
+    for bad in (dict(window=64, sinks=-1), dict(window=-1, sinks=1), dict(window=64, sinks=1, path=2),
+                dict(window=64, sinks=1, path=3)):
+        with pytest.raises(pd.PagedDecodeError):
+            plan(**bad)
+
+
+def test_prefill_plan_sinks():
+    def plan(q_lens, lens, window, sinks, D=128, sms=152):
+        qs = [0] + list(np.cumsum(q_lens))
+        return pd.paged_prefill_plan_sinks(qs, lens, 8, 2, D, window, sinks, sms)
+    for D, rows in ((64, 64), (128, 256), (512, 64)):
+        for window, sinks in ((100, 4), (64, 300), (1, 1), (0, 50)):
+            q_lens, lens = [300, 1, 0, 90], [1300, 1, 40, 3000]
+            items, info = plan(q_lens, lens, window, sinks, D)
+            blocks = {(int(i[0]), int(i[1])): int(i[6]) for i in items}
+            for s, (m, L) in enumerate(zip(q_lens, lens)):
+                for t in range(-(-m * 4 // rows)):
+                    first, last = t * rows // 4, min(m - 1, ((t + 1) * rows - 1) // 4)
+                    seen = set()
+                    for i in range(first, last + 1):
+                        seen |= {k // 16 for k in O.visible(L - m + i + 1, window, sinks)}
+                    # (the sinks' last block and the window's first may be one)
+                    assert len(seen) <= blocks[s, t] <= len(seen) + 1, (s, t)
+            assert info.num_items == len(items)
+    a, b = plan([300], [900], 128, 0), pd.paged_prefill_plan([0, 300], [900], 8, 2, 128, 128, 152)
+    assert torch.equal(a[0], b[0])
+    for bad in ((-1, 4), (4, -1)):
+        with pytest.raises(pd.PagedDecodeError):
+            plan([3], [3], *bad)
+    with pytest.raises(pd.PagedDecodeError):
+        pd.paged_prefill_plan_sinks([0, 3, 1], [3, 3], 8, 2, 128, 16, 4, 152)
+
+
+def test_prefill_sinks_refusals():
+    c = W.make_prefill_case("refuse", seed=1, q_lens=[20, 3], contexts=[10, 0], num_q_heads=8,
+                            num_kv_heads=2, window=16)
+    items, info = pd.paged_prefill_plan_sinks(c.query_start_host, c.seq_lens_host, 8, 2, 128, 16, 4,
+                                              1000)
+
+    def call(window=16, sinks=4, scale=0.1, work=items, out=None, D=128, qs=c.query_start):
+        return pd.paged_prefill_attn_sinks(c.q, c.k_cache, c.v_cache, c.block_table, c.seq_lens, qs,
+                                           work, info, torch.empty_like(c.q) if out is None else out,
+                                           8, 2, D, 16, window, sinks, scale, W.HND, None, check=False)
+    assert call() == PASSES
+    for kw, rc in [(dict(sinks=-1), -1), (dict(window=-2), -1), (dict(scale=float("inf")), -1),
+                   (dict(work=items[:0]), -1), (dict(work=items.long()), -2), (dict(out=c.q.float()), -2),
+                   (dict(D=256), -1), (dict(D=100), -3), (dict(qs=c.query_start[:-1]), -1)]:
+        assert call(**kw) == rc, kw
+
+
+# ---- pins of the oracle -----------------------------------------------------
+
+def _pin(**kw):
+    return W.make_case("pin", **{**dict(seed=3, dtype=torch.float16, head_size=64, num_q_heads=4,
+                                        num_kv_heads=2, page_size=16, max_query_len=3,
+                                        seq_lens=[90, 0, 2], window=20), **kw})
+
+
+def test_oracle_against_the_window_and_full_oracles():
+    c, full = _pin(), _pin(window=0)
+    assert np.allclose(O.attention(c, 0), oracle.attention(c), rtol=1e-12, atol=1e-12)
+    # sinks up to the window's start, or past the sequence: every key
+    for sinks in (70, 90, 1000):
+        assert np.allclose(O.attention(c, sinks), oracle.attention(full), rtol=1e-12, atol=1e-12)
+
+
+def test_oracle_as_a_merge_of_two_ranges():
+    c = _pin(num_kv_heads=1, max_query_len=1, seq_lens=[200], window=0)
+    want = oracle.merge([oracle.partial(c, 0, 7), oracle.partial(c, 150, 200)])
+    got = O.attention(W.DecodeCase(**{**c.__dict__, "window": 50}), 7)
+    assert np.allclose(got, want, rtol=1e-12, atol=1e-12)
+
+
+def test_hidden_cases_hold_nan_only_where_no_row_looks():
+    c = _pin(max_query_len=2, seq_lens=[300], window=40)
+    before = O.attention(c, 5)
+    after = hide(c, 5)
+    assert np.array_equal(O.attention(after, 5), before)
+    assert after.block_table[0].eq(-1).nonzero()[:, 0].tolist() == list(range(1, 16))
+    assert np.isnan(O.attention(after, 6)).any()
