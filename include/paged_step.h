@@ -1,7 +1,8 @@
 /*
  * paged_step.h — the calls around and beside paged_decode.h that a serving
  * step makes: attention over a sliding window whose first tokens stay
- * visible (sinks).
+ * visible (sinks), and the tables of a batch built on the GPU from its
+ * requests' lengths.
  *
  * Types, layouts, scratch, streams, graph capture and errors are those of
  * paged_decode.h: every call is asynchronous on `stream`, allocates nothing,
@@ -71,6 +72,57 @@ PD_API int paged_prefill_attn_sinks(const pd_tensor *q, const pd_tensor *k_cache
                                     pd_tensor *out, int num_q_heads, int num_kv_heads,
                                     int head_size, int page_size, int window, int sinks,
                                     float scale, int layout, pd_scratch *scratch, void *stream);
+
+/* ---- The tables of a batch ----
+ *
+ * For requests s = 0 .. S-1 with c_s = context_lens[s] cached tokens and q_s
+ * = query_lens[s] new ones (0: no token in this step), in one launch:
+ *     query_start[s]  = q_0 + .. + q_{s-1}             (query_start[S]: all)
+ *     seq_lens[s]     = c_s + q_s
+ *   new pages, when free_pages is given: request s takes
+ *     need_s = ceil((c_s + q_s) / P) - ceil(c_s / P)
+ *   pages of the list in request order, from f_s = cursor + need_0 + .. +
+ *   need_{s-1} on:
+ *     block_table[s][ceil(c_s / P) + j] = free_pages[f_s + j],  j < need_s
+ *     next_cursor     = cursor + need_0 + .. + need_{S-1}
+ *   token t = query_start[s] + i, at p = c_s + i of its sequence:
+ *     positions[a][t] = p + position_delta[s]          (every axis a)
+ *     slot_mapping[t] = block_table[s][p / P] * P + p % P
+ *   and rows past the last request (padding): position 0, slot -1.
+ * The other entries of block_table are left as they were.  With the same
+ * inputs a call writes the same values again, so it may be repeated or
+ * replayed; to go on, pass next_cursor's value as the next call's cursor.
+ *   context_lens, query_lens  [S] int32
+ *   block_table   [S, W] int32: the pages each request has (in), with the new
+ *                 ones (out)
+ *   query_start   [S + 1] int32 (out)      seq_lens  [S] int32 (out)
+ *   positions     [A, T] or [T] int32 (out), rows contiguous, A <= PD_MAX_AXES;
+ *                 T: rows of the step, padding included
+ *   slot_mapping  [T] int32 (out)
+ *   free_pages    [F] int32, or NULL (then the table already holds every page;
+ *                 cursor and next_cursor may be NULL)
+ *   cursor        [1] int32: entries of free_pages already taken
+ *   next_cursor   [1] int32 (out); not cursor itself
+ *   position_delta  [S] int32 or NULL: what a request's positions are ahead of
+ *                 its token count (image tokens share positions: negative)
+ *   page_size     any (the attention calls take multiples of 16)
+ *   num_pages     pages of the pool; num_pages * page_size <= 2^31 - 1
+ * No output may overlap an input (but block_table, which is both).
+ * Reported: a negative length, or one past the block table (clamped; tokens
+ * past the table get slot -1): PD_DEV_BAD_SEQLEN.  More tokens than T (the
+ * requests are cut off there): PD_DEV_BAD_QSTART.  A page id outside the
+ * pool (slot -1; a new entry is written as -1): PD_DEV_BAD_PAGE.  A list
+ * that is used up (entries and slots -1; next_cursor still counts every
+ * page asked for): PD_DEV_NO_PAGE. */
+#define PD_DEV_NO_PAGE 0x100u /* paged_batch_tables: free_pages is used up */
+#define PD_MAX_AXES 8
+
+PD_API int paged_batch_tables(const pd_tensor *context_lens, const pd_tensor *query_lens,
+                              const pd_tensor *free_pages, const pd_tensor *cursor,
+                              const pd_tensor *position_delta, pd_tensor *block_table,
+                              pd_tensor *query_start, pd_tensor *seq_lens, pd_tensor *positions,
+                              pd_tensor *slot_mapping, pd_tensor *next_cursor, int page_size,
+                              int num_pages, void *stream);
 
 #ifdef __cplusplus
 }

@@ -23,6 +23,8 @@ and of ``include/paged_step.h``, the calls around them in a serving step:
 * ``paged_decode_attn_sinks(...)``, ``paged_prefill_plan_sinks(...)`` /
   ``paged_prefill_attn_sinks(...)``: a sliding window whose first tokens
   stay visible
+* ``paged_batch_tables(...)``: block tables, query starts, lengths,
+  positions and cache slots of a batch, built on the GPU from its lengths
 """
 
 from __future__ import annotations
@@ -49,6 +51,8 @@ STATUS_NAMES = {
 }
 DEV_WAIT_TIMEOUT, DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_BAD_QSTART = 0x1, 0x2, 0x4, 0x8
 DEV_BAD_SCRATCH, DEV_BAD_POSITION, DEV_BAD_SLOT, DEV_BAD_WORK = 0x10, 0x20, 0x40, 0x80
+DEV_NO_PAGE = 0x100
+MAX_AXES = 8  # PD_MAX_AXES
 COUNTERS_PER_PAIR = 16  # PD_COUNTERS_PER_PAIR
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
@@ -179,6 +183,8 @@ def lib():
         L.paged_prefill_attn_sinks.argtypes = [vp] * 7 + [ctypes.POINTER(PdPrefillPlanInfo), vp] + \
             [i32] * 6 + [f32, i32, ctypes.POINTER(PdScratch), vp]
         L.paged_prefill_attn_sinks.restype = i32
+        L.paged_batch_tables.argtypes = [vp] * 11 + [i32, i32, vp]
+        L.paged_batch_tables.restype = i32
         _lib = L
     return _lib
 
@@ -434,6 +440,22 @@ def paged_decode_plan_sinks(num_seqs, num_q_heads, num_kv_heads, head_size, page
     if rc != PD_OK:
         raise PagedDecodeError(rc, "paged_decode_plan_sinks")
     return plan.as_dict()
+
+
+def paged_batch_tables(context_lens, query_lens, block_table, query_start, seq_lens, positions,
+                       slot_mapping, page_size, num_pages, free_pages=None, cursor=None,
+                       next_cursor=None, position_delta=None, stream=None,
+                       check: bool = True) -> int:
+    """Fill the tables of a step on the GPU from its requests' cached
+    (``context_lens``) and new (``query_lens``) tokens: ``query_start``,
+    ``seq_lens``, ``positions`` ([T] or [axes, T]), ``slot_mapping``, and,
+    with ``free_pages``, the new pages' entries of ``block_table`` and
+    ``next_cursor`` (see paged_step.h)."""
+    return _step_call(
+        "paged_batch_tables",
+        (context_lens, query_lens, free_pages, cursor, position_delta, block_table, query_start,
+         seq_lens, positions, slot_mapping, next_cursor),
+        lambda t, st: (*t, int(page_size), int(num_pages), st), stream, check)
 
 
 def paged_rope_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache,

@@ -67,3 +67,21 @@ def run_prefill_sinks(case, sinks, scratch=None, num_sms=0, plan=None, out=None)
                                 case.page_size, case.window, sinks, case.scale, case.layout,
                                 scratch)
     return out
+
+
+def batch(S, P, seed, q_hi=4, c_hi=900, empty=0.1, slack=3):
+    """(contexts, query lengths, table, free list, pages in the pool) of a
+    step: every request's pages so far in its row, the other entries -1."""
+    g = np.random.default_rng(seed)
+    c = g.integers(0, c_hi + 1, S)
+    q = np.where(g.random(S) < empty, 0, g.integers(1, q_hi + 1, S))
+    if S:
+        c[0] = 0
+        c[-1] = (c[-1] // P) * P  # new pages from the first token on
+    have, need = -(-c // P), -(-(c + q) // P)
+    width = int(need.max()) + 1 if S else 1
+    pages = int(need.sum()) + slack
+    ids = g.permutation(pages)
+    table = np.full((S, width), -1)
+    table[np.arange(width)[None] < have[:, None]] = ids[:int(have.sum())]
+    return c, q, table, ids[int(have.sum()):], pages
