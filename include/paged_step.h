@@ -1,8 +1,13 @@
 /*
  * paged_step.h — the calls around and beside paged_decode.h that a serving
  * step makes: attention over a sliding window whose first tokens stay
- * visible (sinks), and the tables of a batch built on the GPU from its
- * requests' lengths.
+ * visible (sinks), the tables of a batch built on the GPU from its requests'
+ * lengths, and the rotary embedding with a position per axis.  On one stream
+ * and without a host round trip:
+ *     paged_batch_tables            block tables, starts, lengths, positions, slots
+ *     (the model's projections)
+ *     paged_rope_axes_cache_write   q, k rotated; k, v stored at the slots
+ *     paged_decode_attn_sinks       or paged_prefill_attn_sinks
  *
  * Types, layouts, scratch, streams, graph capture and errors are those of
  * paged_decode.h: every call is asynchronous on `stream`, allocates nothing,
@@ -123,6 +128,27 @@ PD_API int paged_batch_tables(const pd_tensor *context_lens, const pd_tensor *qu
                               pd_tensor *query_start, pd_tensor *seq_lens, pd_tensor *positions,
                               pd_tensor *slot_mapping, pd_tensor *next_cursor, int page_size,
                               int num_pages, void *stream);
+
+/* ---- Rotary embedding with a position per axis ----
+ *
+ * paged_rope_cache_write for tokens that have A positions each (time, height
+ * and width of an image or video token; text has the same one on every
+ * axis): rotated pair i of every head takes the angle of the axis
+ * pair_axis[i],
+ *     (c, s) = cos_sin_cache[positions[pair_axis[i]][t]] [i], [rot_dim / 2 + i].
+ * Everything else is as there.
+ *   positions  [A, T] int32 device array, rows contiguous (any distance apart,
+ *              0 too: one row for every axis), 1 <= A <= PD_MAX_AXES
+ *   pair_axis  [rot_dim / 2] host array (read during the call), entries < A
+ * A position outside the table on any axis is clamped into it and reported
+ * (PD_DEV_BAD_POSITION). */
+PD_API int paged_rope_axes_cache_write(const pd_tensor *q, const pd_tensor *k, const pd_tensor *v,
+                                       const pd_tensor *positions, const pd_tensor *slot_mapping,
+                                       const pd_tensor *cos_sin_cache, const uint8_t *pair_axis,
+                                       pd_tensor *q_out, pd_tensor *k_cache, pd_tensor *v_cache,
+                                       int num_q_heads, int num_kv_heads, int head_size,
+                                       int rot_dim, int page_size, int layout, int is_neox,
+                                       void *stream);
 
 #ifdef __cplusplus
 }

@@ -25,6 +25,8 @@ and of ``include/paged_step.h``, the calls around them in a serving step:
   stay visible
 * ``paged_batch_tables(...)``: block tables, query starts, lengths,
   positions and cache slots of a batch, built on the GPU from its lengths
+* ``paged_rope_axes_cache_write(...)``: the rotary embedding with a position
+  per axis (time, height, width); ``rope_pair_axis`` lays the axes out
 """
 
 from __future__ import annotations
@@ -185,6 +187,8 @@ def lib():
         L.paged_prefill_attn_sinks.restype = i32
         L.paged_batch_tables.argtypes = [vp] * 11 + [i32, i32, vp]
         L.paged_batch_tables.restype = i32
+        L.paged_rope_axes_cache_write.argtypes = [vp] * 10 + [i32] * 7 + [vp]
+        L.paged_rope_axes_cache_write.restype = i32
         _lib = L
     return _lib
 
@@ -472,6 +476,42 @@ def paged_rope_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache, q_ou
     if check and rc != PD_OK:
         raise PagedDecodeError(rc, "paged_rope_cache_write")
     return rc
+
+
+def rope_pair_axis(sections, interleaved: bool = False) -> bytes:
+    """The axis of every rotated pair, for ``paged_rope_axes_cache_write``:
+    ``sections[a]`` pairs take axis a, as runs one after the other, or
+    ``interleaved``: pair i takes axis i % axes as long as that axis has pairs
+    left (i < axes * sections[i % axes]), else axis 0."""
+    sizes = [int(n) for n in sections]
+    if not 1 <= len(sizes) <= MAX_AXES or min(sizes) < 0:
+        raise ValueError(f"1..{MAX_AXES} sections of >= 0 pairs, got {sizes}")
+    if not interleaved:
+        return bytes(a for a, n in enumerate(sizes) for _ in range(n))
+    axes = len(sizes)
+    out = bytes(i % axes if i < axes * sizes[i % axes] else 0 for i in range(sum(sizes)))
+    if [out.count(a) for a in range(axes)] != sizes:
+        raise ValueError(f"sections {sizes} cannot be interleaved: an axis but the first has "
+                         "more pairs than turns")
+    return out
+
+
+def paged_rope_axes_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache, pair_axis, q_out,
+                                k_cache, v_cache, num_q_heads, num_kv_heads, head_size, rot_dim,
+                                page_size, layout, is_neox=True, stream=None,
+                                check: bool = True) -> int:
+    """``paged_rope_cache_write`` with ``positions`` [axes, T]: rotated pair i
+    takes its angle at the position of axis ``pair_axis[i]`` (``rot_dim / 2``
+    small integers, as ``rope_pair_axis`` gives them)."""
+    pairs = bytes(pair_axis)
+    if len(pairs) != int(rot_dim) // 2:
+        raise ValueError(f"pair_axis has {len(pairs)} entries, rot_dim / 2 is {int(rot_dim) // 2}")
+    return _step_call(
+        "paged_rope_axes_cache_write",
+        (q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache),
+        lambda t, st: (*t[:6], pairs, *t[6:], int(num_q_heads), int(num_kv_heads), int(head_size),
+                       int(rot_dim), int(page_size), int(layout), int(bool(is_neox)), st),
+        stream, check)
 
 
 def rope_case(case, q_out=None, stream=None):

@@ -10,58 +10,10 @@
 // pass-through chunks past rot_dim, then every v chunk.  Rotated values
 // are computed in fp32 from the fp16/bf16 inputs and the fp32 table and
 // rounded once.  Memory-bound: every byte is read or written once.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "paged_decode.h"
-#include "pd_internal.h"
-#include "pd_ptx.cuh"
+#include "pd_rope.cuh"
 
 namespace pd {
 namespace {
-
-template <bool BF16>
-struct Elem;
-template <>
-struct Elem<true> {
-  using T2 = __nv_bfloat162;
-  static __device__ __forceinline__ float2 to2(uint32_t w) {
-    return __bfloat1622float2(*reinterpret_cast<const T2 *>(&w));
-  }
-  static __device__ __forceinline__ uint32_t from2(float a, float b) {
-    T2 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&v);
-  }
-};
-template <>
-struct Elem<false> {
-  using T2 = __half2;
-  static __device__ __forceinline__ float2 to2(uint32_t w) {
-    return __half22float2(*reinterpret_cast<const T2 *>(&w));
-  }
-  static __device__ __forceinline__ uint32_t from2(float a, float b) {
-    T2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&v);
-  }
-};
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
-  using E = Elem<BF16>;
-  const float2 a = E::to2(w.x), b = E::to2(w.y), c = E::to2(w.z), d = E::to2(w.w);
-  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-  x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
-  uint4 w;
-  w.x = Elem<BF16>::from2(y[0], y[1]);
-  w.y = Elem<BF16>::from2(y[2], y[3]);
-  w.z = Elem<BF16>::from2(y[4], y[5]);
-  w.w = Elem<BF16>::from2(y[6], y[7]);
-  return w;
-}
 
 template <bool BF16, bool NEOX, int kU>
 __global__ void __launch_bounds__(128) pd_rope_cache(const __grid_constant__ RopeParams p) {
@@ -197,33 +149,6 @@ __global__ void __launch_bounds__(128) pd_rope_cache(const __grid_constant__ Rop
   }
 }
 
-bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-// [T, H, D] fp16/bf16 token rows: 16-byte aligned rows, innermost stride 1
-int check_token_rows(const pd_tensor *t, int64_t T, int H, int D) {
-  if (!t || t->ndim != 3 || (!t->data && T != 0)) return PD_EINVAL;  // (empty: any pointer)
-  if (t->shape[0] != T || t->shape[1] != H || t->shape[2] != D) return PD_EINVAL;
-  if (t->dtype != PD_F16 && t->dtype != PD_BF16) return PD_EDTYPE;
-  if (t->stride[2] != 1) return PD_EALIGN;
-  if (t->stride[0] < 0 || t->stride[1] < 0) return PD_EINVAL;
-  if (t->stride[0] % 8 != 0 || t->stride[1] % 8 != 0 || !aligned16(t->data)) return PD_EALIGN;
-  return PD_OK;
-}
-
-int check_i32_vector(const pd_tensor *t, int64_t n) {
-  if (!t || (!t->data && n != 0) || t->ndim != 1 || t->shape[0] != n || t->stride[0] != 1)
-    return PD_EINVAL;
-  if (t->dtype != PD_I32) return PD_EDTYPE;
-  return PD_OK;
-}
-
-// (page, token, kv head) element strides of a pool in its layout
-void pool_strides(const pd_tensor *t, int layout, int64_t *page, int64_t *tok, int64_t *head) {
-  *page = t->stride[0];
-  *tok = layout == PD_NHD ? t->stride[1] : t->stride[2];
-  *head = layout == PD_NHD ? t->stride[2] : t->stride[1];
-}
-
 }  // namespace
 }  // namespace pd
 
@@ -234,76 +159,18 @@ extern "C" PD_API int paged_rope_cache_write(
     const pd_tensor *slot_mapping, const pd_tensor *cos_sin_cache, pd_tensor *q_out,
     pd_tensor *k_cache, pd_tensor *v_cache, int num_q_heads, int num_kv_heads, int head_size,
     int rot_dim, int page_size, int layout, int is_neox, void *stream) {
-  if (!q || !k || !v || !positions || !slot_mapping || !cos_sin_cache || !q_out || !k_cache ||
-      !v_cache)
-    return PD_EINVAL;
-  if (num_q_heads <= 0 || num_kv_heads <= 0) return PD_EINVAL;
-  if (head_size != 64 && head_size != 128 && head_size != 256 && head_size != 512) return PD_EHEAD;
-  if (page_size <= 0 || (layout != PD_NHD && layout != PD_HND)) return PD_EINVAL;
-  if (rot_dim <= 0 || rot_dim > head_size || rot_dim % (is_neox ? 16 : 8) != 0) return PD_EINVAL;
-  if (q->ndim != 3 || q->shape[0] < 0 || q->shape[0] > INT32_MAX) return PD_EINVAL;
-  const int64_t T = q->shape[0];
-  int rc;
-  if ((rc = check_token_rows(q, T, num_q_heads, head_size)) != PD_OK) return rc;
-  if ((rc = check_token_rows(q_out, T, num_q_heads, head_size)) != PD_OK) return rc;
-  if ((rc = check_token_rows(k, T, num_kv_heads, head_size)) != PD_OK) return rc;
-  if ((rc = check_token_rows(v, T, num_kv_heads, head_size)) != PD_OK) return rc;
-  if ((rc = check_i32_vector(positions, T)) != PD_OK) return rc;
-  if ((rc = check_i32_vector(slot_mapping, T)) != PD_OK) return rc;
-  if ((rc = check_cache_tensor(k_cache, layout, num_kv_heads, page_size, head_size)) != PD_OK)
-    return rc;
-  if ((rc = check_cache_tensor(v_cache, layout, num_kv_heads, page_size, head_size)) != PD_OK)
-    return rc;
-  for (int i = 0; i < 4; ++i)
-    if (k_cache->shape[i] != v_cache->shape[i]) return PD_EINVAL;
-  const int dt = q->dtype;
-  if (q_out->dtype != dt || k->dtype != dt || v->dtype != dt || k_cache->dtype != dt ||
-      v_cache->dtype != dt)
-    return PD_EDTYPE;
-  const pd_tensor *cs = cos_sin_cache;
-  if (!cs->data || cs->ndim != 2 || cs->shape[0] < 1 || cs->shape[0] > INT32_MAX ||
-      cs->shape[1] < rot_dim || cs->stride[1] != 1 || cs->stride[0] < rot_dim)
-    return PD_EINVAL;
-  if (cs->dtype != PD_F32) return PD_EDTYPE;
-  if (cs->stride[0] % 4 != 0 || !aligned16(cs->data)) return PD_EALIGN;
-  if (T == 0) return PD_OK;
-
-  unsigned int *status = nullptr;
-  if ((rc = device_check(nullptr, &status)) != PD_OK) return rc;
-
   RopeParams p{};
-  p.q = q->data;
-  p.q_s0 = q->stride[0];
-  p.q_s1 = q->stride[1];
-  p.k = k->data;
-  p.k_s0 = k->stride[0];
-  p.k_s1 = k->stride[1];
-  p.v = v->data;
-  p.v_s0 = v->stride[0];
-  p.v_s1 = v->stride[1];
-  p.q_out = q_out->data;
-  p.qo_s0 = q_out->stride[0];
-  p.qo_s1 = q_out->stride[1];
-  p.k_cache = k_cache->data;
-  p.v_cache = v_cache->data;
-  pool_strides(k_cache, layout, &p.kc_page, &p.kc_tok, &p.kc_head);
-  pool_strides(v_cache, layout, &p.vc_page, &p.vc_tok, &p.vc_head);
-  p.positions = static_cast<const int32_t *>(positions->data);
-  p.slots = static_cast<const int32_t *>(slot_mapping->data);
-  p.cos_sin = static_cast<const float *>(cs->data);
-  p.cs_s0 = cs->stride[0];
-  p.max_pos = (int)cs->shape[0];
-  p.T = (int)T;
-  p.Hq = num_q_heads;
-  p.Hkv = num_kv_heads;
-  p.D = head_size;
-  p.rot = rot_dim;
-  p.P = page_size;
-  p.num_slots = k_cache->shape[0] * (int64_t)page_size;
-  p.status = status;
+  int rc = rope_params(q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache,
+                       num_q_heads, num_kv_heads, head_size, rot_dim, page_size, layout, is_neox,
+                       &p);
+  if (rc != PD_OK) return rc;
+  if (p.T == 0) return PD_OK;
+
+  int num_sms = 0;
+  if ((rc = device_check(&num_sms, &p.status)) != PD_OK) return rc;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)T);
+  cfg.gridDim = dim3((unsigned)p.T);
   cfg.blockDim = dim3(128);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -311,11 +178,9 @@ extern "C" PD_API int paged_rope_cache_write(
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const bool bf16 = dt == PD_BF16;
-  int num_sms = 0;
-  if ((rc = device_check(&num_sms, nullptr)) != PD_OK) return rc;
+  const bool bf16 = q->dtype == PD_BF16;
   // (4 warps per token; a GB300 SM holds 64)
-  const bool few = T * 4 < (int64_t)num_sms * 32;
+  const bool few = (int64_t)p.T * 4 < (int64_t)num_sms * 32;
   cudaError_t e;
   if (few) {
     if (bf16)
