@@ -81,7 +81,7 @@ def test_tables_of_a_wider_table_and_without_cursors():
     c, q, table, free, pages = batch(6, 16, seed=3, q_hi=30)
     T = int(q.sum())
     full = O.batch_tables(c, q, table, 16, T, 1, free, 0)[0]
-    wide = torch.full((6, 50), 77, dtype=torch.int32, device="cuda")
+    wide = torch.full((6, full.shape[1] + 9), 77, dtype=torch.int32, device="cuda")
     view = wide[:, 4:4 + full.shape[1]]
     view.copy_(_i32(full))
     before = wide.clone()
