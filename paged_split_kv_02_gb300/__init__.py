@@ -31,11 +31,11 @@ and of ``include/paged_step.h``, the calls around them in a serving step:
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
-import struct
 from typing import Optional
 
 import torch
@@ -171,10 +171,6 @@ def lib():
         L.paged_prefill_attn.argtypes = [T] * 7 + [ctypes.POINTER(PdPrefillPlanInfo), T] + \
             [i32] * 5 + [f32, i32, ctypes.POINTER(PdScratch), vp]
         L.paged_prefill_attn.restype = i32
-        # (paged_step.h: packed descriptors, passed as bytes)
-        L.paged_decode_attn_sinks.argtypes = [vp] * 7 + [i32] * 7 + [
-            f32, i32, ctypes.POINTER(PdScratch), vp, ctypes.POINTER(PdOptions)]
-        L.paged_decode_attn_sinks.restype = i32
         L.paged_decode_plan_sinks.argtypes = [i32] * 10 + [ctypes.POINTER(PdScratch),
                                                            ctypes.POINTER(PdOptions),
                                                            ctypes.POINTER(PdPlan)]
@@ -182,13 +178,6 @@ def lib():
         L.paged_prefill_plan_sinks.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, i64,
                                                ctypes.POINTER(PdPrefillPlanInfo)]
         L.paged_prefill_plan_sinks.restype = i32
-        L.paged_prefill_attn_sinks.argtypes = [vp] * 7 + [ctypes.POINTER(PdPrefillPlanInfo), vp] + \
-            [i32] * 6 + [f32, i32, ctypes.POINTER(PdScratch), vp]
-        L.paged_prefill_attn_sinks.restype = i32
-        L.paged_batch_tables.argtypes = [vp] * 11 + [i32, i32, vp]
-        L.paged_batch_tables.restype = i32
-        L.paged_rope_axes_cache_write.argtypes = [vp] * 10 + [i32] * 7 + [vp]
-        L.paged_rope_axes_cache_write.restype = i32
         _lib = L
     return _lib
 
@@ -222,54 +211,36 @@ def tensor_desc(t: torch.Tensor) -> PdTensor:
     return d
 
 
-_DESC = [struct.Struct("Pii%dq%dx%dq%dx" % (n, 8 * (4 - n), n, 8 * (4 - n))) for n in range(5)]
-assert _DESC[4].size == ctypes.sizeof(PdTensor)
+_bind = None
 
 
-def _packed(t: Optional[torch.Tensor]) -> Optional[bytes]:
-    """The bytes of ``tensor_desc(t)`` (None: no tensor).  A step makes some
-    dozens of these, and packing takes a third of the time of filling a
-    ctypes structure (0.8 against 2.4 us)."""
-    if t is None:
-        return None
-    n = t.dim()
-    if n > 4:
-        return bytes(tensor_desc(t))
-    return _DESC[n].pack(t.data_ptr(), _DTYPES.get(t.dtype, 99), n, *t.shape, *t.stride())
+def _step(name):
+    """A call of paged_step.h as the ``_bind`` module makes it (bind.c): its
+    arguments in that file's order.  It returns the status, PD_EINVAL for
+    tensors that are not on one CUDA device; a launch goes to the tensors'
+    device, whichever is current."""
+    global _bind
+    if _bind is None:
+        L = lib()
+        if not os.path.exists(_build.BIND):
+            raise RuntimeError(f"{_build.BIND} is missing: build it with "
+                               "paged_split_kv_02_gb300.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_bind", _build.BIND)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bind", loader))
+        loader.exec_module(m)
+
+        def address(f):
+            return ctypes.cast(f, ctypes.c_void_p).value
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+        m.setup(address(L.paged_decode_attn_sinks), address(L.paged_prefill_attn_sinks),
+                address(L.paged_batch_tables), address(L.paged_rope_axes_cache_write), _DTYPES,
+                raw, torch.cuda.current_device, torch.cuda.set_device, torch.cuda.is_available)
+        _bind = m
+    return getattr(_bind, name)
 
 
-_NO_DEVICE = contextlib.nullcontext()
-
-
-def _launch_on(tensors, stream):
-    """(context, stream handle) of a launch on the tensors' device, whichever
-    is current, or None when they are not on one CUDA device.  Without any
-    CUDA device the library is left to report that."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            return None
-    if dev.type != "cuda":
-        return None if torch.cuda.is_available() else (_NO_DEVICE, 0)
-    if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if dev.index == torch.cuda.current_device():
-        return _NO_DEVICE, handle
-    return torch.cuda.device(dev), handle
-
-
-def _step_call(name, tensors, args, stream, check):
-    """A call of paged_step.h: ``args(packed tensors, stream handle)`` gives
-    the C arguments.  Tensors on several devices, or on none that the library
-    runs on, are PD_EINVAL."""
-    where = _launch_on(tensors, stream)
-    if where is None:
-        rc = -1
-    else:
-        with where[0]:
-            rc = getattr(lib(), name)(*args([_packed(t) for t in tensors], where[1]))
+def _checked(rc, name, check):
     if check and rc != PD_OK:
         raise PagedDecodeError(rc, name)
     return rc
@@ -418,15 +389,12 @@ def paged_decode_attn_sinks(q, k_cache, v_cache, block_table, seq_lens, out, num
     tokens of every sequence stay visible (see paged_step.h);
     ``query_start`` as in ``paged_decode_attn_varlen``, or None for
     ``max_query_len`` query tokens per sequence."""
-    sp = ctypes.byref(scratch.desc) if scratch is not None else None
-    op = ctypes.byref(opts) if opts is not None else None
-    return _step_call(
-        "paged_decode_attn_sinks",
-        (q, k_cache, v_cache, block_table, seq_lens, query_start, out),
-        lambda t, st: (*t, int(num_q_heads), int(num_kv_heads), int(head_size), int(page_size),
-                       int(max_query_len), int(window), int(sinks), float(scale), int(layout), sp,
-                       st, op),
-        stream, check)
+    rc = _step("attn_sinks")(
+        q, k_cache, v_cache, block_table, seq_lens, query_start, out, num_q_heads, num_kv_heads,
+        head_size, page_size, max_query_len, window, sinks, layout, scale,
+        None if scratch is None else ctypes.addressof(scratch.desc),
+        None if opts is None else ctypes.addressof(opts), stream)
+    return _checked(rc, "paged_decode_attn_sinks", check)
 
 
 def paged_decode_plan_sinks(num_seqs, num_q_heads, num_kv_heads, head_size, page_size,
@@ -455,11 +423,10 @@ def paged_batch_tables(context_lens, query_lens, block_table, query_start, seq_l
     ``seq_lens``, ``positions`` ([T] or [axes, T]), ``slot_mapping``, and,
     with ``free_pages``, the new pages' entries of ``block_table`` and
     ``next_cursor`` (see paged_step.h)."""
-    return _step_call(
-        "paged_batch_tables",
-        (context_lens, query_lens, free_pages, cursor, position_delta, block_table, query_start,
-         seq_lens, positions, slot_mapping, next_cursor),
-        lambda t, st: (*t, int(page_size), int(num_pages), st), stream, check)
+    rc = _step("batch_tables")(
+        context_lens, query_lens, free_pages, cursor, position_delta, block_table, query_start,
+        seq_lens, positions, slot_mapping, next_cursor, page_size, num_pages, stream)
+    return _checked(rc, "paged_batch_tables", check)
 
 
 def paged_rope_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache,
@@ -503,15 +470,11 @@ def paged_rope_axes_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache,
     """``paged_rope_cache_write`` with ``positions`` [axes, T]: rotated pair i
     takes its angle at the position of axis ``pair_axis[i]`` (``rot_dim / 2``
     small integers, as ``rope_pair_axis`` gives them)."""
-    pairs = bytes(pair_axis)
-    if len(pairs) != int(rot_dim) // 2:
-        raise ValueError(f"pair_axis has {len(pairs)} entries, rot_dim / 2 is {int(rot_dim) // 2}")
-    return _step_call(
-        "paged_rope_axes_cache_write",
-        (q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache),
-        lambda t, st: (*t[:6], pairs, *t[6:], int(num_q_heads), int(num_kv_heads), int(head_size),
-                       int(rot_dim), int(page_size), int(layout), int(bool(is_neox)), st),
-        stream, check)
+    rc = _step("rope_axes")(
+        q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache, num_q_heads,
+        num_kv_heads, head_size, rot_dim, page_size, layout, bool(is_neox), bytes(pair_axis),
+        stream)
+    return _checked(rc, "paged_rope_axes_cache_write", check)
 
 
 def rope_case(case, q_out=None, stream=None):
@@ -605,14 +568,11 @@ def paged_prefill_attn_sinks(q, k_cache, v_cache, block_table, seq_lens, query_s
     """The prefill call over a sliding window beside which the first
     ``sinks`` tokens stay visible (``work`` and ``info`` from
     ``paged_prefill_plan_sinks``)."""
-    sp = ctypes.byref(scratch.desc) if scratch is not None else None
-    return _step_call(
-        "paged_prefill_attn_sinks",
-        (q, k_cache, v_cache, block_table, seq_lens, query_start, work, out),
-        lambda t, st: (*t[:7], ctypes.byref(info), t[7], int(num_q_heads), int(num_kv_heads),
-                       int(head_size), int(page_size), int(window), int(sinks), float(scale),
-                       int(layout), sp, st),
-        stream, check)
+    rc = _step("prefill_sinks")(
+        q, k_cache, v_cache, block_table, seq_lens, query_start, work, out, num_q_heads,
+        num_kv_heads, head_size, page_size, window, sinks, layout, scale, ctypes.addressof(info),
+        None if scratch is None else ctypes.addressof(scratch.desc), stream)
+    return _checked(rc, "paged_prefill_attn_sinks", check)
 
 
 def prefill_case(case, out=None, scratch=None, stream=None, num_sms=0, plan=None):

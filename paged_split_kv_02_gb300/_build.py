@@ -1,5 +1,6 @@
 """Build of libpaged_decode.so: nvcc, one translation unit per head size,
-compiled in parallel for sm_103a only, linked in-tree next to this file."""
+compiled in parallel for sm_103a only, linked in-tree next to this file; and of
+the Python module that marshals the step calls' arguments (bind.c)."""
 
 from __future__ import annotations
 
@@ -8,11 +9,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpaged_decode.so")
+BIND = os.path.join(HERE, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "bind.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fvisibility=hidden"]
@@ -31,13 +35,13 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")))
+            + glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")) + [BIND_SRC])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -71,6 +75,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-Wall", *inc,
+           "-I" + sysconfig.get_paths()["include"], BIND_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for bind.c:\n{r.stderr}")
+    os.replace(tmp, BIND)
     return LIB
 
 

@@ -31,13 +31,17 @@ def test_exports_every_declared_symbol():
         assert hasattr(pd.lib(), n), n
 
 
-def test_packed_descriptors_are_the_structures():
-    for t in (torch.zeros(3), torch.zeros(4, 5)[:, 1:3],
-              torch.zeros(2, 3, 4, 6, dtype=torch.int32)[..., ::2],
-              torch.zeros(2, 1, 4, dtype=torch.bfloat16).transpose(0, 2), torch.zeros(1, 1, 1, 1, 2),
-              torch.zeros(())):
-        assert pd._packed(t) == bytes(pd.tensor_desc(t))
-    assert pd._packed(None) is None
+def test_arguments_that_are_not_what_they_should_be():
+    q = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
+    with pytest.raises(AttributeError):
+        _attn(q="no tensor")
+    with pytest.raises(OverflowError):
+        _attn(window=2 ** 31)
+    with pytest.raises(TypeError):
+        _attn(sinks=1.5)
+    assert _attn(q=None) == -1 and _attn(out=None) == -1
+    assert _attn(q=torch.zeros(1, 1, 1, 4, 8, 128, dtype=torch.bfloat16)) == -1   # six dims
+    assert _attn(q=q.double()) == -2
 
 
 def _attn(**kw):
