@@ -55,7 +55,12 @@ PD_API int paged_decode_attn_sinks(const pd_tensor *q, const pd_tensor *k_cache,
                                    int sinks, float scale, int layout, pd_scratch *scratch,
                                    void *stream, const pd_options *opts);
 
-/* The launch plan of that call, on the host only. */
+/* The launch plan of that call, on the host only.  A batch that fills the GPU
+ * more than once and sets no knob is planned as path 6: one wave of grid_x
+ * CTAs that each take an equal share of the blocks of every (sequence, kv
+ * head), cut where the shares end (grid_y = 1; seg_blocks, the most blocks of
+ * one; max_segments and max_parts = grid_x).  Its scratch need is two parts
+ * per CTA. */
 PD_API int paged_decode_plan_sinks(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
                                    int page_size, int max_query_len, int window, int sinks,
                                    int block_table_width, int num_sms, const pd_scratch *scratch,

@@ -186,6 +186,66 @@ struct PlanOut {
   int nt, kg, ns;
 };
 
+constexpr int kSmemPerSm = 233472, kSmemReserved = 1024;  // of an SM, and per resident CTA
+
+// The plan of the window kernel; false where it does not serve the call: one
+// sequence or more than kWindowSeqs, wide heads, more than 56 packed rows, a
+// launch knob that asks for something, or a scratch too small for the parts of
+// a quarter of the SMs.
+bool plan_window(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks, int bt_width,
+                 int num_sms, const pd_scratch *scratch, const pd_options &o, pd_plan *plan) {
+  const int64_t R = (int64_t)(Hq / Hkv) * M;
+  if (S < 2 || S > kWindowSeqs || D > 256 || R > 8 * kWindowWarps || Hkv > 65535) return false;
+  if (o.segments || o.row_groups || o.key_groups || o.stages || o.cluster || o.path ||
+      o.max_ctas_hint || o.merge || o.mergers)
+    return false;
+  // warp groups: three of one or two n-tiles (one group took 89 us for what
+  // three took 44, two 54), two of three, else one
+  const int NT = (int)cdiv(R, 8), KG = std::min(kWindowGroups, kWindowWarps / NT);
+  const int threads = 32 * (NT * KG + 1);
+  const int fixed = smem_bytes_window(D, NT, KG, 0, S, true);
+  // Two CTAs on an SM where registers and shared memory leave each three
+  // stages, so that one streams while the other finishes a unit (D = 128, one
+  // n-tile, 128 sequences of 1k keys: 78.8 us against 84.3 with one; at D = 256
+  // two stages each are left, 30.9 against 27.1), else one with the whole SM.
+  int occ = 2, NS = (kSmemPerSm / 2 - kSmemReserved - fixed) / (kStageBytes + 16);
+  if (NS < 3 || threads > 128) {
+    occ = 1;
+    NS = (kSmemLimit - fixed) / (kStageBytes + 16);
+  }
+  NS = std::min(8, NS);
+  if (NS < 2) return false;
+  const int64_t nb_max = std::min<int64_t>(
+      cdiv((int64_t)bt_width * P, kBlockKeys),
+      cdiv((int64_t)window + M - 1, kBlockKeys) + 1 + cdiv(sinks, kBlockKeys));
+  if ((nb_max + kUnitCost) * S * Hkv >= 1 << 30) return false;  // places of the line are ints
+  // two parts of (acc, m, l) per CTA, behind the counters
+  if (!scratch || !scratch->data || scratch->counter_slots < 2LL * S * Hkv) return false;
+  const int64_t cbytes = (scratch->counter_slots * 4 + 255) / 256 * 256;
+  const int64_t per_cta = 2LL * NT * 8 * (D + 2) * 4;
+  const int G = (int)std::min<int64_t>(occ * num_sms,
+                                       ((int64_t)scratch->bytes - cbytes - 256) / per_cta);
+  if (G < 1 || G < num_sms / 4) return false;
+  *plan = pd_plan{};
+  plan->path = 6;
+  plan->merge = 1;
+  plan->rows = plan->rows_per_cta = (int)R;
+  plan->row_groups = 1;
+  plan->n_tiles = NT;
+  plan->key_groups = KG;
+  plan->stages = NS;
+  plan->seg_blocks = (int)nb_max;
+  plan->max_segments = G;
+  plan->cluster = 1;
+  plan->max_parts = G;
+  plan->grid_x = G;
+  plan->grid_y = 1;
+  plan->block_threads = threads;
+  plan->smem_bytes = smem_bytes_window(D, NT, KG, NS, S, true);
+  plan->scratch_needed = G * per_cta + 256;
+  return true;
+}
+
 int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks, int bt_width,
               int num_sms, const pd_scratch *scratch, const pd_options *opts, pd_plan *plan) {
   pd_options o{};
@@ -411,6 +471,15 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   } else if (o.merge == 2 && max_parts > 1) {
     return PD_EINVAL;  // the grid does not fit at once, or a cluster was asked for
   }
+  // A batch over a window with sinks that would take more than one wave goes to
+  // the window kernel.  In one wave the cooperative merge, or no split at all,
+  // is as fast or faster (us, this plan against the window kernel: 8 kv heads
+  // at D = 128, 4 sequences of 128 keys 8.1 / 8.5, 2 of 1k 10.4 / 9.8, 4 of 1k,
+  // two waves, 20.2 / 10.1; 2 at D = 256, 4 of 1k 10.0 / 15.2, 32 of 1k 33.5 /
+  // 19.4).
+  if (sinks > 0 && (int64_t)S * Hkv * rg * nseg > num_sms &&
+      plan_window(S, Hq, Hkv, D, P, M, window, sinks, bt_width, num_sms, scratch, o, plan))
+    return PD_OK;
   // launched as (segments, kv heads x row groups, sequences)
   if ((int64_t)Hkv * rg * nseg > INT32_MAX || (int64_t)Hkv * rg > 65535 || S > 65535)
     return PD_EINVAL;
@@ -539,7 +608,7 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
                         : kWaitLimitNs;
   p.epi_floats = (plan.path == 3 ? epilogue_bytes_tc(head_size, plan.stages)
                                   : epilogue_bytes(head_size, plan.n_tiles, plan.stages)) / 4;
-  if (plan.max_parts > 0) {
+  if (plan.max_parts > 0 && plan.path != 6) {
     char *base = static_cast<char *>(scratch->data);
     const int64_t cbytes = (scratch->counter_slots * 4 + 255) / 256 * 256;
     const int64_t units = S * num_kv_heads * plan.row_groups;
@@ -550,9 +619,24 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
     p.part_ml = reinterpret_cast<float *>(base + cbytes + acc_bytes);
   }
 
+  if (plan.path == 6) {
+    // [2 x CTAs] parts behind the counters
+    char *base = static_cast<char *>(scratch->data);
+    const int64_t cbytes = (scratch->counter_slots * 4 + 255) / 256 * 256;
+    const int64_t acc = (2LL * plan.grid_x * plan.n_tiles * 8 * head_size * 4 + 255) / 256 * 256;
+    p.counters = reinterpret_cast<int *>(base);
+    p.part_acc = reinterpret_cast<float *>(base + cbytes);
+    p.part_ml = reinterpret_cast<float *>(base + cbytes + acc);
+    // (8 line units: at twice as many, 4 sequences x 8 heads of 128 keys take
+    // 10.7 us instead of 8.6)
+    p.min_share = 8;
+  }
+
   Launch l;
   // (segment, kv head x row group, sequence): plan.grid_x CTAs per sequence
-  l.grid = dim3(plan.max_segments, num_kv_heads * plan.row_groups, plan.grid_y);
+  // (the window kernel: CTAs of a line)
+  l.grid = plan.path == 6 ? dim3(plan.grid_x)
+                          : dim3(plan.max_segments, num_kv_heads * plan.row_groups, plan.grid_y);
   l.block = dim3(plan.block_threads, 1, 1);
   l.smem = plan.smem_bytes;
   l.cluster = plan.cluster;

@@ -79,7 +79,14 @@ struct Params {
   // keys at the start of a sequence that stay visible beside the window;
   // > 0 (then window > 0 too) selects the kernel instances built for it
   int sinks;
+  // the window kernel's line of blocks: the least share of a CTA
+  int min_share;
 };
+// What a (sequence, kv head) counts in that line beside its blocks: Q's load,
+// the epilogue and the part's publication take about as long as twelve blocks
+// stream (4 / 8 / 12 / 16, us: 64 sequences of 1k keys at D = 128 43.0 / 42.9
+// / 42.7 / 42.9, 48 of up to 2k at D = 256 28.6 / 23.3 / 22.4 / 22.4).
+constexpr int kUnitCost = 12;
 
 struct Launch {
   dim3 grid;
@@ -99,6 +106,19 @@ inline int smem_bytes(int D, int NT, int NS) {
 inline int smem_bytes_dot(int D, int KG, int NS) {
   const int stage_keys = kStageBytes / 2 / (kBlockKeys * D * 2) * kBlockKeys;
   return smem_bytes(D, 1, NS) + 16 + 8 * D * 4 + KG * stage_keys * 8 * 4;
+}
+
+// The window kernel (pd_window.cuh): ring + the warp groups' sums + barriers +
+// flags + staged page ids + the sequences' lengths and first rows.  It takes
+// batches of up to kWindowSeqs sequences (their lengths lie in shared memory).
+constexpr int kWindowSeqs = 1024;
+constexpr int kWindowGroups = 3;  // warp groups at most
+// consumer warps: with the producer at most two warps per SM sub-partition,
+// which leaves a thread 255 registers (nine warps: 168, and the fragments spill)
+constexpr int kWindowWarps = 7;
+inline int smem_bytes_window(int D, int NT, int KG, int NS, int S, bool varlen) {
+  return kSmemAlign + NS * (kStageBytes + 16) + KG * NT * 8 * (D + 2) * 4 +
+         4 * (kWindowWarps + 1) + 16 + 64 + 4 * kBlockIds + 4 * S + (varlen ? 4 * (S + 1) : 0) + 16;
 }
 
 // Bytes of the epilogue region (the ring and the Q tile once they are dead).
@@ -182,7 +202,8 @@ inline int64_t epilogue_floats(int D, int NT, int KG, int CS, int ncl_max) {
 // rows on the M side, 16 rows per warp (prefill tiles, D <= 128), 5 =
 // tcgen05 prefill tiles of 128 rows with Q, S, P and O in tensor memory
 // (D = 128)
-// (p.sinks > 0: the instances for a window with sinks, paths 1, 4 and 5)
+// (p.sinks > 0: the instances for a window with sinks, paths 1, 4 and 5, and
+// 6, the window kernel of batches, D <= 256)
 cudaError_t launch_mma(int D, bool bf16, int path, const CUtensorMap &tk, const CUtensorMap &tv,
                        const Params &p, const Launch &l, cudaStream_t stream);
 

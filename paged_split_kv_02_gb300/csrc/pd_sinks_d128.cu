@@ -1,5 +1,5 @@
 // Window with sinks, head size 128: decode (mma.sync) and tensor-memory prefill tiles.
-#include "pd_kernel.cuh"
+#include "pd_window.cuh"
 
 namespace pd {
 
@@ -8,6 +8,9 @@ cudaError_t launch_sinks_d128(bool bf16, int path, const CUtensorMap &tk, const 
   if (path == 5)
     return bf16 ? launch_mma_t<128, true, false, false, false, true, true>(tk, tv, p, l, stream)
                 : launch_mma_t<128, false, false, false, false, true, true>(tk, tv, p, l, stream);
+  if (path == 6)
+    return bf16 ? launch_window_t<128, true>(tk, tv, p, l, stream)
+                : launch_window_t<128, false>(tk, tv, p, l, stream);
   if (path != 1) return cudaErrorInvalidValue;
   return bf16 ? launch_mma_t<128, true, false, false, false, false, true>(tk, tv, p, l, stream)
               : launch_mma_t<128, false, false, false, false, false, true>(tk, tv, p, l, stream);

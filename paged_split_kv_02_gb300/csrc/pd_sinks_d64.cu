@@ -1,5 +1,5 @@
 // Window with sinks, head size 64: decode (mma.sync) and prefill tiles with the rows on the M side.
-#include "pd_kernel.cuh"
+#include "pd_window.cuh"
 
 namespace pd {
 
@@ -8,6 +8,9 @@ cudaError_t launch_sinks_d64(bool bf16, int path, const CUtensorMap &tk, const C
   if (path == 4)
     return bf16 ? launch_mma_t<64, true, false, false, true, false, true>(tk, tv, p, l, stream)
                 : launch_mma_t<64, false, false, false, true, false, true>(tk, tv, p, l, stream);
+  if (path == 6)
+    return bf16 ? launch_window_t<64, true>(tk, tv, p, l, stream)
+                : launch_window_t<64, false>(tk, tv, p, l, stream);
   if (path != 1) return cudaErrorInvalidValue;
   return bf16 ? launch_mma_t<64, true, false, false, false, false, true>(tk, tv, p, l, stream)
               : launch_mma_t<64, false, false, false, false, false, true>(tk, tv, p, l, stream);

@@ -87,7 +87,10 @@ def test_plan_sinks():
                 # at its start, and the sinks, or the whole table
                 need = min(2048, -(-(window + 3) // 16) + 1 + -(-sinks // 16))
                 assert p["seg_blocks"] * p["max_segments"] >= need
-                assert p["path"] == 1 and p["smem_bytes"] <= 232448
+                assert p["path"] in ((1, 6) if S > 1 and sinks else (1,)) and p["smem_bytes"] <= 232448
+                assert p["scratch_needed"] <= pd.paged_decode_scratch_bytes(S, 32, 8, 128, 4, 256)
+                if p["path"] == 1 and S > 1 and sinks:   # one wave
+                    assert p["grid_x"] * p["grid_y"] <= 152
     assert (pd.paged_decode_plan_sinks(1, 32, 8, 128, 16, 4, 512, 0, 2048, 152)
             == pd.paged_decode_plan(1, 32, 8, 128, 16, 4, 512, 2048, 152))
     # without a window every key is visible, whatever the sinks
