@@ -95,6 +95,9 @@ __device__ __forceinline__ float add2_f32(float acc, uint32_t w, std::false_type
   return acc;
 }
 
+// the n lowest of 16 bits (n clamped to 0 .. 16)
+__device__ __forceinline__ uint32_t first_bits(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
+
 // Column swizzle of the fp32 partial tiles in shared memory: rows 2x and 2x+1
 // of an n-tile are spread over four 8-word bank groups.
 __device__ __forceinline__ int psw(int d, int r) { return d ^ (((r >> 1) & 3) << 3); }
@@ -561,7 +564,9 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
     if (warp < kTpSoftmaxWarps) {
       // Q rows of tile X into its 128-byte-swizzled K-major tile in shared
       // memory ([tile][64-dim box][128 rows][128 B]); zeros for rows past
-      // the requests
+      // the requests.  Sixteen lanes take a row's 16 chunks, two rows of the
+      // warp at a time (a lane per row would touch 32 lines with every load:
+      // 4.4 us of a tile against 1.2)
       const uint4 *src = nullptr;
       if (live) {
         const int i = token_of(rr_tp), jq = rr_tp - i * p.G;
@@ -570,11 +575,16 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
                                               (int64_t)(h * p.G + jq) * p.q_s1);
       }
       unsigned char *qx = qs + X * (kTpRows * D * 2);
+      static_assert(!TP || D / 8 == 16, "half a warp takes a row");
+      const int c = lane & 15;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4 *>(qx + (c >> 3) * (kTpRows * 128) + r_tp * 128 +
-                                   (((c & 7) ^ (r_tp & 7)) << 4)) = v;
+      for (int i = 0; i < 16; ++i) {
+        const int rw = 2 * i + (lane >> 4), r = 32 * (warp & 3) + rw;
+        const uint4 *row = reinterpret_cast<const uint4 *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), rw));
+        const uint4 v = row ? __ldg(row + c) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(qx + (c >> 3) * (kTpRows * 128) + r * 128 +
+                                   (((c & 7) ^ (r & 7)) << 4)) = v;
       }
       fence_proxy_async_smem();  // the tensor core reads the tiles
     }
@@ -759,15 +769,22 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
           if (fast) {
             mx = fast_max();
           } else {
-            // scaled scores with the mask applied (-inf), kept as fp32 bits
+            // scaled scores with the mask applied (-inf), kept as fp32 bits;
+            // the visible keys of each block as bits
+            uint32_t vis[SC / 32] = {};
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+              const int kb = block_key(b);
+              uint32_t m = first_bits(hi - kb) & ~first_bits(lo - kb);
+              if constexpr (SINK) m |= first_bits(min(p.sinks, hi) - kb);
+              if (live && b < nbt) vis[b >> 1] |= m << (16 * (b & 1));
+            }
             float a[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) a[u] = -INFINITY;
 #pragma unroll
             for (int c = 0; c < SC; ++c) {
-              const int k = block_key(c >> 4) + (c & 15);
-              float x = __uint_as_float(sr[c]) * sl2;
-              if (!live || !(c < nbt * kBlockKeys && sees(k, lo, hi))) x = -INFINITY;
+              const float x = (vis[c >> 5] & (1u << (c & 31))) ? __uint_as_float(sr[c]) * sl2 : -INFINITY;
               sr[c] = __float_as_uint(x);
               a[c & 7] = fmaxf(a[c & 7], x);
             }
@@ -852,14 +869,13 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
         // are the same zeros)
         if (SINK ? !fast : !(nbt == TB && key_t0 >= u_lo && key_t0 + SC <= u_hi)) {
           unsigned char *vb = ring + slot * STAGE + TB * BLOCK_BYTES;
-          for (int c = 32 * (warp & 3) + lane; c < nbt * kBlockKeys; c += 128) {
+          // (a key's 256 bytes by 16 threads)
+          const int x = lane & 15;
+          for (int c = 2 * (warp & 3) + (lane >> 4); c < nbt * kBlockKeys; c += 8) {
             const int k = block_key(c >> 4) + (c & 15);
-            if (!sees(k, u_lo, u_hi)) {
-#pragma unroll 1
-              for (int x = 0; x < NBOX * 8; ++x)
-                *reinterpret_cast<uint4 *>(vb + (c >> 4) * BLOCK_BYTES + (x >> 3) * 2048 +
-                                           (c & 15) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
+            if (!sees(k, u_lo, u_hi))
+              *reinterpret_cast<uint4 *>(vb + (c >> 4) * BLOCK_BYTES + (x >> 3) * 2048 +
+                                         (c & 15) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         tmem_wait_st();
@@ -1742,24 +1758,35 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
       const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
       float *dst = cp + (size_t)r * D;
       if (nseg == 1) {
-        // an unsplit tile: each row normalised and stored from here
+        // an unsplit tile: each row normalised here, turned through the dead
+        // ring (8 KiB of it per warp: the copies and every MMA are done), and
+        // stored by 16 lanes, two rows of the warp at a time
         const float inv = (have && l0 > 0.f) ? sfu_rcp(l0) : 0.f;
         T *orow = r < nrows ? out_row(r) : nullptr;
+        unsigned char *turn = ring + warp * (32 * D * 2);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
           tmem_ld32(tmem_base + tp_o_col(D) + g * D + lane_base + c0, o);
           tmem_wait_ld();
-          if (orow) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              const float v[8] = {__uint_as_float(o[i]) * inv,     __uint_as_float(o[i + 1]) * inv,
-                                  __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv,
-                                  __uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv,
-                                  __uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv};
-              store8<BF16>(orow + c0 + i, v);
-            }
+          for (int i = 0; i < 32; i += 8) {
+            const float v[8] = {__uint_as_float(o[i]) * inv,     __uint_as_float(o[i + 1]) * inv,
+                                __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv,
+                                __uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv,
+                                __uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv};
+            store8<BF16>(turn + lane * (D * 2) + ((((c0 + i) >> 3) ^ (lane & 7)) << 4), v);
           }
+        }
+        __syncwarp();
+        const int c = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int rw = 2 * i + (lane >> 4);
+          T *dst = reinterpret_cast<T *>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(orow), rw));
+          const uint4 v = *reinterpret_cast<const uint4 *>(turn + rw * (D * 2) + ((c ^ (rw & 7)) << 4));
+          if (dst) *reinterpret_cast<uint4 *>(dst + 8 * c) = v;
         }
       }
 #pragma unroll 1
