@@ -110,19 +110,3 @@ def rope_cache_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                 v_pool[page, h, off] = vv[t, h]
         written.append((t, page, off))
     return q_out, k_pool, v_pool, written
-
-
-def rope_axes(x: np.ndarray, positions: np.ndarray, cos_sin: np.ndarray, pair_axis, rot_dim: int,
-              is_neox: bool) -> np.ndarray:
-    """``rope`` with a position per axis, positions [axes, T]: pair i by the
-    angle at positions[pair_axis[i], t]."""
-    out = np.array(x, dtype=np.float64, copy=True)
-    half = rot_dim // 2
-    a, b = pair_index(rot_dim, is_neox)
-    for i in range(half):
-        p = positions[pair_axis[i]]
-        c, s = cos_sin[p, i][:, None], cos_sin[p, half + i][:, None]
-        x1, x2 = x[:, :, a[i]], x[:, :, b[i]]
-        out[:, :, a[i]] = x1 * c - x2 * s
-        out[:, :, b[i]] = x2 * c + x1 * s
-    return out

@@ -19,6 +19,9 @@ constexpr int kCountersPerPair = 2 * kMaxRowGroups;
 static_assert(kCountersPerPair == PD_COUNTERS_PER_PAIR, "counter reservation of the C ABI");
 constexpr int kMaxConsumerWarps = 8;  // warps that compute; one more loads
 constexpr int kMaxThreads = 32 * (kMaxConsumerWarps + 1);
+// prefill tiles of a window with sinks at head size 64: four consumer warps, two
+// CTAs on an SM
+constexpr int kRmThreads = 32 * 5;
 constexpr int kSmemAlign = 1024;      // the 128-byte TMA swizzle repeats every 1 KiB
 constexpr int kBlockIds = 512;        // page ids of 16-key blocks staged in shared memory
 constexpr int kMaxBatchSegBlocks = 384;  // longest planned segment of a batch (6144 keys)

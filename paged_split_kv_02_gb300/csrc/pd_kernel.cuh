@@ -144,7 +144,8 @@ __device__ __forceinline__ float exp2_or_zero(float x, float m) {
 }
 
 template <int D, bool BF16, bool TC, bool DOT, bool RM, bool TP, bool SINK>
-__global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThreads, 1)
+__global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : RM && SINK ? kRmThreads : kMaxThreads,
+                                  RM && SINK ? 2 : 1)
     pd_decode_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ Params p) {
   static_assert((int)TC + (int)DOT + (int)RM + (int)TP <= 1, "one consumer kind per instance");
@@ -1393,15 +1394,33 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : kMaxThread
       float mxa = -INFINITY, mxb = -INFINITY;
 #pragma unroll
       for (int kn = 0; kn < KN; ++kn) {
-        const int k0 = (SINK ? seq_block(my_b0 + j * TB + (kn >> 1)) * kBlockKeys + (kn & 1) * 8
-                             : key_t0 + kn * 8) +
-                       2 * tq;
         const bool blk = (kn >> 1) < nbt;
+        if constexpr (SINK) {
+          // a block that every row sees, or the visible keys of this lane's
+          // two rows as bits
+          const int key0 = seq_block(my_b0 + j * TB + (kn >> 1)) * kBlockKeys;
+          uint32_t va = 0, vb = 0;
+          if (blk && all_see(key0)) {
+            va = vb = 0xffffu;
+          } else if (blk) {
+            va = (first_bits(hi_a - key0) & ~first_bits(lo_a - key0)) |
+                 first_bits(min(p.sinks, hi_a) - key0);
+            vb = (first_bits(hi_b - key0) & ~first_bits(lo_b - key0)) |
+                 first_bits(min(p.sinks, hi_b) - key0);
+          }
+          const int at = (kn & 1) * 8 + 2 * tq;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = k0 + (e & 1);
-          const bool ok = blk && ((e < 2) ? sees(k, lo_a, hi_a) : sees(k, lo_b, hi_b));
-          sc[kn][e] = ok ? sc[kn][e] * p.scale_log2 : -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            sc[kn][e] = ((e < 2 ? va : vb) >> (at + (e & 1))) & 1u ? sc[kn][e] * p.scale_log2
+                                                                   : -INFINITY;
+        } else {
+          const int k0 = key_t0 + kn * 8 + 2 * tq;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = k0 + (e & 1);
+            const bool ok = blk && ((e < 2) ? (k >= lo_a && k < hi_a) : (k >= lo_b && k < hi_b));
+            sc[kn][e] = ok ? sc[kn][e] * p.scale_log2 : -INFINITY;
+          }
         }
         mxa = fmaxf(mxa, fmaxf(sc[kn][0], sc[kn][1]));
         mxb = fmaxf(mxb, fmaxf(sc[kn][2], sc[kn][3]));

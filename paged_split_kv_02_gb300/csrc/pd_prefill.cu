@@ -120,7 +120,7 @@ struct PrefillShape {
   int64_t epi;  // bytes of the epilogue region
 };
 
-int prefill_shape(int D, PrefillShape *sh) {
+int prefill_shape(int D, bool sinks, PrefillShape *sh) {
   if (D == 128) {
     sh->path = 5;
     sh->NT = 2 * kTpRows / 8;
@@ -139,6 +139,14 @@ int prefill_shape(int D, PrefillShape *sh) {
   sh->KG = sh->path == 4 ? 2 : 1;
   const int fixed = smem_bytes(D, sh->NT, 0);
   sh->NS = std::min(8, (kSmemLimit - fixed - 16 * 8) / kStageBytes) / sh->KG * sh->KG;
+  // A tile of a window is a few stages, so its start and end weigh: one warp
+  // group and three stages, and an SM holds two CTAs (a ragged batch of 1276
+  // tokens, 16 / 4 heads, window 700: 30.7 us; one CTA of two groups and six
+  // stages 37.9).
+  if (sinks && sh->path == 4) {
+    sh->KG = 1;
+    sh->NS = 3;
+  }
   if (sh->NS < 2) return PD_EINVAL;
   if (epilogue_floats(D, sh->NT, sh->KG, 1, kMaxSegments) * 4 > epilogue_bytes(D, sh->NT, sh->NS))
     return PD_EINVAL;
@@ -249,7 +257,7 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   unsigned int *status = nullptr;
   if ((rc = device_check(&num_sms, &status)) != PD_OK) return rc;
   PrefillShape sh;
-  if ((rc = prefill_shape(head_size, &sh)) != PD_OK) return rc;
+  if ((rc = prefill_shape(head_size, sinks > 0 && window > 0, &sh)) != PD_OK) return rc;
 
   Params p{};
   // split tiles need scratch: counters for every (split tile, kv head) and

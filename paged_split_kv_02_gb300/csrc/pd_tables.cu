@@ -3,16 +3,22 @@
 // one launch.
 //
 // The starts and the pages taken are exclusive sums over the requests.  Every
-// block forms them itself, in passes of one request per thread (a block-wide
-// scan of two sums), so no block waits on another: block 0 writes what
-// belongs to requests, block b > 0 the kTokens tokens from (b - 1) kTokens
-// on.  A token block notes each request that owns some of its tokens at the
-// first of them; a running maximum over the tokens then gives every token
-// its request.  A new page is written to the block table by the one token
-// that opens it (the token whose position is a multiple of the page size).
+// block forms them itself, a few requests of a thread at a time and a
+// block-wide scan of two sums, so no block waits on another: block 0 writes what
+// belongs to requests, block b > 0 the kTokens tokens from (b - 1) kTokens on,
+// four of a thread.  A token block notes each request that owns some of its
+// tokens at the first of them; a running maximum over the tokens then gives
+// every token its request.  A new page is written to the block table by the
+// one token that opens it (the token whose position is a multiple of the page
+// size).
 //
 // The work is a few bytes per token: launch latency and one chain of dependent
-// loads (lengths -> sums -> page id) bound it.
+// loads (lengths -> sums -> page id) bound it.  256 requests of 1 .. 4 tokens
+// take 2.9 us, 1500 with 234000 tokens on three axes 4.6 us (3.7 MB).  Up to 256
+// requests take one request of a thread and 256 threads (with 512: 3.5 us),
+// more take four and 512 threads (1500 requests in one pass; with 256 threads
+// and two passes 5.0, eight of a thread 5.3).  One token of a thread, in blocks
+// of 1024, took 3.2 and 6.1 us; four whose loads wait for one another 4.1 and 6.1.
 #include "paged_step.h"
 #include "pd_internal.h"
 #include "pd_ptx.cuh"
@@ -20,8 +26,10 @@
 namespace pd {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kTokens = kThreads;  // tokens of a block
+constexpr int kFew = 256;   // threads, with a request each
+constexpr int kMany = 512;  // threads, with kPerMany requests each per pass
+constexpr int kPerMany = 4;
+constexpr int kRun = 4;     // tokens of a thread
 
 struct TablesParams {
   const int32_t *context, *query, *free_pages, *cursor, *delta;
@@ -31,8 +39,20 @@ struct TablesParams {
   int32_t *query_start, *seq_lens, *positions, *slots, *next_cursor;
   int64_t pos_stride;
   int axes, S, T, num_free, P, num_pages;
+  unsigned long long magic;  // ceil(2^shift / P), shift = 31 + ceil(log2 P)
+  int shift;
   unsigned int *status;
 };
+
+// n / P for n < 2^31: n x (magic P - 2^shift) < 2^31 P <= 2^shift, so the
+// product's high part is exact
+__device__ __forceinline__ unsigned int div_p(unsigned int n, const TablesParams &p) {
+  return (unsigned int)((n * p.magic) >> p.shift);
+}
+__device__ __forceinline__ unsigned int cdiv_p(unsigned int n, const TablesParams &p) {
+  const unsigned int q = div_p(n, p);
+  return q + (q * (unsigned)p.P != n);
+}
 
 // Two running sums: tokens (held at T, so that they cannot wrap) and pages
 // (wrapping, and then of requests past T only, which take none).
@@ -44,71 +64,96 @@ __device__ __forceinline__ Sums add(Sums a, Sums b, unsigned int T) {
   return {min(a.tok + b.tok, T), a.pages + b.pages};
 }
 
-__device__ __forceinline__ unsigned int cdiv_u(unsigned int a, unsigned int b) {
-  return (a + b - 1) / b;
+// v[0 .. 4) to the four places from p on that lie before n, in one store
+// where the address allows it
+__device__ __forceinline__ void store4(int32_t *p, const int (&v)[kRun], int n) {
+  if (n >= kRun && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+    *reinterpret_cast<int4 *>(p) = make_int4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+      if (i < n) p[i] = v[i];
+  }
 }
 
+template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) pd_batch_tables(const __grid_constant__ TablesParams p) {
-  __shared__ Sums warp_sums[kThreads / 32];
-  __shared__ int owner[kTokens], o_start[kTokens], o_ctx[kTokens], warp_max[kThreads / 32];
+  constexpr int kWarps = kThreads / 32, kTokens = kThreads * kRun;
+  __shared__ Sums warp_sums[kWarps];
+  __shared__ int warp_max[kWarps];
+  // by token: the request noted there (or -1), its start, cached tokens, pages before it
+  __shared__ __align__(16) int owner[kTokens];
+  __shared__ int o_start[kTokens], o_ctx[kTokens];
   __shared__ unsigned int o_off[kTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool requests = blockIdx.x == 0;
   const int t0 = requests ? 0 : (int)(blockIdx.x - 1) * kTokens;
   const int t1 = requests ? 0 : min(p.T - t0, kTokens) + t0;
-  owner[tid] = -1;
+  *reinterpret_cast<int4 *>(owner + kRun * tid) = make_int4(-1, -1, -1, -1);
   // the lengths may be the previous kernel's outputs
   grid_dependency_wait();
   grid_dependents_launch();
-  const unsigned int T = (unsigned)p.T, P = (unsigned)p.P;
-  const unsigned int cap = (unsigned)p.bt_width * P;  // tokens a table row can address
+  constexpr int kRequests = kThreads * kPer;  // of a pass
+  const unsigned int T = (unsigned)p.T;
+  const unsigned int cap = (unsigned)p.bt_width * (unsigned)p.P;  // tokens a table row can address
   unsigned int bad = 0;
+  const int cursor = p.cursor ? __ldg(p.cursor) : 0;
   Sums carry = {0, 0};
   // (a token block stops at the first pass that starts past its tokens)
-  for (int base = 0; base < p.S && (requests || (int)carry.tok < t1); base += kThreads) {
-    const int s = base + tid;
-    int c_in = 0, q_in = 0;
-    if (s < p.S) {
-      c_in = __ldg(p.context + s);
-      q_in = __ldg(p.query + s);
+  for (int base = 0; base < p.S && (requests || (int)carry.tok < t1); base += kRequests) {
+    const int s0 = base + kPer * tid;
+    int c_in[kPer], q_in[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      c_in[i] = s0 + i < p.S ? __ldg(p.context + s0 + i) : 0;
+      q_in[i] = s0 + i < p.S ? __ldg(p.query + s0 + i) : 0;
     }
-    const unsigned int c = min((unsigned)max(c_in, 0), cap), q = min((unsigned)max(q_in, 0), T);
-    const unsigned int have = cdiv_u(c, P);
-    Sums x = {q, cdiv_u(min(c + q, cap), P) - have};
+    auto ctx = [&](int i) { return min((unsigned)max(c_in[i], 0), cap); };
+    auto want = [&](int i) {
+      const unsigned int c = ctx(i), q = min((unsigned)max(q_in[i], 0), T);
+      return Sums{q, cdiv_p(min(c + q, cap), p) - cdiv_p(c, p)};
+    };
+    Sums own = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) own = add(own, want(i), T);
+    Sums x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const Sums y = {__shfl_up_sync(0xffffffffu, x.tok, o), __shfl_up_sync(0xffffffffu, x.pages, o)};
       if (lane >= o) x = add(y, x, T);
     }
     if (lane == 31) warp_sums[warp] = x;
+    // the sums before this thread's first request
+    Sums run = {__shfl_up_sync(0xffffffffu, x.tok, 1), __shfl_up_sync(0xffffffffu, x.pages, 1)};
+    if (lane == 0) run = {0, 0};
     __syncthreads();
-    Sums w = warp_sums[lane];  // 32 warps
+    Sums before = carry;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const Sums y = {__shfl_up_sync(0xffffffffu, w.tok, o), __shfl_up_sync(0xffffffffu, w.pages, o)};
-      if (lane >= o) w = add(y, w, T);
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) before = carry;
+      carry = add(carry, warp_sums[w], T);
     }
-    const Sums before = {__shfl_sync(0xffffffffu, w.tok, max(warp - 1, 0)),
-                         __shfl_sync(0xffffffffu, w.pages, max(warp - 1, 0))};
-    Sums end = warp ? add(before, x, T) : x;
-    end = add(carry, end, T);
-    // start: the sums before this request
-    Sums start = {__shfl_up_sync(0xffffffffu, end.tok, 1), __shfl_up_sync(0xffffffffu, end.pages, 1)};
-    if (lane == 0) start = warp ? add(carry, before, T) : carry;
-    const unsigned int len = min(c + (end.tok - start.tok), cap);
-    if (s < p.S) {
+    run = add(before, run, T);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int s = s0 + i;
+      const Sums start = run, end = add(run, want(i), T);
+      run = end;
+      if (s >= p.S) break;
+      const unsigned int c = ctx(i), len = min(c + (end.tok - start.tok), cap);
       if (requests) {
         p.query_start[s] = (int)start.tok;
         p.seq_lens[s] = (int)len;
-        if (c_in < 0 || q_in < 0 || (unsigned)max(c_in, 0) > cap || c + (end.tok - start.tok) > cap)
+        if (c_in[i] < 0 || q_in[i] < 0 || (unsigned)max(c_in[i], 0) > cap ||
+            c + (end.tok - start.tok) > cap)
           bad |= PD_DEV_BAD_SEQLEN;
-        if ((unsigned)max(q_in, 0) != end.tok - start.tok) bad |= PD_DEV_BAD_QSTART;
+        if ((unsigned)max(q_in[i], 0) != end.tok - start.tok) bad |= PD_DEV_BAD_QSTART;
         if (s == p.S - 1) p.query_start[p.S] = (int)end.tok;
         // the last request with tokens before T closes the pages' sum (those
         // after it take no token and no page)
         if (p.next_cursor && start.tok < T && (s == p.S - 1 || end.tok == T)) {
-          const int64_t n = (int64_t)(p.cursor ? __ldg(p.cursor) : 0) +
-                            (p.free_pages ? start.pages + (cdiv_u(len, P) - have) : 0u);
+          const int64_t n = (int64_t)cursor +
+                            (p.free_pages ? start.pages + (cdiv_p(len, p) - cdiv_p(c, p)) : 0u);
           *p.next_cursor = (int)min(n, (int64_t)INT32_MAX);
         }
       } else if (end.tok > start.tok && (int)end.tok > t0 && (int)start.tok < t1) {
@@ -119,65 +164,85 @@ __global__ void __launch_bounds__(kThreads) pd_batch_tables(const __grid_constan
         o_off[at] = start.pages;
       }
     }
-    const Sums all = {__shfl_sync(0xffffffffu, w.tok, 31), __shfl_sync(0xffffffffu, w.pages, 31)};
-    carry = add(carry, all, T);
     __syncthreads();
   }
   if (requests) {
     if (tid == 0) {
       if (p.S == 0) p.query_start[0] = 0;
-      if (p.next_cursor && (p.S == 0 || p.T == 0)) *p.next_cursor = p.cursor ? __ldg(p.cursor) : 0;
+      if (p.next_cursor && (p.S == 0 || p.T == 0)) *p.next_cursor = cursor;
     }
     if (bad) atomicOr(p.status, bad);
     return;
   }
   // ---- the tokens: the request noted last at or before each of them --------
   __syncthreads();
-  int at = owner[tid] >= 0 ? tid : -1;
+  const int4 mine = *reinterpret_cast<const int4 *>(owner + kRun * tid);
+  int at = mine.w >= 0   ? kRun * tid + 3
+           : mine.z >= 0 ? kRun * tid + 2
+           : mine.y >= 0 ? kRun * tid + 1
+           : mine.x >= 0 ? kRun * tid
+                         : -1;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, at, o);
     if (lane >= o) at = max(at, y);
   }
   if (lane == 31) warp_max[warp] = at;
+  at = __shfl_up_sync(0xffffffffu, at, 1);  // before this thread's first token
+  if (lane == 0) at = -1;
   __syncthreads();
-  int m = lane < warp ? warp_max[lane] : -1;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  at = max(at, m);
-  const int t = t0 + tid;
-  if (t >= t1) return;
-  int pos = 0, slot = -1;
-  // (carry.tok: the tokens of all requests, or of enough of them to pass t1)
-  if (t < (int)carry.tok) {
-    const int s = owner[at];
-    const unsigned int c = (unsigned)o_ctx[at], i = (unsigned)(t - o_start[at]);
-    const unsigned int at_pos = c + i, page = at_pos / P, in = at_pos - page * P;
-    pos = (int)at_pos + (p.delta ? __ldg(p.delta + s) : 0);
-    if (at_pos < cap) {
-      const unsigned int have = cdiv_u(c, P);
-      int32_t *entry = p.table + (int64_t)s * p.bt_stride + page;
-      int id;
-      if (p.free_pages && page >= have) {
-        const int64_t f = (int64_t)__ldg(p.cursor) + (int64_t)(o_off[at] + (page - have));
-        const bool left = f >= 0 && f < p.num_free;
-        id = left ? __ldg(p.free_pages + f) : -1;
-        if (!left) bad |= PD_DEV_NO_PAGE;
-        else if ((unsigned)id >= (unsigned)p.num_pages) bad |= PD_DEV_BAD_PAGE;
-        if ((unsigned)id >= (unsigned)p.num_pages) id = -1;
-        if (in == 0) *entry = id;
-      } else {
-        id = *entry;
-        if ((unsigned)id >= (unsigned)p.num_pages) {
-          bad |= PD_DEV_BAD_PAGE;
-          id = -1;
-        }
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) at = max(at, warp_max[w]);
+  const int first = t0 + kRun * tid;
+  if (first >= t1) return;
+  // (every load of the four tokens is under way before one is used)
+  const int noted[kRun] = {mine.x, mine.y, mine.z, mine.w};
+  int pos[kRun], slot[kRun], in[kRun], id[kRun], ahead[kRun];
+  int32_t *opened[kRun];  // the table's entry of a page that the token opens
+  bool free_page[kRun], held[kRun];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int t = first + k;
+    if (noted[k] >= 0) at = kRun * tid + k;
+    // (carry.tok: the tokens of all requests, or of enough of them to pass t1)
+    const bool live = t < t1 && t < (int)carry.tok;
+    const int o = live ? at : 0;
+    const int s = live ? owner[o] : 0;
+    const unsigned int c = (unsigned)o_ctx[o], i = (unsigned)(t - o_start[o]);
+    const unsigned int at_pos = c + i, page = div_p(at_pos, p), have = cdiv_p(c, p);
+    held[k] = live && at_pos < cap;
+    free_page[k] = held[k] && p.free_pages && page >= have;
+    in[k] = (int)(at_pos - page * p.P);
+    pos[k] = live ? (int)at_pos : 0;
+    ahead[k] = live && p.delta ? __ldg(p.delta + s) : 0;
+    int32_t *entry = p.table + (int64_t)s * p.bt_stride + page;
+    opened[k] = free_page[k] && in[k] == 0 ? entry : nullptr;
+    id[k] = -1;
+    if (free_page[k]) {
+      const int64_t f = (int64_t)cursor + (int64_t)(o_off[o] + (page - have));
+      if (f >= 0 && f < p.num_free)
+        id[k] = __ldg(p.free_pages + f);
+      else {
+        bad |= PD_DEV_NO_PAGE;
+        held[k] = false;
       }
-      if (id >= 0) slot = id * p.P + (int)in;
+    } else if (held[k]) {
+      id[k] = *entry;
     }
   }
-  for (int a = 0; a < p.axes; ++a) p.positions[a * p.pos_stride + t] = pos;
-  p.slots[t] = slot;
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    if (held[k] && (unsigned)id[k] >= (unsigned)p.num_pages) {
+      bad |= PD_DEV_BAD_PAGE;
+      id[k] = -1;
+    }
+    if (opened[k]) *opened[k] = id[k];
+    slot[k] = id[k] >= 0 ? id[k] * p.P + in[k] : -1;
+    pos[k] += ahead[k];
+  }
+  for (int a = 0; a < p.axes; ++a) store4(p.positions + a * p.pos_stride + first, pos, t1 - first);
+  store4(p.slots + first, slot, t1 - first);
   if (bad) atomicOr(p.status, bad);
 }
 
@@ -220,7 +285,7 @@ extern "C" PD_API int paged_batch_tables(
     return PD_EINVAL;
   if (context_lens->ndim != 1 || slot_mapping->ndim != 1) return PD_EINVAL;
   const int64_t S = context_lens->shape[0], T = slot_mapping->shape[0];
-  if (S < 0 || S > INT32_MAX - kThreads || T < 0 || T > INT32_MAX - kTokens) return PD_EINVAL;
+  if (S < 0 || S > INT32_MAX - kMany * kPerMany || T < 0 || T > INT32_MAX - kMany * kRun) return PD_EINVAL;
   int rc;
   if ((rc = check_vec(context_lens, S)) != PD_OK) return rc;
   if ((rc = check_vec(query_lens, S)) != PD_OK) return rc;
@@ -295,19 +360,26 @@ extern "C" PD_API int paged_batch_tables(
   p.S = (int)S;
   p.T = (int)T;
   p.P = page_size;
+  int lg = 0;
+  while (((int64_t)1 << lg) < page_size) ++lg;
+  p.shift = 31 + lg;
+  p.magic = ((1ull << p.shift) + page_size - 1) / page_size;
   p.num_pages = num_pages;
   p.status = status;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(1 + (T + kTokens - 1) / kTokens));
-  cfg.blockDim = dim3(kThreads);
+  const int threads = S <= kFew ? kFew : kMany, tokens = threads * kRun;
+  cfg.gridDim = dim3((unsigned)(1 + (T + tokens - 1) / tokens));
+  cfg.blockDim = dim3(threads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, pd_batch_tables, p) != cudaSuccess) {
+  const cudaError_t e = S <= kFew ? cudaLaunchKernelEx(&cfg, pd_batch_tables<kFew, 1>, p)
+                                  : cudaLaunchKernelEx(&cfg, pd_batch_tables<kMany, kPerMany>, p);
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return PD_ECUDA;
   }

@@ -13,6 +13,7 @@ import torch
 
 import paged_split_kv_02_gb300 as pd
 from oracle import rope_cache as R
+from oracle.rope_axes import rope_axes
 from paged_split_kv_02_gb300 import workloads as W
 
 pytestmark = pytest.mark.gpu
@@ -67,7 +68,7 @@ def _rope(c, pos, axis, inplace=False):
     _call(g, torch.from_numpy(pos).cuda(), axis, q_out)
     torch.cuda.synchronize()
     table = c.cos_sin.double().numpy()
-    qr, kr = (R.rope_axes(x.double().numpy(), pos, table, axis, c.rot_dim, c.is_neox)
+    qr, kr = (rope_axes(x.double().numpy(), pos, table, axis, c.rot_dim, c.is_neox)
               for x in (c.q, c.k))
     _near(q_out, qr, c.q.double().numpy(), c.rot_dim, c.is_neox, c.dtype, "q")
     by = (lambda x: x) if c.layout == W.NHD else (lambda x: x.permute(0, 2, 1, 3))
@@ -160,7 +161,7 @@ def test_rope_axes_report_positions_and_slots():
     _call(g, torch.from_numpy(pos).cuda(), axis, q_out)
     torch.cuda.synchronize()
     assert pd.paged_decode_device_status(reset=True) == pd.DEV_BAD_POSITION | pd.DEV_BAD_SLOT
-    ref = R.rope_axes(c.q.double().numpy(), pos.clip(0, 99), c.cos_sin.double().numpy(), axis, 64, True)
+    ref = rope_axes(c.q.double().numpy(), pos.clip(0, 99), c.cos_sin.double().numpy(), axis, 64, True)
     _near(q_out, ref, c.q.double().numpy(), 64, True, torch.float16, "q")
 
 
@@ -176,11 +177,11 @@ def test_rope_axes_captured_and_on_another_stream():
     st.synchronize()
     table = c.cos_sin.double().numpy()
     x = c.q.double().numpy()
-    _near(q_out, R.rope_axes(x, pos, table, axis, 128, True), x, 128, True, c.dtype, "q")
+    _near(q_out, rope_axes(x, pos, table, axis, 128, True), x, 128, True, c.dtype, "q")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         _call(g, p, axis, q_out)
     p.copy_(torch.from_numpy(pos[::-1].copy()))
     graph.replay()
     torch.cuda.synchronize()
-    _near(q_out, R.rope_axes(x, pos[::-1], table, axis, 128, True), x, 128, True, c.dtype, "q")
+    _near(q_out, rope_axes(x, pos[::-1], table, axis, 128, True), x, 128, True, c.dtype, "q")

@@ -7,6 +7,7 @@ import torch
 
 import paged_split_kv_02_gb300 as pd
 from oracle import rope_cache as R
+from oracle.rope_axes import rope_axes
 from paged_split_kv_02_gb300 import workloads as W
 
 PASSES = -8  # a call that passes every check reaches the missing device
@@ -70,9 +71,9 @@ def test_oracle_of_one_position():
     pos = c.positions.numpy()
     for neox in (True, False):
         want = R.rope(x, pos, table, 32, neox)
-        assert np.array_equal(R.rope_axes(x, np.stack([pos, pos]), table, [0, 1] * 8, 32, neox), want)
+        assert np.array_equal(rope_axes(x, np.stack([pos, pos]), table, [0, 1] * 8, 32, neox), want)
         # a pair turned by the other axis's position alone
-        two = R.rope_axes(x, np.stack([pos, pos * 0]), table, [1] * 15 + [0], 32, neox)
+        two = rope_axes(x, np.stack([pos, pos * 0]), table, [1] * 15 + [0], 32, neox)
         a, b = R.pair_index(32, neox)
         same = np.ones(64, dtype=bool)
         same[[a[15], b[15]]] = False
