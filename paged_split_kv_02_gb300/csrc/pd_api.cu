@@ -91,14 +91,7 @@ MapEntry g_maps[kMapCache];
 int g_map_next = 0;
 std::mutex g_map_mu;
 
-// One copy moves one 16-token block of one kv head of one page, all D dims:
-// dims (innermost first) = d within a 128-byte row (64), token, 128-byte row
-// of the head dim (D/64, stride 128 B), kv head, page.  The copy lands as
-// [D/64][16 tokens][128 B] with the 128-byte swizzle, the layout the
-// consumers' ldmatrix reads.  A TMA copy has a fixed per-copy cost (2 KiB
-// boxes stream at ~33 GB/s per SM on GB300); one copy per block is 32*D
-// bytes (4 KiB at D = 128, 16 KiB at D = 512).
-int encode_cache_map(const pd_tensor *t, int layout, CUtensorMap *out, bool one_box = false) {
+bool have_encode() {
   std::call_once(g_encode_once, [] {
     cudaDriverEntryPointQueryResult q;
     void *fn = nullptr;
@@ -109,7 +102,18 @@ int encode_cache_map(const pd_tensor *t, int layout, CUtensorMap *out, bool one_
     else
       cudaGetLastError();
   });
-  if (!g_encode) return PD_ECUDA;
+  return g_encode != nullptr;
+}
+
+// One copy moves one 16-token block of one kv head of one page, all D dims:
+// dims (innermost first) = d within a 128-byte row (64), token, 128-byte row
+// of the head dim (D/64, stride 128 B), kv head, page.  The copy lands as
+// [D/64][16 tokens][128 B] with the 128-byte swizzle, the layout the
+// consumers' ldmatrix reads.  A TMA copy has a fixed per-copy cost (2 KiB
+// boxes stream at ~33 GB/s per SM on GB300); one copy per block is 32*D
+// bytes (4 KiB at D = 128, 16 KiB at D = 512).
+int encode_cache_map(const pd_tensor *t, int layout, CUtensorMap *out, bool one_box = false) {
+  if (!have_encode()) return PD_ECUDA;
   int dev = 0;
   cudaGetDevice(&dev);
   // NHD [NB, P, Hkv, D]; HND [NB, Hkv, P, D]
@@ -701,6 +705,19 @@ int check_rows(const pd_tensor *t, int64_t rows, int Hq, int D) {
 
 int cache_tensor_map(const pd_tensor *t, int layout, CUtensorMap *out, bool one_box) {
   return encode_cache_map(t, layout, out, one_box);
+}
+
+int query_tensor_map(const pd_tensor *q, int G, CUtensorMap *out) {
+  if (!have_encode()) return PD_ECUDA;
+  cuuint64_t dims[4] = {64, (cuuint64_t)q->shape[1], (cuuint64_t)q->shape[0], 2};
+  cuuint64_t strides[3] = {(cuuint64_t)q->stride[1] * 2, (cuuint64_t)q->stride[0] * 2, 128};  // bytes
+  cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)(kTpRows / G), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, q->data, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PD_OK : PD_EALIGN;
 }
 
 }  // namespace pd

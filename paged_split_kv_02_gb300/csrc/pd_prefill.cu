@@ -323,6 +323,29 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   p.pf_groups = info->num_split_tiles;
   p.pf_slots = info->num_slots;
 
+  // A window with sinks at head size 128: the kernel that runs tile after tile,
+  // unless a tile is split, its rows are no box of q (heads to a kv head not a
+  // power of two up to 128) or TMA does not take q's strides.
+  if (sh.path == 5 && p.sinks > 0 && info->num_split_tiles == 0 && p.G <= kTpRows &&
+      (p.G & (p.G - 1)) == 0 && info->num_items * num_kv_heads <= 1 << 30 &&
+      q->stride[0] > 0 && q->stride[1] > 0) {
+    CUtensorMap tq;
+    if (query_tensor_map(q, p.G, &tq) == PD_OK) {
+      p.num_items = (int)info->num_items;
+      Launch w{};
+      w.grid = dim3((unsigned)std::min<int64_t>(num_sms, info->num_items * num_kv_heads));
+      w.block = dim3(kTpThreads);
+      p.NS = std::min(8, (kSmemLimit - smem_bytes_wp(0)) / (kStageBytes + 16));
+      w.smem = smem_bytes_wp(p.NS);
+      if (launch_window_prefill(q->dtype == PD_BF16, tk, tv, tq, p, w,
+                                static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return PD_ECUDA;
+      }
+      return PD_OK;
+    }
+  }
+
   Launch l;
   l.grid = dim3((unsigned)info->num_items, (unsigned)num_kv_heads, 1);
   l.block = dim3(sh.threads, 1, 1);
