@@ -709,7 +709,8 @@ int cache_tensor_map(const pd_tensor *t, int layout, CUtensorMap *out, bool one_
 
 int query_tensor_map(const pd_tensor *q, int G, CUtensorMap *out) {
   if (!have_encode()) return PD_ECUDA;
-  cuuint64_t dims[4] = {64, (cuuint64_t)q->shape[1], (cuuint64_t)q->shape[0], 2};
+  cuuint64_t dims[4] = {64, (cuuint64_t)q->shape[1], (cuuint64_t)q->shape[0],
+                        (cuuint64_t)(q->shape[2] / 64)};
   cuuint64_t strides[3] = {(cuuint64_t)q->stride[1] * 2, (cuuint64_t)q->stride[0] * 2, 128};  // bytes
   cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)(kTpRows / G), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};

@@ -188,12 +188,13 @@ inline int64_t epilogue_bytes_tp(int D, int NS) {
   return (int64_t)NS * kStageBytes + 2LL * kTpRows * D * 2;
 }
 
-// The window prefill kernel (pd_window_prefill.cuh, head size 128): ring + both
-// halves' Q + barriers + flags and the tensor-memory address + two item slots
+// The window prefill kernel (pd_window_prefill.cuh, head sizes 64 and 128):
+// ring of 64-key stages + both halves' Q + barriers + flags and the tensor-memory address + two item slots
 // + staged page ids.
 constexpr int kWpBarriers = 18;
-inline int smem_bytes_wp(int NS) {
-  return kSmemAlign + NS * (kStageBytes + 16) + 2 * kTpRows * 128 * 2 + kWpBarriers * 8 + 16 + 64 +
+constexpr int wp_stage_bytes(int D) { return 64 * 2 * D * 2; }
+inline int smem_bytes_wp(int D, int NS) {
+  return kSmemAlign + NS * (wp_stage_bytes(D) + 16) + 2 * kTpRows * D * 2 + kWpBarriers * 8 + 16 + 64 +
          4 * kTpBlockIds;
 }
 
@@ -221,11 +222,14 @@ cudaError_t launch_mma(int D, bool bf16, int path, const CUtensorMap &tk, const 
                        const Params &p, const Launch &l, cudaStream_t stream);
 
 // The window prefill kernel, with Q's tensor map (dims: 64 of a row, q head,
-// token row, half of the row; a box of one kv head's q heads by as many tokens
+// token row, 64-dim part of the row; a box of one kv head's q heads by as many tokens
 // as make 128 packed rows).
-cudaError_t launch_window_prefill(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv,
-                                  const CUtensorMap &tq, const Params &p, const Launch &l,
-                                  cudaStream_t stream);
+cudaError_t launch_window_prefill_d64(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv,
+                                      const CUtensorMap &tq, const Params &p, const Launch &l,
+                                      cudaStream_t stream);
+cudaError_t launch_window_prefill_d128(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv,
+                                       const CUtensorMap &tq, const Params &p, const Launch &l,
+                                       cudaStream_t stream);
 
 // The calls behind the public entry points, with the sinks beside the window
 // (0: none; the entry points without sinks).
@@ -259,7 +263,7 @@ int check_rows(const pd_tensor *t, int64_t rows, int Hq, int D);
 // one_box: a copy lands one 64-dim box of a 16-key block instead of all of
 // them (the tensor-memory prefill's K, landed box-major).
 int cache_tensor_map(const pd_tensor *t, int layout, CUtensorMap *out, bool one_box = false);
-// The tensor map of q [T, Hq, 128] for the window prefill kernel, G q heads to
+// The tensor map of q [T, Hq, D] for the window prefill kernel, G q heads to
 // a kv head; an error where TMA does not take the strides.
 int query_tensor_map(const pd_tensor *q, int G, CUtensorMap *out);
 

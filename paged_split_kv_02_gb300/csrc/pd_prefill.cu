@@ -40,9 +40,26 @@ struct Tile {
   int32_t nseg;
 };
 
+// Can a half of a tile be a box of q: G q heads to a kv head by 128 / G tokens.
+bool rows_are_a_box(int G) { return G <= kTpRows && (G & (G - 1)) == 0; }
+
+// Tile rows of a plan over a window with sinks: at head size 64 the tile kernel
+// too, on tiles of 256 rows that are never split, once they fill half the SMs
+// (with fewer, 64-row tiles on mma.sync, which may be split).
+int window_tile_rows(const int32_t *query_start, int S, int Hq, int Hkv, int D, int num_sms) {
+  if (D != 64 || S <= 0 || !query_start || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
+      !rows_are_a_box(Hq / Hkv))
+    return tile_rows_for(D);
+  int64_t tiles = 0;
+  for (int s = 0; s < S; ++s)
+    tiles += cdiv(std::max<int64_t>((int64_t)query_start[s + 1] - query_start[s], 0) * (Hq / Hkv),
+                  PD_PREFILL_TILE_ROWS_D128);
+  return 2 * tiles * Hkv >= num_sms ? PD_PREFILL_TILE_ROWS_D128 : tile_rows_for(D);
+}
+
 // The tiles of a plan and their segments.
 int plan_tiles(const int32_t *query_start, const int32_t *seq_lens, int S, int Hq, int Hkv,
-               int rows, int window, int sinks, int target, std::vector<Tile> *tiles,
+               int rows, bool split, int window, int sinks, int target, std::vector<Tile> *tiles,
                pd_prefill_plan_info *info) {
   if (S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || window < 0 || sinks < 0 || target <= 0 ||
       rows <= 0)
@@ -80,7 +97,7 @@ int plan_tiles(const int32_t *query_start, const int32_t *seq_lens, int S, int H
   const double load = std::max((double)Hkv * (double)total / target, (double)kMinSegmentBlocks);
   int32_t n_split = 0, n_slots = 0;
   for (Tile &t : *tiles) {
-    if ((double)t.blocks > load) {
+    if (split && (double)t.blocks > load) {
       const int64_t by_load = (int64_t)std::ceil((double)t.blocks / load);
       const int64_t by_floor = t.blocks / kMinSegmentBlocks;
       t.nseg = (int32_t)std::max<int64_t>(1, std::min<int64_t>({by_load, by_floor, kMaxSegments}));
@@ -171,8 +188,12 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
     if (rc != PD_OK) return rc;
   }
   std::vector<Tile> tiles;
-  int rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads,
-                      tile_rows_for(head_size), window, sinks, num_sms, &tiles, info);
+  const int rows = sinks > 0 && window > 0
+                       ? window_tile_rows(query_start, num_seqs, num_q_heads, num_kv_heads, head_size,
+                                          num_sms)
+                       : tile_rows_for(head_size);
+  int rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, rows,
+                      rows == tile_rows_for(head_size), window, sinks, num_sms, &tiles, info);
   if (rc != PD_OK) return rc;
   if (!items) return PD_OK;  // a size query
   if (capacity < info->num_items) return PD_EINVAL;
@@ -209,7 +230,9 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
     return PD_EINVAL;
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return PD_EINVAL;
   if (!head_size_ok(head_size)) return PD_EHEAD;
-  const int rows = tile_rows_for(head_size);
+  // (head size 64: a plan of 256-row tiles is for the tile kernel)
+  const bool tiles64 = head_size == 64 && info->tile_rows == PD_PREFILL_TILE_ROWS_D128;
+  const int rows = tiles64 ? PD_PREFILL_TILE_ROWS_D128 : tile_rows_for(head_size);
   if (page_size <= 0 || page_size % kBlockKeys != 0 || window < 0 || sinks < 0 ||
       !std::isfinite(scale))
     return PD_EINVAL;
@@ -245,8 +268,10 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
     if (k_cache->shape[i] != v_cache->shape[i]) return PD_EINVAL;
   // the plan: its work list on the device, its sizes from paged_prefill_plan
   if (info->num_items < 0 || info->num_items > INT32_MAX || info->tile_rows != rows ||
-      info->num_split_tiles < 0 || info->num_slots < 0 || info->max_segments != kMaxSegments)
+      info->num_split_tiles < 0 || info->num_slots < 0 || info->max_segments != kMaxSegments ||
+      (tiles64 && (info->num_split_tiles != 0 || !rows_are_a_box(num_q_heads / num_kv_heads))))
     return PD_EINVAL;
+  if (tiles64 && T > 0 && (q->stride[0] == 0 || q->stride[1] == 0)) return PD_EALIGN;
   if (work->ndim != 2 || work->shape[0] != info->num_items || work->shape[1] != 8 ||
       work->stride[1] != 1 || work->stride[0] != 8 || (info->num_items > 0 && !work->data) ||
       (reinterpret_cast<uintptr_t>(work->data) & 15u) != 0)
@@ -323,27 +348,32 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   p.pf_groups = info->num_split_tiles;
   p.pf_slots = info->num_slots;
 
-  // A window with sinks at head size 128: the kernel that runs tile after tile,
-  // unless a tile is split, its rows are no box of q (heads to a kv head not a
-  // power of two up to 128) or TMA does not take q's strides.
-  if (sh.path == 5 && p.sinks > 0 && info->num_split_tiles == 0 && p.G <= kTpRows &&
-      (p.G & (p.G - 1)) == 0 && info->num_items * num_kv_heads <= 1 << 30 &&
-      q->stride[0] > 0 && q->stride[1] > 0) {
+  // A window with sinks at head size 128 without split tiles, or a plan of
+  // 256-row tiles at head size 64: the kernel that runs tile after tile.  (At
+  // 128 where q's rows are no box, heads to a kv head not a power of two up to
+  // 128 or a stride of 0, a CTA per tile.)
+  const bool tiles128 = sh.path == 5 && p.sinks > 0 && info->num_split_tiles == 0 &&
+                        rows_are_a_box(p.G) && q->stride[0] > 0 && q->stride[1] > 0;
+  if (tiles64 || tiles128) {
+    if (info->num_items * num_kv_heads > 1 << 30) return PD_EINVAL;
     CUtensorMap tq;
-    if (query_tensor_map(q, p.G, &tq) == PD_OK) {
-      p.num_items = (int)info->num_items;
-      Launch w{};
-      w.grid = dim3((unsigned)std::min<int64_t>(num_sms, info->num_items * num_kv_heads));
-      w.block = dim3(kTpThreads);
-      p.NS = std::min(8, (kSmemLimit - smem_bytes_wp(0)) / (kStageBytes + 16));
-      w.smem = smem_bytes_wp(p.NS);
-      if (launch_window_prefill(q->dtype == PD_BF16, tk, tv, tq, p, w,
-                                static_cast<cudaStream_t>(stream)) != cudaSuccess) {
-        cudaGetLastError();
-        return PD_ECUDA;
-      }
-      return PD_OK;
+    if ((rc = query_tensor_map(q, p.G, &tq)) != PD_OK) return rc;
+    p.num_items = (int)info->num_items;
+    p.window = window > 0 ? window : INT32_MAX;
+    p.sinks = sinks;
+    p.NS = std::min(8, (kSmemLimit - smem_bytes_wp(head_size, 0)) / (wp_stage_bytes(head_size) + 16));
+    Launch w{};
+    w.grid = dim3((unsigned)std::min<int64_t>(num_sms, info->num_items * num_kv_heads));
+    w.block = dim3(kTpThreads);
+    w.smem = smem_bytes_wp(head_size, p.NS);
+    const cudaError_t e =
+        (tiles64 ? launch_window_prefill_d64 : launch_window_prefill_d128)(
+            q->dtype == PD_BF16, tk, tv, tq, p, w, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return PD_ECUDA;
     }
+    return PD_OK;
   }
 
   Launch l;

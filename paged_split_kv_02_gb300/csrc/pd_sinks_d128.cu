@@ -17,11 +17,11 @@ cudaError_t launch_sinks_d128(bool bf16, int path, const CUtensorMap &tk, const 
               : launch_mma_t<128, false, false, false, false, false, true>(tk, tv, p, l, stream);
 }
 
-cudaError_t launch_window_prefill(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv,
-                                  const CUtensorMap &tq, const Params &p, const Launch &l,
-                                  cudaStream_t stream) {
-  return bf16 ? launch_window_prefill_t<true>(tk, tv, tq, p, l, stream)
-              : launch_window_prefill_t<false>(tk, tv, tq, p, l, stream);
+cudaError_t launch_window_prefill_d128(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv,
+                                        const CUtensorMap &tq, const Params &p, const Launch &l,
+                                        cudaStream_t stream) {
+  return bf16 ? launch_window_prefill_t<128, true>(tk, tv, tq, p, l, stream)
+              : launch_window_prefill_t<128, false>(tk, tv, tq, p, l, stream);
 }
 
 }  // namespace pd

@@ -1,9 +1,9 @@
-// Prefill over a window with sinks at head size 128, tile after tile.
+// Prefill over a window with sinks at head sizes 64 and 128, tile after tile.
 //
 // The tiles, stages, products and softmax are those of pd_kernel.cuh's
 // tensor-memory prefill (256 packed rows as two halves that share every K/V
 // stage; S, P and O in tensor memory).  A window makes a tile short: at 1024
-// keys 17 stages of ~1.1 us, beside ~11 us of starting the CTA, reading the
+// keys 17 stages of 64 keys, ~1.1 us each, beside ~11 us of starting the CTA, reading the
 // work item and lengths, loading Q, filling the ring and storing O.  Here a
 // CTA keeps its tensor memory and ring and runs through a list of tiles (one
 // CTA per SM, item i of CTA b is the list's b + i G, every kv head of an
@@ -27,14 +27,16 @@
 
 namespace pd {
 
-template <bool BF16>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kTpThreads, 1)
     pd_window_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ Params p) {
-  constexpr int D = 128, KS = D / 16, TB = 4, SC = TB * kBlockKeys, NBOX = D / 64;
-  constexpr int BLOCK_BYTES = kBlockKeys * D * 2, STAGE = kStageBytes, BIDS = kTpBlockIds;
+  constexpr int KS = D / 16, TB = 4, SC = TB * kBlockKeys, NBOX = D / 64;
+  constexpr int BLOCK_BYTES = kBlockKeys * D * 2, STAGE = wp_stage_bytes(D), BIDS = kTpBlockIds;
   constexpr int kHalf = kTpRows * D * 2;  // bytes of a half's Q
+  constexpr int kCols = 512;              // tensor memory: S / P 4 x 64 columns, O 2 x D
   static_assert(2 * TB * BLOCK_BYTES == STAGE, "K and V of 64 keys");
+  static_assert(D == 64 || D == 128, "O of two halves beside S");
   using tag = std::integral_constant<bool, BF16>;
   using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
 
@@ -72,13 +74,13 @@ __global__ void __launch_bounds__(kTpThreads, 1)
     prefetch_tensormap(&tmV);
     prefetch_tensormap(&tmQ);
   }
-  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), tp_tmem_cols(D));
+  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base =
       __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
-  const uint32_t tS = tmem_base + tp_s_col(D), tO = tmem_base + tp_o_col(D);
+  const uint32_t tS = tmem_base, tO = tmem_base + 4 * SC;
   grid_dependency_wait();
 
   const int lg_g = __ffs(p.G) - 1;  // G is a power of two here
@@ -538,8 +540,9 @@ __global__ void __launch_bounds__(kTpThreads, 1)
         // before its own PV MMAs (the other half's writes are the same zeros)
         if (!fast) {
           unsigned char *vb = ring + (g % NS) * STAGE + TB * BLOCK_BYTES;
-          const int v = lane & 15;  // a key's 256 bytes by 16 threads
-          for (int c = 2 * (warp & 3) + (lane >> 4); c < nbt * kBlockKeys; c += 8) {
+          constexpr int kV = D / 8;  // threads to a key's bytes
+          const int v = lane % kV;
+          for (int c = (32 * (warp & 3) + lane) / kV; c < nbt * kBlockKeys; c += 128 / kV) {
             const int k = block_key(c >> 4) + (c & 15);
             if (!(k < t.u_hi && (k >= t.u_lo || k < p.sinks)))
               *reinterpret_cast<uint4 *>(vb + (c >> 4) * BLOCK_BYTES + (v >> 3) * 2048 + (c & 15) * 128 +
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, tp_tmem_cols(D));
+    tmem_dealloc(tmem_base, kCols);
   }
   if (blockIdx.x == 0) {
     // rows at and past the last request's end (padding) see no key: zeros
@@ -640,10 +643,10 @@ __global__ void __launch_bounds__(kTpThreads, 1)
   }
 }
 
-template <bool BF16>
+template <int D, bool BF16>
 cudaError_t launch_window_prefill_t(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq,
                                     const Params &p, const Launch &l, cudaStream_t stream) {
-  auto kern = pd_window_prefill<BF16>;
+  auto kern = pd_window_prefill<D, BF16>;
   static int configured_smem[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;

@@ -1,8 +1,8 @@
-"""Prefill over a window with sinks at head size 128, tile after tile (plans
-without split tiles), against the fp64 oracle.
+"""Prefill over a window with sinks at head sizes 64 and 128, tile after tile
+(plans of 256-row tiles without a split), against the fp64 oracle.
 
 Bounds: those of gpu_helpers.  Keys that no row sees are NaN, pages without a
-visible key -1 in the table.  A plan for one SM splits no tile."""
+visible key -1 in the table.  A plan for one SM has such tiles."""
 
 import dataclasses
 
@@ -34,8 +34,10 @@ def _clean():
 def _plan(case, sinks, num_sms=1):
     plan = pd.paged_prefill_plan_sinks(case.query_start_host, case.seq_lens_host, case.num_q_heads,
                                        case.num_kv_heads, case.head_size, case.window, sinks, num_sms)
+    G = case.num_q_heads // case.num_kv_heads
     if num_sms == 1:
         assert plan[1].num_split_tiles == 0
+        assert plan[1].tile_rows == (64 if case.head_size == 64 and G & (G - 1) else 256)
     return plan
 
 
@@ -58,44 +60,54 @@ def _case(seed, q_lens, contexts, **kw):
     return W.make_prefill_case("tiles", seed=seed, q_lens=q_lens, contexts=contexts, **base)
 
 
+both = pytest.mark.parametrize("D", [64, 128])
+
+
+@both
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("window,sinks", [(200, 4), (17, 40), (64, 64), (1, 16), (1000, 130)])
-def test_tiles_types_and_windows(dtype, window, sinks):
+def test_tiles_types_and_windows(dtype, window, sinks, D):
     _run(_case(window, [300, 1, 77, 0, 160, 64], [0, 700, 333, 50, 16, 2000], dtype=dtype, window=window,
-               pad_tokens=3), sinks)
+               pad_tokens=3, head_size=D), sinks)
 
 
+@both
 @pytest.mark.parametrize("heads", [(2, 2), (4, 2), (32, 8), (16, 2), (32, 1), (6, 2), (20, 4), (128, 1), (256, 2)])
-def test_tiles_heads(heads):
+def test_tiles_heads(heads, D):
     """1 .. 128 q heads to a kv head; 3 and 5, whose rows are no box of q, run
     tile by tile."""
-    _run(_case(heads[0], [70, 9, 130], [150, 0, 600], num_q_heads=heads[0], num_kv_heads=heads[1]), 20)
+    _run(_case(heads[0], [70, 9, 130], [150, 0, 600], num_q_heads=heads[0], num_kv_heads=heads[1],
+               head_size=D), 20)
 
 
-def test_tiles_many_to_a_cta():
+@both
+def test_tiles_many_to_a_cta(D):
     """Some eight rounds over the SMs, of tiles of one to ten stages."""
     g = np.random.default_rng(1)
     q = [int(x) for x in g.integers(1, 900, 24)]
     c = [int(x) for x in g.integers(0, 1500, 24)]
-    _run(_case(2, q, c, num_q_heads=32, num_kv_heads=8, window=500, pad_tokens=1), 7, rows=400)
+    _run(_case(2, q, c, num_q_heads=32, num_kv_heads=8, window=500, pad_tokens=1, head_size=D), 7, rows=400)
 
 
-def test_tiles_of_single_tokens():
+@both
+def test_tiles_of_single_tokens(D):
     g = np.random.default_rng(2)
     c = [int(x) for x in g.integers(0, 400, 90)]
-    _run(_case(3, [1] * 90, c, num_q_heads=32, num_kv_heads=8, window=100), 3, rows=400)
+    _run(_case(3, [1] * 90, c, num_q_heads=32, num_kv_heads=8, window=100, head_size=D), 3, rows=400)
 
 
+@both
 @pytest.mark.parametrize("layout", [W.NHD, W.HND])
 @pytest.mark.parametrize("P", [48, 784])
-def test_tiles_layouts_and_pages(layout, P):
-    _run(_case(P, [500, 33], [900, 5], layout=layout, page_size=P, window=300), 21)
+def test_tiles_layouts_and_pages(layout, P, D):
+    _run(_case(P, [500, 33], [900, 5], layout=layout, page_size=P, window=300, head_size=D), 21)
 
 
+@both
 @pytest.mark.parametrize("std,scale", [(4.0, None), (3.0, -0.09)])
-def test_tiles_large_scores(std, scale):
+def test_tiles_large_scores(std, scale, D):
     """Scores far apart and of either sign: O rescaled, stages taken again."""
-    case = _case(7, [256, 300], [500, 40], window=400, std=std)
+    case = _case(7, [256, 300], [500, 40], window=400, std=std, head_size=D)
     if scale is not None:
         case = dataclasses.replace(case, scale=scale)
     v = 2 * 2.0 ** -8 * float(case.v_cache[torch.isfinite(case.v_cache)].float().abs().max())
@@ -131,10 +143,11 @@ def test_tiles_strided_q_and_out():
     check(same, out, rows=rows, ref=O.attention(same, 4, rows))
 
 
-def test_tiles_rows_of_other_requests_hold_nan():
+@both
+def test_tiles_rows_of_other_requests_hold_nan(D):
     """A tile's box of q reads on into the next request's rows and past the
     batch: NaN and infinities there stay where they are."""
-    case = _case(9, [30, 50, 20], [400, 10, 60], pad_tokens=2)
+    case = _case(9, [30, 50, 20], [400, 10, 60], pad_tokens=2, head_size=D)
     hidden, g, want = _run(case, 5)
     for value in (float("nan"), float("inf")):
         q = g.q.clone()
@@ -144,9 +157,10 @@ def test_tiles_rows_of_other_requests_hold_nan():
         assert torch.equal(out[:30], want[:30]) and torch.equal(out[80:], want[80:])
 
 
-def test_tiles_a_request_longer_than_its_keys():
+@both
+def test_tiles_a_request_longer_than_its_keys(D):
     """Rows before the sequence's start see nothing and are zero."""
-    case = _case(10, [90, 40], [100, 0])
+    case = _case(10, [90, 40], [100, 0], head_size=D)
     g = case.to("cuda")
     lens = torch.tensor([30, 0], dtype=torch.int32)
     out = run_prefill_sinks(dataclasses.replace(g, seq_lens=lens.cuda()), 4, None, plan=_plan(case, 4))
@@ -192,8 +206,9 @@ def _status():
     return pd.paged_decode_device_status(reset=True)
 
 
-def test_tiles_report_bad_inputs():
-    case = _case(12, [200, 100, 64], [300, 0, 900], num_q_heads=32, num_kv_heads=8)
+@both
+def test_tiles_report_bad_inputs(D):
+    case = _case(12, [200, 100, 64], [300, 0, 900], num_q_heads=32, num_kv_heads=8, head_size=D)
     hidden, g, want = _run(case, 4)
     plan = _plan(case, 4)
     # work items out of range, or of a segment: skipped, the rest runs
@@ -224,3 +239,35 @@ def test_tiles_report_bad_inputs():
     run_prefill_sinks(dataclasses.replace(g, query_start=start), 4, None, plan=plan)
     assert _status() & pd.DEV_BAD_QSTART
     assert torch.equal(run_prefill_sinks(g, 4, None, plan=plan), want)
+
+
+def test_tiles_at_head_size_64_under_either_plan():
+    """Plans of 256-row and of 64-row tiles, the plan made without sinks, and
+    256-row tiles under calls without sinks or without a window."""
+    case = _case(13, [300, 77], [500, 0], head_size=64)
+    g = case.to("cuda")
+    sc = pd.prefill_scratch(2, 64, num_sms=160)
+    rows = sample_rows(case, 300)
+    wide, narrow = _plan(case, 9), _plan(case, 9, 152)
+    plain = pd.paged_prefill_plan(case.query_start_host, case.seq_lens_host, 8, 2, 64, 200, 152)
+    assert (wide[1].tile_rows, narrow[1].tile_rows, plain[1].tile_rows) == (256, 64, 64)
+    for sinks, window, plans in ((9, 200, (wide, narrow, plain)), (0, 200, (wide, plain)), (9, 0, (wide, plain))):
+        c = dataclasses.replace(case, window=window)
+        ref = O.attention(c, sinks, rows)
+        for plan in plans:
+            out = run_prefill_sinks(dataclasses.replace(g, window=window), sinks, sc, plan=plan)
+            torch.cuda.synchronize()
+            check(c, out, rows=rows, ref=ref)
+    out = pd.prefill_case(g, plan=wide)
+    torch.cuda.synchronize()
+    check(case, out, rows=rows, ref=O.attention(case, 0, rows))
+    # strides that TMA does not take are refused under this plan
+    one = dataclasses.replace(g, q=g.q[:, :1].expand(-1, 8, -1))
+    with pytest.raises(pd.PagedDecodeError, match="PD_EALIGN"):
+        run_prefill_sinks(one, 9, sc, plan=wide)
+    run_prefill_sinks(one, 9, sc, plan=narrow)
+    # the split of a 64-row plan is not for 256-row tiles
+    info = pd.PdPrefillPlanInfo.from_buffer_copy(narrow[1])
+    info.tile_rows, info.num_split_tiles = 256, 1
+    with pytest.raises(pd.PagedDecodeError, match="PD_EINVAL"):
+        run_prefill_sinks(g, 9, sc, plan=(narrow[0], info))

@@ -129,6 +129,21 @@ def test_prefill_plan_sinks():
         pd.paged_prefill_plan_sinks([0, 3, 1], [3, 3], 8, 2, 128, 16, 4, 152)
 
 
+def test_prefill_plan_rows_at_head_size_64():
+    """256-row tiles, unsplit, once they fill half the SMs; else 64-row ones."""
+    def rows(q_lens, window=100, sinks=4, Hq=8, Hkv=2, sms=152):
+        qs = [0] + list(np.cumsum(q_lens))
+        info = pd.paged_prefill_plan_sinks(qs, [9000] * len(q_lens), Hq, Hkv, 64, window, sinks, sms)[1]
+        assert info.tile_rows == 64 or info.num_split_tiles == 0
+        return info.tile_rows
+    assert rows([64 * 38]) == 256 and rows([64 * 37]) == 64        # 2 kv heads x 38 = 76 tiles
+    assert rows([1] * 38) == 256 and rows([1] * 37 + [0]) == 64
+    assert rows([64 * 37], sms=100) == 256
+    assert rows([6400], Hq=6) == 64                                # three heads to a kv head
+    assert rows([6400], sinks=0) == 64 and rows([6400], window=0) == 64
+    assert rows([]) == 64
+
+
 def test_prefill_sinks_refusals():
     c = W.make_prefill_case("refuse", seed=1, q_lens=[20, 3], contexts=[10, 0], num_q_heads=8,
                             num_kv_heads=2, window=16)
