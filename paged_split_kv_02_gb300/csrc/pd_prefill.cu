@@ -43,24 +43,11 @@ struct Tile {
 // Can a half of a tile be a box of q: G q heads to a kv head by 128 / G tokens.
 bool rows_are_a_box(int G) { return G <= kTpRows && (G & (G - 1)) == 0; }
 
-// Tile rows of a plan over a window with sinks: at head size 64 the tile kernel
-// too, on tiles of 256 rows that are never split, once they fill half the SMs
-// (with fewer, 64-row tiles on mma.sync, which may be split).
-int window_tile_rows(const int32_t *query_start, int S, int Hq, int Hkv, int D, int num_sms) {
-  if (D != 64 || S <= 0 || !query_start || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
-      !rows_are_a_box(Hq / Hkv))
-    return tile_rows_for(D);
-  int64_t tiles = 0;
-  for (int s = 0; s < S; ++s)
-    tiles += cdiv(std::max<int64_t>((int64_t)query_start[s + 1] - query_start[s], 0) * (Hq / Hkv),
-                  PD_PREFILL_TILE_ROWS_D128);
-  return 2 * tiles * Hkv >= num_sms ? PD_PREFILL_TILE_ROWS_D128 : tile_rows_for(D);
-}
-
-// The tiles of a plan and their segments.
+// The tiles of a plan and their segments (split: heavy ones are cut).  *heaviest:
+// the most blocks of a tile.
 int plan_tiles(const int32_t *query_start, const int32_t *seq_lens, int S, int Hq, int Hkv,
                int rows, bool split, int window, int sinks, int target, std::vector<Tile> *tiles,
-               pd_prefill_plan_info *info) {
+               pd_prefill_plan_info *info, int64_t *heaviest = nullptr) {
   if (S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || window < 0 || sinks < 0 || target <= 0 ||
       rows <= 0)
     return PD_EINVAL;
@@ -90,6 +77,7 @@ int plan_tiles(const int32_t *query_start, const int32_t *seq_lens, int S, int H
                              std::min(cdiv(sinks, kBlockKeys), key_begin / kBlockKeys);
       tiles->push_back({s, (int32_t)t, blocks, 1});
       total += blocks;
+      if (heaviest) *heaviest = std::max(*heaviest, blocks);
     }
   }
   // the load each resident CTA would carry with every tile on every kv head
@@ -188,12 +176,35 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
     if (rc != PD_OK) return rc;
   }
   std::vector<Tile> tiles;
-  const int rows = sinks > 0 && window > 0
-                       ? window_tile_rows(query_start, num_seqs, num_q_heads, num_kv_heads, head_size,
-                                          num_sms)
-                       : tile_rows_for(head_size);
-  int rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, rows,
-                      rows == tile_rows_for(head_size), window, sinks, num_sms, &tiles, info);
+  // Over a window with sinks the tile kernel is the rule, on whole tiles of 256
+  // rows at head sizes 64 and 128.  Few long tiles are cut instead, for a CTA
+  // per segment (at 64 in tiles of 64 rows on mma.sync): when they fill less
+  // than half the SMs (a fifth at 64) and one is heavier than 288 blocks, or 96
+  // where the merge is cheap (head size 64; requests of up to 64 rows).
+  // Measured, whole / cut, us: head size 128, window 1024, 21 % of the SMs 26 /
+  // 53, 84 % 28 / 80; 2048, 5 % 41 / 71, of 4 rows 38 / 20; 16384, 21 % 254 /
+  // 149, 42 % 254 / 217, 84 % 255 / 322; head size 64, window 1024, 11 % 24 / 23;
+  // 2048, 11 % 39 / 34, 21 % 39 / 44; 16384, 11 % 237 / 172, 21 % 240 / 252.
+  int rows = tile_rows_for(head_size);
+  int rc = PD_OK;
+  if (sinks > 0 && window > 0 && (head_size == 64 || head_size == 128) && num_q_heads > 0 &&
+      num_kv_heads > 0 && num_q_heads % num_kv_heads == 0 &&
+      rows_are_a_box(num_q_heads / num_kv_heads)) {
+    int64_t heaviest = 0;
+    rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads,
+                    PD_PREFILL_TILE_ROWS_D128, false, window, sinks, num_sms, &tiles, info,
+                    &heaviest);
+    if (rc != PD_OK) return rc;
+    const int64_t ctas = info->num_items * num_kv_heads;
+    int64_t longest = 0;
+    for (int s = 0; s < num_seqs; ++s)
+      longest = std::max<int64_t>(longest, query_start[s + 1] - query_start[s]);
+    const bool light = head_size == 64 || longest * (num_q_heads / num_kv_heads) <= 64;
+    if (heaviest <= (light ? 96 : 288) || ctas * (head_size == 64 ? 5 : 2) >= num_sms) rows = 0;
+  }
+  if (rows > 0)
+    rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, rows, true, window,
+                    sinks, num_sms, &tiles, info);
   if (rc != PD_OK) return rc;
   if (!items) return PD_OK;  // a size query
   if (capacity < info->num_items) return PD_EINVAL;

