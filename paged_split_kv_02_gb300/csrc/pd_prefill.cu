@@ -178,10 +178,10 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
   std::vector<Tile> tiles;
   // Over a window with sinks the tile kernel is the rule, on whole tiles of 256
   // rows at head sizes 64 and 128.  Few long tiles are cut instead, for a CTA
-  // per segment (at 64 in tiles of 64 rows on mma.sync): when they fill less
-  // than half the SMs (a fifth at 64) and one is heavier than 288 blocks, or 96
-  // where the merge is cheap (head size 64; requests of up to 64 rows).
-  // Measured, whole / cut, us: head size 128, window 1024, 21 % of the SMs 26 /
+  // per segment (at 64 in tiles of 64 rows on mma.sync): when one is heavier
+  // than twice the SMs' mean load (five times at 64; equal tiles on half or a
+  // fifth of the SMs) and than 288 blocks, or 96 where the merge is cheap
+  // (head size 64; requests of up to 64 rows).  Measured, whole / cut, us: head size 128, window 1024, 21 % of the SMs 26 /
   // 53, 84 % 28 / 80; 2048, 5 % 41 / 71, of 4 rows 38 / 20; 16384, 21 % 254 /
   // 149, 42 % 254 / 217, 84 % 255 / 322; head size 64, window 1024, 11 % 24 / 23;
   // 2048, 11 % 39 / 34, 21 % 39 / 44; 16384, 11 % 237 / 172, 21 % 240 / 252.
@@ -195,12 +195,13 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
                     PD_PREFILL_TILE_ROWS_D128, false, window, sinks, num_sms, &tiles, info,
                     &heaviest);
     if (rc != PD_OK) return rc;
-    const int64_t ctas = info->num_items * num_kv_heads;
     int64_t longest = 0;
     for (int s = 0; s < num_seqs; ++s)
       longest = std::max<int64_t>(longest, query_start[s + 1] - query_start[s]);
     const bool light = head_size == 64 || longest * (num_q_heads / num_kv_heads) <= 64;
-    if (heaviest <= (light ? 96 : 288) || ctas * (head_size == 64 ? 5 : 2) >= num_sms) rows = 0;
+    if (heaviest <= (light ? 96 : 288) ||
+        heaviest * num_sms <= (head_size == 64 ? 5 : 2) * num_kv_heads * info->total_blocks)
+      rows = 0;
   }
   if (rows > 0)
     rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, rows, true, window,

@@ -146,6 +146,12 @@ def test_prefill_plan_whole_tiles():
     assert plan([64 * 38], 30000, 128) == (256, False) and plan([64 * 37], 30000, 128) == (256, True)
     assert plan([64 * 16], 30000, 64) == (256, False) and plan([64 * 15], 30000, 64)[0] == 64
     assert plan([64 * 25], 30000, 128, sms=100) == (256, False)
+    # one long request among short ones is cut
+    lens = [60000] + [16] * 100
+    qs = list(range(0, 16 * 102, 16))
+    for window, split in ((1000, 0), (30000, 2)):
+        info = pd.paged_prefill_plan_sinks(qs, lens, 8, 2, 128, window, 4, 152)[1]
+        assert (info.num_split_tiles > 0) == (split > 0), window
     # three heads to a kv head are no box of q
     assert plan([6400], 1000, 64, Hq=6)[0] == 64
     # without sinks or a window, the plan of those calls
