@@ -20,16 +20,32 @@
 // Barriers are counted through the tiles: stage g of the CTA uses S / P buffer
 // g & 1, ring slot g % NS.
 //
+// A half's softmax has two warps on each scheduler and is bound by latency, so
+// what a stage does not need is kept out of it: which stages need a mask, and
+// which may hold V to zero, are ranges of stages worked out per tile (four
+// blocks' tests per stage cost ~200 of ~1200 cycles); a masked stage takes the
+// same exponentials as the others and clears P by the row's visible keys, and
+// with sinks only a tile's first stage takes a max (a masked stage 1900 cycles,
+// 3000 with its own max and tests); the row sums follow the hand-over of P.
+//
 // Measured (CUDA events over graph replays, bf16, P = 16; in brackets a CTA per
 // tile, at head size 64 tiles of 64 rows on mma.sync): 4 requests of 2048 tokens
-// after 2048, 32 / 8 heads of 128, window 1024, 4 sinks 165 us (206); 2 of 8192,
-// window 4096, 64 sinks 709 us (800), 61 % of the tensor peak; 1276 ragged
-// tokens, 16 / 4 heads of 64, window 700 20.2 us (30.6).
+// after 2048, 32 / 8 heads of 128, window 1024, 4 sinks 142 us (206); 2 of 8192,
+// window 4096, 64 sinks 678 us (800), 64 % of the tensor peak; 1276 ragged
+// tokens, 16 / 4 heads of 64, window 700 17.7 us (30.6).  Not kept: a warp per
+// half for its S and its PV MMAs (the same); S of 128 keys at once, one buffer
+// per half (800 against 700, halves in turn 830); O stored without the exchange
+// in 32-byte pieces or in 128-byte runs (2 - 3 % slower).
 #pragma once
 
 #include "pd_kernel.cuh"
 
 namespace pd {
+
+// the n lowest of 32 bits (none below 0, all from 32 on)
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kTpThreads, 1)
@@ -104,7 +120,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
   struct Tile {
     int s, h, rr0, q0, ml, L;
     int rows;                    // packed rows of the request
-    int u_lo, u_hi, v_lo, v_hi;  // union / intersection of the rows' windows
+    int u_lo, u_hi;              // union of the rows' windows
     int sk_nb, sk_gap, nb;
   };
   auto tile_of = [&](int s, int h, int rr0, int q0, int ml, int L) -> Tile {
@@ -117,12 +133,10 @@ __global__ void __launch_bounds__(kTpThreads, 1)
     t.L = L;
     t.rows = ml << lg_g;
     const int last = min(rr0 + 2 * kTpRows, t.rows) - 1;
-    t.u_lo = t.u_hi = t.v_lo = t.v_hi = 0;
+    t.u_lo = t.u_hi = 0;
     if (last >= rr0) {
-      t.v_hi = max(L - ml + (rr0 >> lg_g) + 1, 0);
       t.u_hi = max(L - ml + (last >> lg_g) + 1, 0);
-      t.u_lo = max(0, t.v_hi - p.window);
-      t.v_lo = max(0, t.u_hi - p.window);
+      t.u_lo = max(0, max(L - ml + (rr0 >> lg_g) + 1, 0) - p.window);
     }
     const int first = t.u_lo / kBlockKeys;
     t.sk_nb = (min(p.sinks, t.u_hi) + kBlockKeys - 1) / kBlockKeys;
@@ -376,61 +390,65 @@ __global__ void __launch_bounds__(kTpThreads, 1)
         lo = max(0, hi - p.window);
       }
       const int ntile = (t.nb + TB - 1) / TB;
-      float m_used = -INFINITY, lsum = 0.f;
+      // The run of the tile's blocks leaves this many keys out, behind the
+      // sinks: key k past them is the run's k - hole.  (No row sees keys of
+      // the hole, nor a key of the sinks' blocks past the sinks.)
+      const int hole = t.sk_gap * kBlockKeys;
+      // Stages that may hold keys no row sees: those of the sinks' last block,
+      // the window's first and the last one.
+      const int j_hid0 = (t.sk_nb - 1) >> 2, j_hid2 = (t.nb - 1) >> 2;
+      const int j_hid1 = (t.u_lo / kBlockKeys - t.sk_gap) >> 2;
+      static_assert(TB == 4, "blocks of a stage");
+      // Stages whose keys every row of the half sees: [0, j_sinks) and [j_lo, j_hi).
+      int j_sinks, j_lo, j_hi;
+      {
+        const int first = t.rr0 + kTpRows * X, last = min(first + kTpRows, t.rows) - 1;
+        const int h_hi = max(t.L - t.ml + (first >> lg_g) + 1, 0);
+        const int h_lo = max(0, t.L - t.ml + (last >> lg_g) + 1 - p.window);
+        j_sinks = min(p.sinks, h_hi) / SC;
+        const int b_lo = max((h_lo + kBlockKeys - 1) / kBlockKeys - t.sk_gap, t.sk_gap > 0 ? t.sk_nb : 0);
+        j_lo = (b_lo + TB - 1) / TB;
+        j_hi = min(h_hi / kBlockKeys - t.sk_gap, t.nb) / TB;
+      }
+      // (rows past the request's tokens hold other rows of q or zeros and are
+      // never stored: an infinite reference makes their weights 0)
+      float m_used = live ? -INFINITY : INFINITY, lsum = 0.f;
       for (int j = 0; j < ntile; ++j, ++g) {
         const uint32_t tSx = tS + (2 * X + (g & 1)) * SC;  // S, then P, of the stage
         ok = wait(bars + 2 * X + (g & 1), (g >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[SC];  // the row's scores of the stage (fp32 bits)
-        {
-          uint32_t x0[32], x1[32];
-          tmem_ld32(tSx + lane_base, x0);
-          tmem_ld32(tSx + lane_base + 32, x1);
-          tmem_wait_ld();
+        // the row's scores of the stage (fp32 bits), the second half's load
+        // under way while the first half's exponentials are taken
+        uint32_t sr[2][32];
+        tmem_ld32(tSx + lane_base, sr[0]);
+        tmem_wait_ld();
+        tmem_ld32(tSx + lane_base + 32, sr[1]);
+        const bool fast = j < j_sinks || (j >= j_lo && j < j_hi);
+        // the keys of the stage that the row sees, as bits
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+        if (!fast) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            sr[i] = x0[i];
-            sr[32 + i] = x1[i];
+          for (int y = 0; y < 2; ++y) {
+            const int at = SC * j + 32 * y;
+            vis[y] = (low_bits(hi - hole - at) & ~low_bits(lo - hole - at)) | low_bits(min(p.sinks, hi) - at);
           }
         }
-        const int nbt = min(TB, t.nb - j * TB);
-        // first key of the stage's block b
-        auto block_key = [&](int b) -> int {
-          const int k = j * TB + b;
-          return (k >= t.sk_nb ? k + t.sk_gap : k) * kBlockKeys;
-        };
-        // every row of the tile sees every key of the stage: no mask, and the
-        // scale is applied inside the exponent (rows past the request's
-        // tokens hold other rows of q or zeros, and are never stored)
-        bool fast = nbt == TB;
-#pragma unroll
-        for (int b = 0; b < TB; ++b) {
-          const int k0 = block_key(b), k1 = k0 + kBlockKeys;
-          fast = fast && k1 <= t.v_hi && (k0 >= t.v_lo || k1 <= p.sinks);
-        }
-        // the largest scaled score of an unmasked stage: the largest (scale
-        // >= 0) or smallest raw score, eight independent chains
-        auto fast_max = [&]() -> float {
+        // the row's largest scaled score of the stage, eight independent chains
+        auto row_max = [&]() -> float {
           float a[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) a[u] = __uint_as_float(sr[u]);
-          if (sl2 >= 0.f) {
+          for (int u = 0; u < 8; ++u) a[u] = -INFINITY;
 #pragma unroll
-            for (int c = 8; c < SC; ++c) a[c & 7] = fmaxf(a[c & 7], __uint_as_float(sr[c]));
+          for (int c = 0; c < SC; ++c)
+            a[c & 7] = fmaxf(a[c & 7], (vis[c >> 5] & (1u << (c & 31)))
+                                           ? __uint_as_float(sr[c >> 5][c & 31]) * sl2
+                                           : -INFINITY);
 #pragma unroll
-            for (int u = 4; u >= 1; u >>= 1)
+          for (int u = 4; u >= 1; u >>= 1)
 #pragma unroll
-              for (int v = 0; v < u; ++v) a[v] = fmaxf(a[v], a[v + u]);
-          } else {
-#pragma unroll
-            for (int c = 8; c < SC; ++c) a[c & 7] = fminf(a[c & 7], __uint_as_float(sr[c]));
-#pragma unroll
-            for (int u = 4; u >= 1; u >>= 1)
-#pragma unroll
-              for (int v = 0; v < u; ++v) a[v] = fminf(a[v], a[v + u]);
-          }
-          return a[0] * sl2;
+            for (int v = 0; v < u; ++v) a[v] = fmaxf(a[v], a[v + u]);
+          return a[0];
         };
         // O_X *= alpha row by row in tensor memory (the whole warp), once the
         // PV MMAs of the stage before have completed
@@ -450,114 +468,91 @@ __global__ void __launch_bounds__(kTpThreads, 1)
           tc_fence_before();
           return true;
         };
-        // An unmasked stage with a reference on every row takes its
-        // exponentials straight against that reference, tracking the largest
-        // P; only a row whose P exceeds 2^8 (its max grew more than 8 past
-        // the reference) needs the max, a rescale and the stage again.
-        const bool direct = fast && __all_sync(0xffffffffu, m_used != -INFINITY);
-        if (!direct) {
-          float mx;
-          if (fast) {
-            mx = fast_max();
-          } else {
-            // scaled scores with the mask applied (-inf), kept as fp32 bits;
-            // the visible keys of each block as bits
-            uint32_t vis[SC / 32] = {};
+        // P = 2^(x - m) against the row's reference m, rounded to the input
+        // type; keys that the row does not see give 0.  Where every row has a
+        // reference (with sinks, from the tile's first stage on) the max is
+        // not taken: the largest P tells when a row's max grew more than 8
+        // past its reference, and only then the row takes the max, O a
+        // rescale and the stage its exponentials again.
+        uint32_t w[2][16];
+        auto exps = [&](int y, float mu) {
 #pragma unroll
-            for (int b = 0; b < TB; ++b) {
-              const int kb = block_key(b);
-              const uint32_t m = (first_bits(hi - kb) & ~first_bits(lo - kb)) |
-                                 first_bits(min(p.sinks, hi) - kb);
-              if (live && b < nbt) vis[b >> 1] |= m << (16 * (b & 1));
+          for (int c = 0; c < 32; c += 2)
+            w[y][c >> 1] = pack2(sfu_exp2(fmaf(__uint_as_float(sr[y][c]), sl2, -mu)),
+                                 sfu_exp2(fmaf(__uint_as_float(sr[y][c + 1]), sl2, -mu)), tag{});
+        };
+        auto hide = [&]() {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (!fast && __any_sync(0xffffffffu, vis[y] != 0xffffffffu)) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const uint32_t two = vis[y] >> (2 * c);
+                w[y][c] &= ((two & 1u) | ((two << 15) & 0x10000u)) * 0xffffu;
+              }
             }
-            float a[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) a[u] = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < SC; ++c) {
-              const float v = (vis[c >> 5] & (1u << (c & 31))) ? __uint_as_float(sr[c]) * sl2 : -INFINITY;
-              sr[c] = __float_as_uint(v);
-              a[c & 7] = fmaxf(a[c & 7], v);
-            }
-#pragma unroll
-            for (int u = 4; u >= 1; u >>= 1)
-#pragma unroll
-              for (int v = 0; v < u; ++v) a[v] = fmaxf(a[v], a[v + u]);
-            mx = a[0];
-          }
-          const float m_new = fmaxf(m_used, mx);
+        };
+        // the reference raised to m_new where that is more than 8 past it
+        auto raise = [&](float m_new) -> bool {
           const bool need = m_used != -INFINITY && m_new > m_used + 8.f;
-          // (need implies j >= 1)
-          if (__any_sync(0xffffffffu, need)) {
+          if (__any_sync(0xffffffffu, need)) {  // (implies j >= 1)
             const float alpha = need ? sfu_exp2(m_used - m_new) : 1.f;
-            ok = rescale_o(alpha);
-            if (!ok) break;
+            if (!rescale_o(alpha)) return false;
             if (need) {
               lsum *= alpha;
               m_used = m_new;
             }
           }
+          return true;
+        };
+        const bool refs = __all_sync(0xffffffffu, m_used != -INFINITY);
+        if (!refs) {
+          wait_ld32(sr[1]);
+          const float m_new = row_max();
+          ok = raise(m_new);
+          if (!ok) break;
           if (m_used == -INFINITY) m_used = m_new;
         }
-        // P = 2^(x - m) rounded to the input type, over the S this warp has
-        // just read; the row sum takes P as rounded for the MMA (four
-        // chains), so O is normalised by the weights it was formed with
-        {
-          uint32_t w[SC / 2];
-          auto exps = [&](float mu) -> float {  // returns the largest P (direct stages)
-            float pmax = 0.f;
-            if (fast) {
-#pragma unroll
-              for (int c = 0; c < SC; c += 2)
-                w[c >> 1] = pack2(sfu_exp2(fmaf(__uint_as_float(sr[c]), sl2, -mu)),
-                                  sfu_exp2(fmaf(__uint_as_float(sr[c + 1]), sl2, -mu)), tag{});
-              pmax = max2_of(w, tag{});  // as rounded, two per instruction
-            } else {
-#pragma unroll
-              for (int c = 0; c < SC; c += 2)
-                w[c >> 1] = pack2(sfu_exp2(__uint_as_float(sr[c]) - mu),
-                                  sfu_exp2(__uint_as_float(sr[c + 1]) - mu), tag{});
-            }
-            return pmax;
-          };
-          const float pmax = exps(m_used == -INFINITY ? 0.f : m_used);
-          // (fmaxf skips a NaN P, as the max skipped a NaN score)
-          if (direct && __any_sync(0xffffffffu, pmax > 256.f)) {
-            const float m_new = fmaxf(m_used, fast_max());
-            const bool need = m_new > m_used + 8.f;
-            const float alpha = need ? sfu_exp2(m_used - m_new) : 1.f;
-            ok = rescale_o(alpha);
-            if (!ok) break;
-            if (need) {
-              lsum *= alpha;
-              m_used = m_new;
-            }
-            exps(m_used);
-          }
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < SC / 2; ++c) ls[c & 3] = add2_f32(ls[c & 3], w[c], tag{});
-          lsum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-          tmem_st32(tSx + lane_base, w);
+        const float mu = m_used == -INFINITY ? 0.f : m_used;
+        exps(0, mu);
+        wait_ld32(sr[1]);
+        exps(1, mu);
+        hide();
+        // (the largest as rounded; a NaN P is skipped, as by the max)
+        if (refs && __any_sync(0xffffffffu, fmaxf(max2_of(w[0], tag{}), max2_of(w[1], tag{})) > 256.f)) {
+          ok = raise(fmaxf(m_used, row_max()));
+          if (!ok) break;
+          exps(0, m_used);
+          exps(1, m_used);
+          hide();
         }
-        // zero V of keys no row sees (stale or NaN slots); each half does it
-        // before its own PV MMAs (the other half's writes are the same zeros)
-        if (!fast) {
-          unsigned char *vb = ring + (g % NS) * STAGE + TB * BLOCK_BYTES;
+        tmem_st16(tSx + lane_base, w[0]);
+        tmem_st16(tSx + lane_base + 16, w[1]);
+        // zero V of keys no row of the tile sees (stale or NaN slots); each half
+        // does it before its own PV MMAs (the other half's writes are the same
+        // zeros)
+        if (j == j_hid0 || j == j_hid1 || j == j_hid2) {
           constexpr int kV = D / 8;  // threads to a key's bytes
-          const int v = lane % kV;
-          for (int c = (32 * (warp & 3) + lane) / kV; c < nbt * kBlockKeys; c += 128 / kV) {
-            const int k = block_key(c >> 4) + (c & 15);
-            if (!(k < t.u_hi && (k >= t.u_lo || k < p.sinks)))
-              *reinterpret_cast<uint4 *>(vb + (c >> 4) * BLOCK_BYTES + (v >> 3) * 2048 + (c & 15) * 128 +
-                                         (v & 7) * 16) = make_uint4(0, 0, 0, 0);
+          const int v = lane % kV, c0 = (32 * (warp & 3) + lane) / kV;
+          unsigned char *vb = ring + (g % NS) * STAGE + TB * BLOCK_BYTES + (v >> 3) * 2048 + (v & 7) * 16;
+#pragma unroll 1
+          for (int k = TB * j; k < min(TB * j + TB, t.nb); ++k) {
+            const int k0 = (k >= t.sk_nb ? k + t.sk_gap : k) * kBlockKeys;
+            if (k0 + kBlockKeys <= t.u_hi && (k0 >= t.u_lo || k0 + kBlockKeys <= p.sinks)) continue;
+            for (int c = c0; c < kBlockKeys; c += 128 / kV)
+              if (!(k0 + c < t.u_hi && (k0 + c >= t.u_lo || k0 + c < p.sinks)))
+                *reinterpret_cast<uint4 *>(vb + (k - TB * j) * BLOCK_BYTES + c * 128) = make_uint4(0, 0, 0, 0);
           }
+          fence_proxy_async_smem();  // the zeros reach the tensor core
         }
         tmem_wait_st();
-        fence_proxy_async_smem();  // the zeroed V reaches the tensor core
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(bars + 4 + 2 * X + (g & 1)));  // P of the stage written
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < SC / 2; ++c) ls[c & 3] = add2_f32(ls[c & 3], w[c >> 4][c & 15], tag{});
+        lsum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
       }
       if (!ok) break;
 
