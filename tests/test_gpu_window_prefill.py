@@ -116,6 +116,30 @@ def test_tiles_large_scores(std, scale, D):
     _run(case, 10, tol=v, rel_tol=2.0 ** -6)
 
 
+@both
+@pytest.mark.parametrize("slope", [0.02, -0.02, 0.3])
+def test_tiles_scores_along_the_keys(slope, D):
+    """Scores that rise (or fall) from key to key, past every reference in
+    masked and unmasked stages, on every other head the other way round."""
+    case = _case(8, [150, 200], [900, 60], window=300, head_size=D)
+    q, k = case.q.clone(), case.k_cache.clone()
+    q[:] = 1.0
+    q[:, 1::2] = -1.0
+    for s, L in enumerate(case.seq_lens_host):
+        for p in range(L):
+            k[int(case.block_table[s, p // 16]), :, p % 16] = slope * p
+    case = dataclasses.replace(case, q=q, k_cache=k)
+    # (as above: a few keys matter to a row)
+    v = 2 * 2.0 ** -8 * float(case.v_cache[torch.isfinite(case.v_cache)].float().abs().max())
+    _run(case, 10, tol=v, rel_tol=2.0 ** -6)
+
+
+@both
+def test_tiles_scale_zero(D):
+    """The mean of the visible V."""
+    _run(dataclasses.replace(_case(9, [150, 200], [900, 60], window=300, head_size=D), scale=0.0), 10)
+
+
 def test_tiles_strided_q_and_out():
     case = hide(_case(8, [100, 200], [90, 300]), 4)
     g = case.to("cuda")
