@@ -11,21 +11,22 @@
 // before the angles arrive.  Rotated in fp32, rounded once.  Memory-bound:
 // every byte is read or written once.
 //
-// A token takes 128 threads with four heads in flight each when few tokens
-// leave the SMs empty (fewer than 8 per SM: 64 tokens of 32 / 8 heads at D =
-// 128 3.4 us; with 64 threads and one head 4.3), else 64 threads, one head and
-// the next, and as many CTAs as registers allow: 16384 such tokens 69.5 us (89
-// % of the measured copy rate; 128 threads 76 - 80, a warp per token 69 - 73,
-// four heads in flight 110, angles gathered by every thread 122); 5001 tokens
-// of 16 / 2 heads at D = 256 with 64 rotated dims 21.4 us (73 %).
+// A CTA per token: of 128 threads with four heads in flight each when few tokens
+// leave the SMs empty (fewer than 8 per SM: 64 tokens of 32 / 8 heads at D = 128
+// 3.4 us; with 64 threads and one head 4.3), else of 64 threads, one head and
+// the next, and as many CTAs as registers allow: 16384 such tokens 69 us (89
+// % of the measured copy rate; two tokens to a CTA 71, 128 threads 76 - 80, a
+// warp per token 69 - 73, four heads in flight 110, angles gathered by every
+// thread 122); 5001 tokens of 16 / 2 heads at D = 256 with 64 rotated dims 22
+// us (71 %; two loads in flight past rot_dim 23, eight 25).
 #include "paged_step.h"
 #include "pd_rope.cuh"
 
 namespace pd {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kManyGroup = 64;  // threads of a token when there are many
+constexpr int kFewGroup = 128;  // threads of a token when there are few
+constexpr int kManyGroup = 64;  // and when there are many
 constexpr int kMaxPairs = 256;  // rot_dim / 2 at head size 512
 
 struct RopeAxesParams {
@@ -39,15 +40,13 @@ struct RopeAxesParams {
 // the loads of the next kU are issued before the present ones are turned and
 // stored.
 template <bool BF16, bool NEOX, int kGroup, int kU>
-__global__ void __launch_bounds__(kThreads, kGroup == kManyGroup ? (NEOX ? 8 : 10) : 1)
+__global__ void __launch_bounds__(kGroup, kGroup == kManyGroup ? (NEOX ? 16 : 20) : 1)
     pd_rope_axes(const __grid_constant__ RopeAxesParams pa) {
   const RopeParams &p = pa.r;
   constexpr int kPairs = NEOX ? 8 : 4;  // pairs of a chunk
-  // the tokens' angles: cos, then sin
-  __shared__ __align__(16) float angles[kThreads / kGroup][2 * kMaxPairs];
-  const int me = threadIdx.x % kGroup;
-  float *cs = angles[threadIdx.x / kGroup];
-  const int t = blockIdx.x * (kThreads / kGroup) + threadIdx.x / kGroup;
+  // the token's angles: cos, then sin
+  __shared__ __align__(16) float cs[2 * kMaxPairs];
+  const int me = threadIdx.x, t = blockIdx.x;
   const int half = p.rot >> 1, heads = p.Hq + p.Hkv;
   const int chunks = half / kPairs;            // per head, <= 64
   const int wide = min(chunks, kGroup);        // chunks taken at a time
@@ -77,16 +76,15 @@ __global__ void __launch_bounds__(kThreads, kGroup == kManyGroup ? (NEOX ? 8 : 1
   // the inputs may be the previous kernel's outputs
   grid_dependency_wait();
   grid_dependents_launch();
-  const bool live = t < p.T;  // (the last CTA may have one token less)
-  const int first = live && h0 < hs ? h0 : heads;
+  const int first = h0 < hs ? h0 : heads;
   load(first, c0);
-  const int slot = live ? __ldg(p.slots + t) : -1;
-  if (live && me < pa.axes) {
+  const int slot = __ldg(p.slots + t);
+  if (me < pa.axes) {
     const int pos = __ldg(p.positions + me * pa.pos_stride + t);
     if (pos < 0 || pos >= p.max_pos) atomicOr(p.status, PD_DEV_BAD_POSITION);
   }
   // the angles of the token's pairs, once
-  for (int i = me; live && i < half; i += kGroup) {
+  for (int i = me; i < half; i += kGroup) {
     const int pos = __ldg(p.positions + pa.axis[i] * pa.pos_stride + t);
     const float *row = p.cos_sin + (int64_t)min(max(pos, 0), p.max_pos - 1) * p.cs_s0;
     cs[i] = __ldg(row + i);
@@ -104,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, kGroup == kManyGroup ? (NEOX ? 8 : 1
   };
   // the dims past rot_dim of q and k, and v
   constexpr int kW = 4;
-  const int pass = (p.D - p.rot) / 8, n_pass = live ? heads * pass : 0;
+  const int pass = (p.D - p.rot) / 8, n_pass = heads * pass;
   const int per_v = p.D / 8, n_v = write_kv ? p.Hkv * per_v : 0;
 #pragma unroll 1
   for (int i0 = me; i0 < n_pass + n_v; i0 += kW * kGroup) {
@@ -222,7 +220,6 @@ extern "C" PD_API int paged_rope_axes_cache_write(
   p.pos_stride = positions->stride[0];
 
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -230,12 +227,13 @@ extern "C" PD_API int paged_rope_axes_cache_write(
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool bf16 = q->dtype == PD_BF16, few = (int64_t)p.r.T * 4 < (int64_t)num_sms * 32;
-  cfg.gridDim = dim3((unsigned)(few ? p.r.T : ((int64_t)p.r.T + 1) / 2));
+  cfg.gridDim = dim3((unsigned)p.r.T);
+  cfg.blockDim = dim3(few ? kFewGroup : kManyGroup);
   auto launch = [&](auto kern) { return cudaLaunchKernelEx(&cfg, kern, p); };
   cudaError_t e;
   if (few)
-    e = bf16 ? (is_neox ? launch(pd_rope_axes<true, true, 128, 4>) : launch(pd_rope_axes<true, false, 128, 4>))
-             : (is_neox ? launch(pd_rope_axes<false, true, 128, 4>) : launch(pd_rope_axes<false, false, 128, 4>));
+    e = bf16 ? (is_neox ? launch(pd_rope_axes<true, true, kFewGroup, 4>) : launch(pd_rope_axes<true, false, kFewGroup, 4>))
+             : (is_neox ? launch(pd_rope_axes<false, true, kFewGroup, 4>) : launch(pd_rope_axes<false, false, kFewGroup, 4>));
   else
     e = bf16 ? (is_neox ? launch(pd_rope_axes<true, true, kManyGroup, 1>) : launch(pd_rope_axes<true, false, kManyGroup, 1>))
              : (is_neox ? launch(pd_rope_axes<false, true, kManyGroup, 1>) : launch(pd_rope_axes<false, false, kManyGroup, 1>));

@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(32 * (kWindowWarps + 1), 1)
   auto merge_unit = [&](const Piece &u) {
     // rows and parts whose loads are in flight at once (fewer at D = 256, where
     // more registers here cost the main loop its own: 31 us against 23 for 48
-    // sequences of 16 rows)
+    // sequences of 16 rows; bulk copies of the parts to shared memory are no
+    // faster)
     constexpr int kRows = D == 256 ? 2 : 3, kChunk = D == 256 ? 2 : 4;
     for (int r0_ = warp; r0_ < u.r.rows; r0_ += kRows * NC) {
       float M[kRows], ls[kRows], a[kRows][kV][kW];
