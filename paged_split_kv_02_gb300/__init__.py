@@ -215,7 +215,7 @@ _bind = None
 
 
 def _step(name):
-    """A call of paged_step.h as the ``_bind`` module makes it (bind.c): its
+    """A call of paged_step.h as the ``_bind`` module makes it (bind.cpp): its
     arguments in that file's order.  It returns the status, PD_EINVAL for
     tensors that are not on one CUDA device; a launch goes to the tensors'
     device, whichever is current."""
@@ -231,11 +231,8 @@ def _step(name):
 
         def address(f):
             return ctypes.cast(f, ctypes.c_void_p).value
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda d: torch.cuda.current_stream(d).cuda_stream)
         m.setup(address(L.paged_decode_attn_sinks), address(L.paged_prefill_attn_sinks),
-                address(L.paged_batch_tables), address(L.paged_rope_axes_cache_write), _DTYPES,
-                raw, torch.cuda.current_device, torch.cuda.set_device, torch.cuda.is_available)
+                address(L.paged_batch_tables), address(L.paged_rope_axes_cache_write))
         _bind = m
     return getattr(_bind, name)
 

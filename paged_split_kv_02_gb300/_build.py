@@ -1,6 +1,6 @@
 """Build of libpaged_decode.so: nvcc, one translation unit per head size,
 compiled in parallel for sm_103a only, linked in-tree next to this file; and of
-the Python module that marshals the step calls' arguments (bind.c)."""
+the Python module that marshals the step calls' arguments (bind.cpp)."""
 
 from __future__ import annotations
 
@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpaged_decode.so")
 BIND = os.path.join(HERE, "_bind.so")
-BIND_SRC = os.path.join(CSRC, "bind.c")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fvisibility=hidden"]
@@ -63,8 +63,27 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    def bind():
+        import torch
+
+        root = os.path.dirname(torch.__file__)
+        libs = os.path.join(root, "lib")
+        tmp = BIND + f".tmp{os.getpid()}"
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+               "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+               "-isystem", os.path.join(cuda, "include"), BIND_SRC, "-o", tmp, "-L" + libs,
+               "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stderr}")
+        os.replace(tmp, BIND)
+
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        bound = ex.submit(bind)
         logs = list(ex.map(compile_one, zip(srcs, objs)))
+        bound.result()
     if verbose:
         for lg in logs:
             if lg.strip():
@@ -75,13 +94,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    tmp = BIND + f".tmp{os.getpid()}"
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-Wall", *inc,
-           "-I" + sysconfig.get_paths()["include"], BIND_SRC, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for bind.c:\n{r.stderr}")
-    os.replace(tmp, BIND)
     return LIB
 
 
