@@ -222,7 +222,16 @@ bool plan_window(int S, int Hq, int Hkv, int D, int P, int M, int window, int si
   const int64_t nb_max = std::min<int64_t>(
       cdiv((int64_t)bt_width * P, kBlockKeys),
       cdiv((int64_t)window + M - 1, kBlockKeys) + 1 + cdiv(sinks, kBlockKeys));
-  if ((nb_max + kUnitCost) * S * Hkv >= 1 << 30) return false;  // places of the line are ints
+  const int64_t line = (nb_max + kUnitCost) * S * Hkv;
+  if (line >= 1 << 30) return false;  // places of the line are ints
+  // Four n-tiles leave one warp group of four warps, where the kernel of a CTA
+  // per unit has two: from about 68 blocks an SM on, that one streams faster
+  // (32 / 8 heads, M = 8, D = 128, window 4096: 16 sequences 71 us against 85, 64
+  // 228 against 328; window 1024: 16 sequences 38 against 34 here).  At head size
+  // 64 a window of a few blocks is less than its unit's end costs three n-tiles
+  // or more here (64 sequences of 128 keys, 20 / 4 heads, M = 4, 13.7 against 17.2).
+  if (NT == 4 && line > 68LL * num_sms) return false;
+  if (D == 64 && NT >= 3 && nb_max <= 12) return false;
   // two parts of (acc, m, l) per CTA, behind the counters
   if (!scratch || !scratch->data || scratch->counter_slots < 2LL * S * Hkv) return false;
   const int64_t cbytes = (scratch->counter_slots * 4 + 255) / 256 * 256;

@@ -102,6 +102,19 @@ def test_plan_sinks():
             plan(**bad)
 
 
+def test_decode_plan_window_kernel():
+    """Batches of more than a wave take the window kernel, but for many blocks
+    of four n-tiles, and three or more over a short window at head size 64."""
+    def path(S, D, M, window, Hq=32, Hkv=8):
+        scratch = pd.PdScratch(data=1 << 40, bytes=1 << 30, counter_slots=1 << 20)
+        return pd.paged_decode_plan_sinks(S, Hq, Hkv, D, 16, M, window, 4, 1000, 152,
+                                          scratch_desc=scratch)["path"]
+    assert path(64, 128, 4, 1024) == 6 and path(64, 128, 7, 1024) == 1 and path(8, 128, 8, 1024) == 6
+    assert path(64, 128, 8, 1024, Hq=20, Hkv=4) == 6
+    assert path(64, 64, 4, 128, Hq=20, Hkv=4) == 1 and path(64, 64, 4, 256, Hq=20, Hkv=4) == 6
+    assert path(2, 128, 1, 128) == 1 and path(64, 512, 1, 1024) == 1
+
+
 def test_prefill_plan_sinks():
     def plan(q_lens, lens, window, sinks, D=128, sms=152):
         qs = [0] + list(np.cumsum(q_lens))
