@@ -188,14 +188,19 @@ inline int64_t epilogue_bytes_tp(int D, int NS) {
   return (int64_t)NS * kStageBytes + 2LL * kTpRows * D * 2;
 }
 
-// The window prefill kernel (pd_window_prefill.cuh, head sizes 64 and 128):
-// ring of 64-key stages + both halves' Q + barriers + flags and the tensor-memory address + two item slots
-// + staged page ids.
+// The window prefill kernel (pd_window_prefill.cuh, head sizes 64 to 256): a
+// tile's halves of 128 rows (O of two fits beside S up to head size 128), its
+// rows, threads, and shared memory: ring of 64-key stages + the halves' Q +
+// barriers + flags and the tensor-memory address + two item slots + staged
+// page ids.
 constexpr int kWpBarriers = 18;
+constexpr int wp_halves(int D) { return D <= 128 ? 2 : 1; }
+constexpr int wp_tile_rows(int D) { return wp_halves(D) * kTpRows; }
+constexpr int wp_threads(int D) { return 32 * (5 * wp_halves(D) + 2); }
 constexpr int wp_stage_bytes(int D) { return 64 * 2 * D * 2; }
 inline int smem_bytes_wp(int D, int NS) {
-  return kSmemAlign + NS * (wp_stage_bytes(D) + 16) + 2 * kTpRows * D * 2 + kWpBarriers * 8 + 16 + 64 +
-         4 * kTpBlockIds;
+  return kSmemAlign + NS * (wp_stage_bytes(D) + 16) + wp_tile_rows(D) * D * 2 + kWpBarriers * 8 + 16 +
+         64 + 4 * kTpBlockIds;
 }
 
 // Floats the epilogue needs: combine phase and final-merge phase.
@@ -228,6 +233,9 @@ cudaError_t launch_window_prefill_d64(bool bf16, const CUtensorMap &tk, const CU
                                       const CUtensorMap &tq, const Params &p, const Launch &l,
                                       cudaStream_t stream);
 cudaError_t launch_window_prefill_d128(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv,
+                                       const CUtensorMap &tq, const Params &p, const Launch &l,
+                                       cudaStream_t stream);
+cudaError_t launch_window_prefill_d256(bool bf16, const CUtensorMap &tk, const CUtensorMap &tv,
                                        const CUtensorMap &tq, const Params &p, const Launch &l,
                                        cudaStream_t stream);
 

@@ -177,30 +177,32 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
   }
   std::vector<Tile> tiles;
   // Over a window with sinks the tile kernel is the rule, on whole tiles of 256
-  // rows at head sizes 64 and 128.  Few long tiles are cut instead, for a CTA
-  // per segment (at 64 in tiles of 64 rows on mma.sync): when one is heavier
-  // than twice the SMs' mean load (five times at 64; equal tiles on half or a
-  // fifth of the SMs) and than 288 blocks, or 96 where the merge is cheap
-  // (head size 64; requests of up to 64 rows).  Measured, whole / cut, us: head size 128, window 1024, 21 % of the SMs 26 /
+  // rows at head sizes 64 and 128, of 128 at 256.  Few long tiles are cut
+  // instead, for a CTA per segment (at 64 and 256 in tiles of 64 rows on
+  // mma.sync): when one is heavier than twice the SMs' mean load (five times at
+  // 64 and 256; equal tiles on half or a fifth of the SMs) and than 288 blocks,
+  // or 96 where the merge is cheap (head size 64; requests of up to 64 rows).
+  // Measured, whole / cut, us: head size 128, window 1024, 21 % of the SMs 26 /
   // 53, 84 % 28 / 80; 2048, 5 % 41 / 71, of 4 rows 38 / 20; 16384, 21 % 254 /
   // 149, 42 % 254 / 217, 84 % 255 / 322; head size 64, window 1024, 11 % 24 / 23;
-  // 2048, 11 % 39 / 34, 21 % 39 / 44; 16384, 11 % 237 / 172, 21 % 240 / 252.
+  // 2048, 11 % 39 / 34, 21 % 39 / 44; 16384, 11 % 237 / 172, 21 % 240 / 252; head
+  // size 256, window 1024, 5 % 30 / 33, 84 % 32 / 120; 16384, 5 % 375 / 195, 21 %
+  // 369 / 565.
   int rows = tile_rows_for(head_size);
   int rc = PD_OK;
-  if (sinks > 0 && window > 0 && (head_size == 64 || head_size == 128) && num_q_heads > 0 &&
+  if (sinks > 0 && window > 0 && head_size <= 256 && num_q_heads > 0 &&
       num_kv_heads > 0 && num_q_heads % num_kv_heads == 0 &&
       rows_are_a_box(num_q_heads / num_kv_heads)) {
     int64_t heaviest = 0;
     rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads,
-                    PD_PREFILL_TILE_ROWS_D128, false, window, sinks, num_sms, &tiles, info,
-                    &heaviest);
+                    wp_tile_rows(head_size), false, window, sinks, num_sms, &tiles, info, &heaviest);
     if (rc != PD_OK) return rc;
     int64_t longest = 0;
     for (int s = 0; s < num_seqs; ++s)
       longest = std::max<int64_t>(longest, query_start[s + 1] - query_start[s]);
     const bool light = head_size == 64 || longest * (num_q_heads / num_kv_heads) <= 64;
     if (heaviest <= (light ? 96 : 288) ||
-        heaviest * num_sms <= (head_size == 64 ? 5 : 2) * num_kv_heads * info->total_blocks)
+        heaviest * num_sms <= (head_size == 128 ? 2 : 5) * num_kv_heads * info->total_blocks)
       rows = 0;
   }
   if (rows > 0)
@@ -242,9 +244,10 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
     return PD_EINVAL;
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return PD_EINVAL;
   if (!head_size_ok(head_size)) return PD_EHEAD;
-  // (head size 64: a plan of 256-row tiles is for the tile kernel)
-  const bool tiles64 = head_size == 64 && info->tile_rows == PD_PREFILL_TILE_ROWS_D128;
-  const int rows = tiles64 ? PD_PREFILL_TILE_ROWS_D128 : tile_rows_for(head_size);
+  // (head sizes 64 and 256: a plan of the tile kernel's rows is for it)
+  const bool own_rows =
+      (head_size == 64 || head_size == 256) && info->tile_rows == wp_tile_rows(head_size);
+  const int rows = own_rows ? wp_tile_rows(head_size) : tile_rows_for(head_size);
   if (page_size <= 0 || page_size % kBlockKeys != 0 || window < 0 || sinks < 0 ||
       !std::isfinite(scale))
     return PD_EINVAL;
@@ -281,9 +284,9 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   // the plan: its work list on the device, its sizes from paged_prefill_plan
   if (info->num_items < 0 || info->num_items > INT32_MAX || info->tile_rows != rows ||
       info->num_split_tiles < 0 || info->num_slots < 0 || info->max_segments != kMaxSegments ||
-      (tiles64 && (info->num_split_tiles != 0 || !rows_are_a_box(num_q_heads / num_kv_heads))))
+      (own_rows && (info->num_split_tiles != 0 || !rows_are_a_box(num_q_heads / num_kv_heads))))
     return PD_EINVAL;
-  if (tiles64 && T > 0 && (q->stride[0] == 0 || q->stride[1] == 0)) return PD_EALIGN;
+  if (own_rows && T > 0 && (q->stride[0] == 0 || q->stride[1] == 0)) return PD_EALIGN;
   if (work->ndim != 2 || work->shape[0] != info->num_items || work->shape[1] != 8 ||
       work->stride[1] != 1 || work->stride[0] != 8 || (info->num_items > 0 && !work->data) ||
       (reinterpret_cast<uintptr_t>(work->data) & 15u) != 0)
@@ -315,7 +318,7 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   }
 
   CUtensorMap tk, tv;
-  if ((rc = cache_tensor_map(k_cache, layout, &tk, sh.path == 5)) != PD_OK) return rc;
+  if ((rc = cache_tensor_map(k_cache, layout, &tk, sh.path == 5 || own_rows)) != PD_OK) return rc;
   if ((rc = cache_tensor_map(v_cache, layout, &tv)) != PD_OK) return rc;
 
   p.q = q->data;
@@ -360,13 +363,13 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   p.pf_groups = info->num_split_tiles;
   p.pf_slots = info->num_slots;
 
-  // A window with sinks at head size 128 without split tiles, or a plan of
-  // 256-row tiles at head size 64: the kernel that runs tile after tile.  (At
+  // A window with sinks at head size 128 without split tiles, or a plan of its
+  // rows at 64 and 256: the kernel that runs tile after tile.  (At
   // 128 where q's rows are no box, heads to a kv head not a power of two up to
   // 128 or a stride of 0, a CTA per tile.)
   const bool tiles128 = sh.path == 5 && p.sinks > 0 && info->num_split_tiles == 0 &&
                         rows_are_a_box(p.G) && q->stride[0] > 0 && q->stride[1] > 0;
-  if (tiles64 || tiles128) {
+  if (own_rows || tiles128) {
     if (info->num_items * num_kv_heads > 1 << 30) return PD_EINVAL;
     CUtensorMap tq;
     if ((rc = query_tensor_map(q, p.G, &tq)) != PD_OK) return rc;
@@ -376,10 +379,12 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
     p.NS = std::min(8, (kSmemLimit - smem_bytes_wp(head_size, 0)) / (wp_stage_bytes(head_size) + 16));
     Launch w{};
     w.grid = dim3((unsigned)std::min<int64_t>(num_sms, info->num_items * num_kv_heads));
-    w.block = dim3(kTpThreads);
+    w.block = dim3(wp_threads(head_size));
     w.smem = smem_bytes_wp(head_size, p.NS);
     const cudaError_t e =
-        (tiles64 ? launch_window_prefill_d64 : launch_window_prefill_d128)(
+        (head_size == 64    ? launch_window_prefill_d64
+         : head_size == 128 ? launch_window_prefill_d128
+                            : launch_window_prefill_d256)(
             q->dtype == PD_BF16, tk, tv, tq, p, w, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
       cudaGetLastError();

@@ -1,8 +1,8 @@
-// Prefill over a window with sinks at head sizes 64 and 128, tile after tile.
+// Prefill over a window with sinks at head sizes 64 to 256, tile after tile.
 //
 // The tiles, stages, products and softmax are those of pd_kernel.cuh's
 // tensor-memory prefill (256 packed rows as two halves that share every K/V
-// stage; S, P and O in tensor memory).  A window makes a tile short: at 1024
+// stage, at head size 256 one half of 128 rows; S, P and O in tensor memory).  A window makes a tile short: at 1024
 // keys 17 stages of 64 keys, ~1.1 us each, beside ~11 us of starting the CTA,
 // reading the work item and lengths, loading Q, filling the ring and storing
 // O.  Here a CTA keeps its tensor memory and ring and runs through a list of
@@ -32,7 +32,9 @@
 // tile, at head size 64 tiles of 64 rows on mma.sync): 4 requests of 2048 tokens
 // after 2048, 32 / 8 heads of 128, window 1024, 4 sinks 142 us (206); 2 of 8192,
 // window 4096, 64 sinks 678 us (800), 64 % of the tensor peak; 1276 ragged
-// tokens, 16 / 4 heads of 64, window 700 17.7 us (30.6).  Not kept: a warp per
+// tokens, 16 / 4 heads of 64, window 700 17.7 us (30.6); 1024 tokens, 32 / 8
+// heads of 256, window 1024 62 us (64 rows on mma.sync 245), 4096 of window 4096
+// 694 (2942).  Not kept: a warp per
 // half for its S and its PV MMAs (the same); S of 128 keys at once, one buffer
 // per half (800 against 700, halves in turn 830); O stored without the exchange
 // in 32-byte pieces or in 128-byte runs (2 - 3 % slower).
@@ -48,15 +50,16 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kTpThreads, 1)
+__global__ void __launch_bounds__(wp_threads(D), 1)
     pd_window_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ Params p) {
   constexpr int KS = D / 16, TB = 4, SC = TB * kBlockKeys, NBOX = D / 64;
   constexpr int BLOCK_BYTES = kBlockKeys * D * 2, STAGE = wp_stage_bytes(D), BIDS = kTpBlockIds;
-  constexpr int kHalf = kTpRows * D * 2;  // bytes of a half's Q
-  constexpr int kCols = 512;              // tensor memory: S / P 4 x 64 columns, O 2 x D
+  constexpr int H = wp_halves(D), ROWS = H * kTpRows;  // halves of a tile, its rows
+  constexpr int kHalf = kTpRows * D * 2;               // bytes of a half's Q
+  constexpr int kCols = 512;  // tensor memory: S / P 2 H x 64 columns, O H x D
   static_assert(2 * TB * BLOCK_BYTES == STAGE, "K and V of 64 keys");
-  static_assert(D == 64 || D == 128, "O of two halves beside S");
+  static_assert(2 * H * SC + H * D <= kCols, "O beside S");
   using tag = std::integral_constant<bool, BF16>;
   using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
 
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
   const int NS = p.NS;
   unsigned char *ring = smem;
   unsigned char *qs = ring + NS * STAGE;
-  uint64_t *full = reinterpret_cast<uint64_t *>(qs + 2 * kHalf);
+  uint64_t *full = reinterpret_cast<uint64_t *>(qs + H * kHalf);
   uint64_t *empty = full + NS;
   // [0..3] S full (2 x + b), [4..7] P written, [8..11] PV done, [12] every MMA
   // done, [13] Q landed, [14,15] item slot full, [16,17] item slot read
@@ -77,15 +80,15 @@ __global__ void __launch_bounds__(kTpThreads, 1)
   int *pids = const_cast<int *>(items) + 16;        // [BIDS]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kSWarp = kTpSoftmaxWarps, kLoadWarp = kSWarp + 1, kPvWarp = kSWarp + 2;
-  constexpr int kReaders = kTpSoftmaxWarps + 3;  // warps that read an item slot
+  constexpr int kSWarp = 4 * H, kLoadWarp = kSWarp + 1, kPvWarp = kSWarp + 2;
+  constexpr int kReaders = 5 * H + 1;  // warps that read an item slot: all but the load warp
   if (warp == 0) {
     if (lane < NS) {
       mbar_init(smem_u32(full + lane), 1);
-      mbar_init(smem_u32(empty + lane), 2);  // both halves' PV commits
+      mbar_init(smem_u32(empty + lane), H);  // the halves' PV commits
     }
     if (lane < kWpBarriers)
-      mbar_init(smem_u32(bars + lane), lane >= 4 && lane <= 7 ? 4 : lane == 12 ? 3 : lane >= 16 ? kReaders : 1);
+      mbar_init(smem_u32(bars + lane), lane >= 4 && lane <= 7 ? 4 : lane == 12 ? H + 1 : lane >= 16 ? kReaders : 1);
     if (lane == 31) flags[0] = 0;
     fence_mbar_init();
   }
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base =
       __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
-  const uint32_t tS = tmem_base, tO = tmem_base + 4 * SC;
+  const uint32_t tS = tmem_base, tO = tmem_base + 2 * H * SC;
   grid_dependency_wait();
 
   const int lg_g = __ffs(p.G) - 1;  // G is a power of two here
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
     t.ml = ml;
     t.L = L;
     t.rows = ml << lg_g;
-    const int last = min(rr0 + 2 * kTpRows, t.rows) - 1;
+    const int last = min(rr0 + ROWS, t.rows) - 1;
     t.u_lo = t.u_hi = 0;
     if (last >= rr0) {
       t.u_hi = max(L - ml + (last >> lg_g) + 1, 0);
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
     };
     auto good = [&](const int4 &w0) {
       // (this launch has no split tiles: one segment each)
-      return w0.x >= 0 && w0.x < p.num_seqs && w0.y >= 0 && w0.y <= (INT32_MAX - 64) / (2 * kTpRows) &&
+      return w0.x >= 0 && w0.x < p.num_seqs && w0.y >= 0 && w0.y <= (INT32_MAX - 64) / ROWS &&
              w0.z == 0 && w0.w == 1;
     };
     auto lengths = [&](const int4 &w0, int &L, int &qa, int &qb) {
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
         it[0] = more;
         it[1] = c0.x;
         it[2] = ch;
-        it[3] = c0.y * 2 * kTpRows;
+        it[3] = c0.y * ROWS;
         it[4] = a;
         it[5] = b - a;
         it[6] = len;
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
       __syncwarp();
       if (!more) break;
       ++n;
-      const Tile t = tile_of(c0.x, ch, c0.y * 2 * kTpRows, a, b - a, len);
+      const Tile t = tile_of(c0.x, ch, c0.y * ROWS, a, b - a, len);
       const int32_t *bt_row = p.block_table + (int64_t)t.s * p.bt_stride;
       auto seq_block = [&](int k) -> int { return k >= t.sk_nb ? k + t.sk_gap : k; };
       const int ntile = (t.nb + TB - 1) / TB;
@@ -301,14 +304,14 @@ __global__ void __launch_bounds__(kTpThreads, 1)
       const int ntile = (t.nb + TB - 1) / TB;
       if (ntile == 0) continue;
       // Q's buffer is free once the last S of the tile before is done
-      for (int x = 0; x < 2 && ok && g > 0; ++x)
+      for (int x = 0; x < H && ok && g > 0; ++x)
         ok = wait(bars + 2 * x + ((g - 1) & 1), ((g - 1) >> 1) & 1);
       if (!ok) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(bars + 13), 2 * kHalf);
+        mbar_arrive_expect_tx(smem_u32(bars + 13), H * kHalf);
         const int tok = t.q0 + (t.rr0 >> lg_g);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < H; ++x)
 #pragma unroll
           for (int b = 0; b < NBOX; ++b)
             tma_load_4d(qb_u + x * kHalf + b * (kTpRows * 128), &tmQ, smem_u32(bars + 13), 0, t.h << lg_g,
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
         ok = wait(full + slot, (g / NS) & 1);
         const uint32_t kst = ring_u + slot * STAGE;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < H; ++x) {
           // (S over the buffer once the PV MMAs of stage g - 2 have read its P)
           if (ok && g >= 2) ok = wait(bars + 8 + 2 * x + sb, ((g - 2) >> 1) & 1);
           if (!ok) break;

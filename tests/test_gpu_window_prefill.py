@@ -37,7 +37,8 @@ def _plan(case, sinks, num_sms=1):  # (one SM: whole tiles)
     G = case.num_q_heads // case.num_kv_heads
     if num_sms == 1:
         assert plan[1].num_split_tiles == 0
-        assert plan[1].tile_rows == (64 if case.head_size == 64 and G & (G - 1) else 256)
+        box = G & (G - 1) == 0
+        assert plan[1].tile_rows == {64: 256 if box else 64, 128: 256, 256: 128 if box else 64}[case.head_size]
     return plan
 
 
@@ -60,7 +61,7 @@ def _case(seed, q_lens, contexts, **kw):
     return W.make_prefill_case("tiles", seed=seed, q_lens=q_lens, contexts=contexts, **base)
 
 
-both = pytest.mark.parametrize("D", [64, 128])
+both = pytest.mark.parametrize("D", [64, 128, 256])
 
 
 @both
@@ -244,7 +245,8 @@ def test_tiles_report_bad_inputs(D):
         out = torch.full_like(g.q, 7.0)
         run_prefill_sinks(g, 4, None, plan=(items, plan[1]), out=out)
         assert _status() == pd.DEV_BAD_WORK
-        skipped = slice(200 + 64 * tile, min(300, 264 + 64 * tile))
+        n = plan[1].tile_rows // 4  # tokens of a tile
+        skipped = slice(200 + n * tile, min(300, 200 + n + n * tile))
         assert bool((out[skipped] == 7.0).all())
         out[skipped] = want[skipped]
         assert torch.equal(out, want)
@@ -265,20 +267,21 @@ def test_tiles_report_bad_inputs(D):
     assert torch.equal(run_prefill_sinks(g, 4, None, plan=plan), want)
 
 
-def test_tiles_at_head_size_64_under_either_plan():
-    """Plans of 256-row and of 64-row tiles, the plan made without sinks, and
-    256-row tiles under calls without sinks or without a window."""
-    case = _case(13, [300, 77], [500, 0], head_size=64)
+@pytest.mark.parametrize("D,wide_rows", [(64, 256), (256, 128)])
+def test_tiles_under_either_plan(D, wide_rows):
+    """Plans of the tile kernel's rows and of 64-row tiles (the plan made
+    without sinks), under calls without sinks or without a window too."""
+    case = _case(13, [300, 77], [500, 0], head_size=D)
     g = case.to("cuda")
-    sc = pd.prefill_scratch(2, 64, num_sms=160)
+    sc = pd.prefill_scratch(2, D, num_sms=160)
     rows = sample_rows(case, 300)
     wide = _plan(case, 9)
-    narrow = plain = pd.paged_prefill_plan(case.query_start_host, case.seq_lens_host, 8, 2, 64, 200, 152)
-    assert (wide[1].tile_rows, narrow[1].tile_rows, plain[1].tile_rows) == (256, 64, 64)
-    for sinks, window, plans in ((9, 200, (wide, plain)), (0, 200, (wide, plain)), (9, 0, (wide, plain))):
+    narrow = pd.paged_prefill_plan(case.query_start_host, case.seq_lens_host, 8, 2, D, 200, 152)
+    assert (wide[1].tile_rows, narrow[1].tile_rows) == (wide_rows, 64)
+    for sinks, window in ((9, 200), (0, 200), (9, 0)):
         c = dataclasses.replace(case, window=window)
         ref = O.attention(c, sinks, rows)
-        for plan in plans:
+        for plan in (wide, narrow):
             out = run_prefill_sinks(dataclasses.replace(g, window=window), sinks, sc, plan=plan)
             torch.cuda.synchronize()
             check(c, out, rows=rows, ref=ref)
@@ -290,8 +293,8 @@ def test_tiles_at_head_size_64_under_either_plan():
     with pytest.raises(pd.PagedDecodeError, match="PD_EALIGN"):
         run_prefill_sinks(one, 9, sc, plan=wide)
     run_prefill_sinks(one, 9, sc, plan=narrow)
-    # the split of a 64-row plan is not for 256-row tiles
+    # the split of a 64-row plan is not for these tiles
     info = pd.PdPrefillPlanInfo.from_buffer_copy(narrow[1])
-    info.tile_rows, info.num_split_tiles = 256, 1
+    info.tile_rows, info.num_split_tiles = wide_rows, 1
     with pytest.raises(pd.PagedDecodeError, match="PD_EINVAL"):
         run_prefill_sinks(g, 9, sc, plan=(narrow[0], info))

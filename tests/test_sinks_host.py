@@ -144,7 +144,8 @@ def test_prefill_plan_sinks():
 
 
 def test_prefill_plan_whole_tiles():
-    """Whole 256-row tiles at head sizes 64 and 128, but for few long ones."""
+    """Whole tiles of 256 rows at head sizes 64 and 128, of 128 at 256, but for
+    few long ones."""
     def plan(q_lens, window, D, sinks=4, Hq=8, Hkv=2, sms=152):
         qs = [0] + list(np.cumsum(q_lens))
         info = pd.paged_prefill_plan_sinks(qs, [60000] * len(q_lens), Hq, Hkv, D, window, sinks, sms)[1]
@@ -165,8 +166,12 @@ def test_prefill_plan_whole_tiles():
     for window, split in ((1000, 0), (30000, 2)):
         info = pd.paged_prefill_plan_sinks(qs, lens, 8, 2, 128, window, 4, 152)[1]
         assert (info.num_split_tiles > 0) == (split > 0), window
+    # at 256: 128 rows, or 64
+    assert plan([64], 4000, 256) == (128, False) and plan([64], 5000, 256) == (64, True)
+    assert plan([32 * 16], 30000, 256) == (128, False) and plan([32 * 15], 30000, 256) == (64, True)
     # three heads to a kv head are no box of q
     assert plan([6400], 1000, 64, Hq=6)[0] == 64
+    assert plan([6400], 1000, 256, Hq=6)[0] == 64
     # without sinks or a window, the plan of those calls
     for kw in (dict(window=1000, sinks=0), dict(window=0, sinks=4)):
         assert plan([640], D=64, **kw)[0] == 64 and plan([64], D=128, **kw) == (256, True)
