@@ -70,10 +70,12 @@ PD_API int paged_decode_plan_sinks(int num_seqs, int num_q_heads, int num_kv_hea
  * paged_prefill_attn; scratch from paged_prefill_scratch_bytes).  The plan's
  * loads are those of the window with sinks; a plan made for another window
  * or sinks gives the same outputs, less evenly spread.  At head sizes 64 to
- * 256, with a power of two of q heads to a kv head (up to 128), the plan keeps
- * its tiles whole unless they are few and long: info.tile_rows is then 256 (128
- * at head size 256), which at head sizes 64 and 256 wants q's strides above 0
- * (else PD_EALIGN). */
+ * 256, with up to 128 q heads to a kv head (at 128 at least 5/8 of a power of
+ * two), the plan keeps its tiles whole unless they are few and long: the rows
+ * of 256 / G' tokens (128 / G' at head size 256), G' the q heads to a kv head
+ * rounded up to a power of two, are then a tile (info.tile_rows).  But for
+ * PD_PREFILL_TILE_ROWS_D128 at head size 128 such a plan wants q's strides above
+ * 0 (else PD_EALIGN). */
 PD_API int paged_prefill_plan_sinks(const int32_t *query_start, const int32_t *seq_lens,
                                     int num_seqs, int num_q_heads, int num_kv_heads,
                                     int head_size, int window, int sinks, int num_sms,

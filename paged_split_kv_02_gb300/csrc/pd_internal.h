@@ -196,6 +196,14 @@ inline int64_t epilogue_bytes_tp(int D, int NS) {
 constexpr int kWpBarriers = 18;
 constexpr int wp_halves(int D) { return D <= 128 ? 2 : 1; }
 constexpr int wp_tile_rows(int D) { return wp_halves(D) * kTpRows; }
+// (G q heads to a kv head, padded to a power of two; the packed rows of a
+// tile's whole tokens)
+inline int wp_padded(int G) {
+  int p = 1;
+  while (p < G) p *= 2;
+  return p;
+}
+inline int wp_packed_rows(int D, int G) { return wp_tile_rows(D) / wp_padded(G) * G; }
 constexpr int wp_threads(int D) { return 32 * (5 * wp_halves(D) + 2); }
 constexpr int wp_stage_bytes(int D) { return 64 * 2 * D * 2; }
 inline int smem_bytes_wp(int D, int NS) {

@@ -40,8 +40,14 @@ struct Tile {
   int32_t nseg;
 };
 
-// Can a half of a tile be a box of q: G q heads to a kv head by 128 / G tokens.
-bool rows_are_a_box(int G) { return G <= kTpRows && (G & (G - 1)) == 0; }
+// Does the tile kernel take G q heads to a kv head: a half is 128 / G' tokens of
+// G padded to a power of two G'.  At head size 128 a CTA per tile of unpadded
+// rows is faster where padding takes more than three rows of eight (4096 tokens
+// of 24 / 8 heads, 3 padded to 4, window 4096: 252 us against 234; window 256: 42
+// against 58); elsewhere the other kernel is mma.sync (2 - 4 times slower).
+bool tile_kernel_takes(int D, int G) {
+  return D <= 256 && G <= kTpRows && (D != 128 || 8 * G >= 5 * wp_padded(G));
+}
 
 // The tiles of a plan and their segments (split: heavy ones are cut).  *heaviest:
 // the most blocks of a tile.
@@ -181,7 +187,8 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
   // instead, for a CTA per segment (at 64 and 256 in tiles of 64 rows on
   // mma.sync): when one is heavier than twice the SMs' mean load (five times at
   // 64 and 256; equal tiles on half or a fifth of the SMs) and than 288 blocks,
-  // or 96 where the merge is cheap (head size 64; requests of up to 64 rows).
+  // or 96 where the merge is cheap (head size 64; requests of up to 64 rows), 40
+  // where it is a few rows.
   // Measured, whole / cut, us: head size 128, window 1024, 21 % of the SMs 26 /
   // 53, 84 % 28 / 80; 2048, 5 % 41 / 71, of 4 rows 38 / 20; 16384, 21 % 254 /
   // 149, 42 % 254 / 217, 84 % 255 / 322; head size 64, window 1024, 11 % 24 / 23;
@@ -190,18 +197,19 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
   // 369 / 565.
   int rows = tile_rows_for(head_size);
   int rc = PD_OK;
-  if (sinks > 0 && window > 0 && head_size <= 256 && num_q_heads > 0 &&
-      num_kv_heads > 0 && num_q_heads % num_kv_heads == 0 &&
-      rows_are_a_box(num_q_heads / num_kv_heads)) {
+  const int G = num_q_heads > 0 && num_kv_heads > 0 ? num_q_heads / num_kv_heads : 0;
+  const bool own_rows = G > 0 && tile_kernel_takes(head_size, G);
+  if (sinks > 0 && window > 0 && (own_rows || head_size == 128)) {
     int64_t heaviest = 0;
     rc = plan_tiles(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads,
-                    wp_tile_rows(head_size), false, window, sinks, num_sms, &tiles, info, &heaviest);
+                    own_rows ? wp_packed_rows(head_size, G) : rows, false, window, sinks, num_sms,
+                    &tiles, info, &heaviest);
     if (rc != PD_OK) return rc;
     int64_t longest = 0;
     for (int s = 0; s < num_seqs; ++s)
       longest = std::max<int64_t>(longest, query_start[s + 1] - query_start[s]);
-    const bool light = head_size == 64 || longest * (num_q_heads / num_kv_heads) <= 64;
-    if (heaviest <= (light ? 96 : 288) ||
+    const bool light = head_size == 64 || longest * G <= 64;
+    if (heaviest <= (longest * G <= 16 ? 40 : light ? 96 : 288) ||
         heaviest * num_sms <= (head_size == 128 ? 2 : 5) * num_kv_heads * info->total_blocks)
       rows = 0;
   }
@@ -244,10 +252,13 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
     return PD_EINVAL;
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return PD_EINVAL;
   if (!head_size_ok(head_size)) return PD_EHEAD;
-  // (head sizes 64 and 256: a plan of the tile kernel's rows is for it)
-  const bool own_rows =
-      (head_size == 64 || head_size == 256) && info->tile_rows == wp_tile_rows(head_size);
-  const int rows = own_rows ? wp_tile_rows(head_size) : tile_rows_for(head_size);
+  // (a plan of the tile kernel's rows is for it; at head size 128 and no padding
+  // they are those of a CTA per tile too)
+  const int G = num_q_heads / num_kv_heads;
+  const bool own_rows = tile_kernel_takes(head_size, G) &&
+                        info->tile_rows == wp_packed_rows(head_size, G) &&
+                        info->tile_rows != tile_rows_for(head_size);
+  const int rows = own_rows ? info->tile_rows : tile_rows_for(head_size);
   if (page_size <= 0 || page_size % kBlockKeys != 0 || window < 0 || sinks < 0 ||
       !std::isfinite(scale))
     return PD_EINVAL;
@@ -284,7 +295,7 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   // the plan: its work list on the device, its sizes from paged_prefill_plan
   if (info->num_items < 0 || info->num_items > INT32_MAX || info->tile_rows != rows ||
       info->num_split_tiles < 0 || info->num_slots < 0 || info->max_segments != kMaxSegments ||
-      (own_rows && (info->num_split_tiles != 0 || !rows_are_a_box(num_q_heads / num_kv_heads))))
+      (own_rows && info->num_split_tiles != 0))
     return PD_EINVAL;
   if (own_rows && T > 0 && (q->stride[0] == 0 || q->stride[1] == 0)) return PD_EALIGN;
   if (work->ndim != 2 || work->shape[0] != info->num_items || work->shape[1] != 8 ||
@@ -364,15 +375,14 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
   p.pf_slots = info->num_slots;
 
   // A window with sinks at head size 128 without split tiles, or a plan of its
-  // rows at 64 and 256: the kernel that runs tile after tile.  (At
-  // 128 where q's rows are no box, heads to a kv head not a power of two up to
-  // 128 or a stride of 0, a CTA per tile.)
+  // own rows: the kernel that runs tile after tile.  (At 128 with more padding
+  // than that, or a stride of 0, a CTA per tile.)
   const bool tiles128 = sh.path == 5 && p.sinks > 0 && info->num_split_tiles == 0 &&
-                        rows_are_a_box(p.G) && q->stride[0] > 0 && q->stride[1] > 0;
+                        G <= kTpRows && wp_padded(G) == G && q->stride[0] > 0 && q->stride[1] > 0;
   if (own_rows || tiles128) {
     if (info->num_items * num_kv_heads > 1 << 30) return PD_EINVAL;
     CUtensorMap tq;
-    if ((rc = query_tensor_map(q, p.G, &tq)) != PD_OK) return rc;
+    if ((rc = query_tensor_map(q, wp_padded(G), &tq)) != PD_OK) return rc;
     p.num_items = (int)info->num_items;
     p.window = window > 0 ? window : INT32_MAX;
     p.sinks = sinks;

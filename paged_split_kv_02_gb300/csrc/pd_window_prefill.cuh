@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
   const uint32_t tS = tmem_base, tO = tmem_base + 2 * H * SC;
   grid_dependency_wait();
 
-  const int lg_g = __ffs(p.G) - 1;  // G is a power of two here
+  // A token's rows: its G q heads of a kv head, padded to a power of two with
+  // the heads behind them (whose rows are not used), so that a half is a box of q
+  const int lg_g = p.G > 1 ? 32 - __clz(p.G - 1) : 0;
   const int total = p.num_items * p.Hkv;
   auto give_up = [&]() {
     if (lane == 0) {
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
   // A tile's keys: its rows' windows and the sinks as one run of nb blocks.
   struct Tile {
     int s, h, rr0, q0, ml, L;
-    int rows;                    // packed rows of the request
+    int rows;                    // padded rows of the request
     int u_lo, u_hi;              // union of the rows' windows
     int sk_nb, sk_gap, nb;
   };
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
         for (int x = 0; x < H; ++x)
 #pragma unroll
           for (int b = 0; b < NBOX; ++b)
-            tma_load_4d(qb_u + x * kHalf + b * (kTpRows * 128), &tmQ, smem_u32(bars + 13), 0, t.h << lg_g,
+            tma_load_4d(qb_u + x * kHalf + b * (kTpRows * 128), &tmQ, smem_u32(bars + 13), 0, t.h * p.G,
                         tok + x * (kTpRows >> lg_g), b);
       }
       __syncwarp();
@@ -386,7 +388,8 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
     Tile t;
     for (int n = 0; ok && take(n, t); ++n) {
       const int rr = t.rr0 + kTpRows * X + 32 * (warp & 3) + lane;
-      const bool live = rr < t.rows;
+      const int rr_q = rr & ((1 << lg_g) - 1);  // q head of the kv head's
+      const bool live = rr < t.rows && rr_q < p.G;
       int lo = 0, hi = 0;
       if (live) {
         hi = max(t.L - t.ml + (rr >> lg_g) + 1, 0);
@@ -413,8 +416,9 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
         j_lo = (b_lo + TB - 1) / TB;
         j_hi = min(h_hi / kBlockKeys - t.sk_gap, t.nb) / TB;
       }
-      // (rows past the request's tokens hold other rows of q or zeros and are
-      // never stored: an infinite reference makes their weights 0)
+      // (rows past the request's tokens or a token's heads hold other rows of q
+      // or zeros and are never stored: an infinite reference makes their
+      // weights 0)
       float m_used = live ? -INFINITY : INFINITY, lsum = 0.f;
       for (int j = 0; j < ntile; ++j, ++g) {
         const uint32_t tSx = tS + (2 * X + (g & 1)) * SC;  // S, then P, of the stage
@@ -568,9 +572,9 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
       const float inv = (ntile > 0 && lsum > 0.f) ? sfu_rcp(lsum) : 0.f;
       unsigned long long row = 0;
       if (live) {
-        const int i = rr >> lg_g, jq = rr - (i << lg_g);
+        const int i = rr >> lg_g;
         row = reinterpret_cast<unsigned long long>(obase + (int64_t)(t.q0 + i) * p.o_s0 +
-                                                   (int64_t)((t.h << lg_g) + jq) * p.o_s1);
+                                                   (int64_t)(t.h * p.G + rr_q) * p.o_s1);
       }
       // Four lanes exchange their rows' 16-byte pieces, so that lane i of them
       // holds piece i of all four rows and they store 64-byte runs.

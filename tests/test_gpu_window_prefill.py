@@ -37,8 +37,9 @@ def _plan(case, sinks, num_sms=1):  # (one SM: whole tiles)
     G = case.num_q_heads // case.num_kv_heads
     if num_sms == 1:
         assert plan[1].num_split_tiles == 0
-        box = G & (G - 1) == 0
-        assert plan[1].tile_rows == {64: 256 if box else 64, 128: 256, 256: 128 if box else 64}[case.head_size]
+        padded = 1 << (G - 1).bit_length()
+        rows = (128 if case.head_size == 256 else 256) // padded * G
+        assert plan[1].tile_rows == (256 if case.head_size == 128 and 8 * G < 5 * padded else rows)
     return plan
 
 
@@ -73,10 +74,10 @@ def test_tiles_types_and_windows(dtype, window, sinks, D):
 
 
 @both
-@pytest.mark.parametrize("heads", [(2, 2), (4, 2), (32, 8), (16, 2), (32, 1), (6, 2), (20, 4), (128, 1), (256, 2)])
+@pytest.mark.parametrize("heads", [(2, 2), (4, 2), (32, 8), (16, 2), (32, 1), (6, 2), (20, 4), (128, 1), (256, 2), (7, 1), (3, 1), (21, 3), (18, 2)])
 def test_tiles_heads(heads, D):
-    """1 .. 128 q heads to a kv head; 3 and 5, whose rows are no box of q, run
-    tile by tile."""
+    """1 .. 128 q heads to a kv head; 3, 5, 7 and 9 padded to 4, 8 and 16 (9 not
+    at head size 128); one kv head, past whose heads q ends."""
     _run(_case(heads[0], [70, 9, 130], [150, 0, 600], num_q_heads=heads[0], num_kv_heads=heads[1],
                head_size=D), 20)
 

@@ -155,6 +155,7 @@ def test_prefill_plan_whole_tiles():
     assert plan([64], 4000, 128) == (256, False) and plan([64], 5000, 128) == (256, True)
     assert plan([16], 1400, 128) == (256, False) and plan([16], 1600, 128) == (256, True)
     assert plan([16, 17], 4000, 128) == (256, False)
+    assert plan([4], 500, 256) == (128, False) and plan([4], 700, 256) == (64, True)
     assert plan([64], 1400, 64) == (256, False) and plan([64], 1600, 64) == (64, True)
     # half the SMs (a fifth at 64) filled: whole at any length
     assert plan([64 * 38], 30000, 128) == (256, False) and plan([64 * 37], 30000, 128) == (256, True)
@@ -169,9 +170,13 @@ def test_prefill_plan_whole_tiles():
     # at 256: 128 rows, or 64
     assert plan([64], 4000, 256) == (128, False) and plan([64], 5000, 256) == (64, True)
     assert plan([32 * 16], 30000, 256) == (128, False) and plan([32 * 15], 30000, 256) == (64, True)
-    # three heads to a kv head are no box of q
-    assert plan([6400], 1000, 64, Hq=6)[0] == 64
-    assert plan([6400], 1000, 256, Hq=6)[0] == 64
+    # three heads to a kv head, padded to four; five to eight; nine not at 128
+    assert [plan([6400], 1000, D, Hq=6) for D in (64, 256)] == [(192, False), (96, False)]
+    assert [plan([6400], 1000, D, Hq=10) for D in (64, 256)] == [(160, False), (80, False)]
+    def rows128(q):
+        return pd.paged_prefill_plan_sinks([0, 6400], [60000], q, 2, 128, 1000, 4, 152)[1].tile_rows
+    assert [rows128(q) for q in (2, 6, 10, 14, 18, 24, 256, 258)] == [256, 192, 160, 224, 256, 192, 256, 256]
+    assert plan([6400], 1000, 128, Hq=18) == (256, False) and plan([6400], 1000, 64, Hq=258)[0] == 64
     # without sinks or a window, the plan of those calls
     for kw in (dict(window=1000, sinks=0), dict(window=0, sinks=4)):
         assert plan([640], D=64, **kw)[0] == 64 and plan([64], D=128, **kw) == (256, True)
