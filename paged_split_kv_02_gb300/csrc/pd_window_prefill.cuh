@@ -36,7 +36,8 @@
 // heads of 256, window 1024 62 us (64 rows on mma.sync 245), 4096 of window 4096
 // 694 (2942).  Not kept: a warp per
 // half for its S and its PV MMAs (the same); S of 128 keys at once, one buffer
-// per half (800 against 700, halves in turn 830); O stored without the exchange
+// per half (800 against 700, halves in turn 830); P handed over 32 keys at a
+// time (153 us for 142); O stored without the exchange
 // in 32-byte pieces or in 128-byte runs (2 - 3 % slower).
 #pragma once
 

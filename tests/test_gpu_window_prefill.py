@@ -184,6 +184,23 @@ def test_tiles_rows_of_other_requests_hold_nan(D):
 
 
 @both
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_tiles_other_heads_hold_nan(bad, D):
+    """The rows that pad a token's heads are the next kv head's: whatever q holds
+    there, a kv head's outputs are its own."""
+    case = _case(14, [90, 40], [300, 0], num_q_heads=9, num_kv_heads=3, head_size=D)
+    q = case.q.clone()
+    q[:, 3:6] = bad
+    hidden = hide(case, 6)
+    g = dataclasses.replace(hidden.to("cuda"), q=q.cuda())
+    out = run_prefill_sinks(g, 6, None, plan=_plan(case, 6))
+    torch.cuda.synchronize()
+    rows = [(t, h) for t, h in sample_rows(case, 400) if not 3 <= h < 6]
+    out[:, 3:6] = 0
+    check(hidden, out, rows=rows, ref=O.attention(hidden, 6, rows))
+
+
+@both
 def test_tiles_a_request_longer_than_its_keys(D):
     """Rows before the sequence's start see nothing and are zero."""
     case = _case(10, [90, 40], [100, 0], head_size=D)
