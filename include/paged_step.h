@@ -46,7 +46,10 @@ extern "C" {
  *   sinks        >= 0 keys
  *   scratch      paged_decode_scratch_bytes / _init, as for paged_decode_attn
  *   opts         may be NULL; with sinks and a window, paths 2 and 3 are not
- *                built (PD_EINVAL) */
+ *                built (PD_EINVAL), and path 6 asks for the window kernel below
+ *                (PD_EINVAL where it does not serve: one sequence or more than
+ *                1024, head size 512, more than 56 rows to a kv head, another
+ *                knob set, too little scratch) */
 PD_API int paged_decode_attn_sinks(const pd_tensor *q, const pd_tensor *k_cache,
                                    const pd_tensor *v_cache, const pd_tensor *block_table,
                                    const pd_tensor *seq_lens, const pd_tensor *query_start,
@@ -56,7 +59,7 @@ PD_API int paged_decode_attn_sinks(const pd_tensor *q, const pd_tensor *k_cache,
                                    void *stream, const pd_options *opts);
 
 /* The launch plan of that call, on the host only.  A batch that fills the GPU
- * more than once and sets no knob is planned as path 6: one wave of grid_x
+ * more than once and sets no knob is mostly planned as path 6: one wave of grid_x
  * CTAs that each take an equal share of the blocks of every (sequence, kv
  * head), cut where the shares end (grid_y = 1; seg_blocks, the most blocks of
  * one; max_segments and max_parts = grid_x).  Its scratch need is two parts

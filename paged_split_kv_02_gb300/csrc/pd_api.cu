@@ -200,8 +200,8 @@ bool plan_window(int S, int Hq, int Hkv, int D, int P, int M, int window, int si
                  int num_sms, const pd_scratch *scratch, const pd_options &o, pd_plan *plan) {
   const int64_t R = (int64_t)(Hq / Hkv) * M;
   if (S < 2 || S > kWindowSeqs || D > 256 || R > 8 * kWindowWarps || Hkv > 65535) return false;
-  if (o.segments || o.row_groups || o.key_groups || o.stages || o.cluster || o.path ||
-      o.max_ctas_hint || o.merge || o.mergers)
+  if (o.segments || o.row_groups || o.key_groups || o.stages || o.cluster ||
+      (o.path && o.path != 6) || o.max_ctas_hint || o.merge || o.mergers)
     return false;
   // warp groups: three of one or two n-tiles (one group took 89 us for what
   // three took 44, two 54), two of three, else one
@@ -230,8 +230,8 @@ bool plan_window(int S, int Hq, int Hkv, int D, int P, int M, int window, int si
   // 228 against 328; window 1024: 16 sequences 38 against 34 here).  At head size
   // 64 a window of a few blocks is less than its unit's end costs three n-tiles
   // or more here (64 sequences of 128 keys, 20 / 4 heads, M = 4, 13.7 against 17.2).
-  if (NT == 4 && line > 68LL * num_sms) return false;
-  if (D == 64 && NT >= 3 && nb_max <= 12) return false;
+  if (!o.path && NT == 4 && line > 68LL * num_sms) return false;
+  if (!o.path && D == 64 && NT >= 3 && nb_max <= 12) return false;
   // two parts of (acc, m, l) per CTA, behind the counters
   if (!scratch || !scratch->data || scratch->counter_slots < 2LL * S * Hkv) return false;
   const int64_t cbytes = (scratch->counter_slots * 4 + 255) / 256 * 256;
@@ -270,7 +270,8 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   if (M < 1 || M > 8) return PD_EQLEN;
   // path: 0 = auto (mma.sync), 1 = mma.sync, 2 = warp dot products (D <=
   // 256, one 8-row n-tile per CTA), 3 = tcgen05 with tensor memory (D <= 256)
-  if (o.path < 0 || o.path > 3) return PD_EINVAL;
+  // (6, the window kernel, with sinks)
+  if (o.path < 0 || (o.path > 3 && o.path != 6)) return PD_EINVAL;
   if (o.wait_limit_us < 0) return PD_EINVAL;
   if (o.early_reads != 0 && o.early_reads != 1) return PD_EINVAL;
   if (o.mergers < 0 || (o.mergers & (o.mergers - 1)) != 0) return PD_EINVAL;
@@ -278,6 +279,11 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   if ((tc || dot) && D > 256) return PD_EINVAL;
   if (window == 0) sinks = 0;  // every key is visible
   if ((tc || dot) && sinks > 0) return PD_EINVAL;  // built for mma.sync
+  if (o.path == 6)
+    return sinks > 0 && plan_window(S, Hq, Hkv, D, P, M, window, sinks, bt_width, num_sms, scratch,
+                                    o, plan)
+               ? PD_OK
+               : PD_EINVAL;
   if ((tc || dot) && o.cluster > 1) return PD_EINVAL;
   const int G = Hq / Hkv, R = G * M;
   // One sequence: at most 16 packed rows per CTA.  Every n-tile warp of a
@@ -484,15 +490,30 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   } else if (o.merge == 2 && max_parts > 1) {
     return PD_EINVAL;  // the grid does not fit at once, or a cluster was asked for
   }
-  // A batch over a window with sinks that would take more than one wave goes to
-  // the window kernel.  In one wave the cooperative merge, or no split at all,
-  // is as fast or faster (us, this plan against the window kernel: 8 kv heads
-  // at D = 128, 4 sequences of 128 keys 8.1 / 8.5, 2 of 1k 10.4 / 9.8, 4 of 1k,
-  // two waves, 20.2 / 10.1; 2 at D = 256, 4 of 1k 10.0 / 15.2, 32 of 1k 33.5 /
-  // 19.4).
-  if (sinks > 0 && (int64_t)S * Hkv * rg * nseg > num_sms &&
-      plan_window(S, Hq, Hkv, D, P, M, window, sinks, bt_width, num_sms, scratch, o, plan))
-    return PD_OK;
+  // A batch over a window with sinks that would take more than one wave: the
+  // window kernel, or as many segments as fit in one wave (one where the units
+  // are more), whose merge is cooperative.  The latter where its CTA's blocks
+  // are few beside the window kernel's equal share of the line: a fit to 290
+  // batches (4 to 64 sequences, head sizes 64 to 256, 4 to 56 rows, windows of 128 to
+  // 4096), within 1 % of the better on average.  Measured, us, one wave / window
+  // kernel, D = 128: 32 / 8 heads, window 128, 16 sequences 7.6 / 11.9; window 1024,
+  // M = 8, 16 sequences 21 / 34, 64 sequences 76 / 104; 64 of M = 1 44 / 43.
+  if (sinks > 0 && S > 1 && units * nseg > num_sms) {
+    const int64_t fit = std::max<int64_t>(1, num_sms / units), waves = cdiv(units * fit, num_sms);
+    const int64_t mine = waves * cdiv(nb_max, fit);
+    const int64_t share = (nb_max + kUnitCost) * S * Hkv / num_sms;
+    if (!(waves <= 2 && 20 * mine <= 13 * share + 560) &&
+        plan_window(S, Hq, Hkv, D, P, M, window, sinks, bt_width, num_sms, scratch, o, plan))
+      return PD_OK;
+    // (head size 512, window 1024, 4 sequences of 32 / 8 heads 20 us against 36 by the
+    // rules above, 16 45 / 58; window 4096, 16 of 8 / 1 heads 29 / 59; but long
+    // units in several waves, 32 of 32 / 8 heads, 326 / 304)
+    if (nseg > 1 && !o.segments && !o.max_ctas_hint && !o.cluster &&
+        (units <= num_sms || nb_max <= 128)) {
+      o.segments = (int)fit;
+      return make_plan(S, Hq, Hkv, D, P, M, window, sinks, bt_width, num_sms, scratch, &o, plan);
+    }
+  }
   // launched as (segments, kv heads x row groups, sequences)
   if ((int64_t)Hkv * rg * nseg > INT32_MAX || (int64_t)Hkv * rg > 65535 || S > 65535)
     return PD_EINVAL;

@@ -1,5 +1,6 @@
-"""Batches over a window with sinks that fill the GPU more than once (the
-one-wave kernel of equal shares: path 6 of the plan), against the fp64 oracle.
+"""Batches over a window with sinks that fill the GPU more than once: the
+one-wave kernel of equal shares (path 6 of the plan), and the plan's choice,
+against the fp64 oracle.
 
 Bounds: those of gpu_helpers.  Keys that no row sees are NaN, pages without a
 visible key -1 in the table."""
@@ -31,11 +32,11 @@ def _clean():
     assert pd.paged_decode_device_status(reset=True) == 0
 
 
-def _path(case, sinks, sc):
+def _path(case, sinks, sc, opts=None):
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     return pd.paged_decode_plan_sinks(case.num_seqs, case.num_q_heads, case.num_kv_heads, case.head_size,
                                       case.page_size, case.max_query_len, case.window, sinks,
-                                      case.block_table.shape[1], sms, scratch=sc)["path"]
+                                      case.block_table.shape[1], sms, scratch=sc, opts=opts)["path"]
 
 
 def _lens(seed, S, hi):
@@ -73,7 +74,9 @@ def _run(case, sinks, splits=64, rows=400, opts=None):
     hidden = hide(case, sinks)
     g = hidden.to("cuda")
     sc = scratch_for(case, splits)
-    assert _path(case, sinks, sc) == 6
+    opts = pd.options() if opts is None else opts
+    opts.path = 6
+    assert _path(case, sinks, sc, opts) == 6
     out = torch.full_like(g.q, 7.0)
     run_sinks(g, sinks, sc, opts, out=out)
     torch.cuda.synchronize()

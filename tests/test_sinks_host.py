@@ -103,16 +103,31 @@ def test_plan_sinks():
 
 
 def test_decode_plan_window_kernel():
-    """Batches of more than a wave take the window kernel, but for many blocks
-    of four n-tiles, and three or more over a short window at head size 64."""
-    def path(S, D, M, window, Hq=32, Hkv=8):
-        scratch = pd.PdScratch(data=1 << 40, bytes=1 << 30, counter_slots=1 << 20)
-        return pd.paged_decode_plan_sinks(S, Hq, Hkv, D, 16, M, window, 4, 1000, 152,
-                                          scratch_desc=scratch)["path"]
-    assert path(64, 128, 4, 1024) == 6 and path(64, 128, 7, 1024) == 1 and path(8, 128, 8, 1024) == 6
-    assert path(64, 128, 8, 1024, Hq=20, Hkv=4) == 6
-    assert path(64, 64, 4, 128, Hq=20, Hkv=4) == 1 and path(64, 64, 4, 256, Hq=20, Hkv=4) == 6
+    """Batches of more than a wave take the window kernel, but for few blocks to
+    a CTA, or many of four n-tiles."""
+    scratch = pd.PdScratch(data=1 << 40, bytes=1 << 30, counter_slots=1 << 20)
+    def plan(S, D, M, window, Hq=32, Hkv=8, sinks=4, opts=None):
+        return pd.paged_decode_plan_sinks(S, Hq, Hkv, D, 16, M, window, sinks, 1000, 152,
+                                          scratch_desc=scratch, opts=opts)
+    def path(*args, **kw):
+        return plan(*args, **kw)["path"]
+    # asked for
+    six = pd.options(path=6)
+    assert path(16, 128, 1, 128, opts=six) == 6 and path(2, 256, 8, 128, Hq=56, opts=six) == 6
+    for bad in (dict(S=1), dict(S=1025), dict(D=512), dict(M=8, Hq=64), dict(window=0), dict(sinks=0)):
+        with pytest.raises(pd.PagedDecodeError):
+            plan(**{**dict(S=16, D=128, M=1, window=128, opts=six), **bad})
+    with pytest.raises(pd.PagedDecodeError):
+        plan(16, 128, 1, 128, opts=pd.options(path=6, stages=4))
+    # one wave where it is not taken
+    for S, M in ((4, 1), (16, 4), (64, 1)):
+        p = plan(S, 512, M, 1024, Hq=16, Hkv=2)
+        assert 100 < p["grid_x"] * p["grid_y"] <= 152
+    assert path(64, 128, 4, 1024) == 6 and path(64, 128, 7, 1024) == 1 and path(64, 128, 7, 100) == 1
+    assert path(64, 128, 8, 1024, Hq=20, Hkv=4) == 6 and path(64, 64, 4, 128, Hq=20, Hkv=4) == 1
     assert path(2, 128, 1, 128) == 1 and path(64, 512, 1, 1024) == 1
+    # few blocks to a CTA: one wave of the other kernel
+    assert path(16, 128, 1, 128) == 1 and path(16, 128, 1, 1024) == 1 and path(16, 128, 1, 4096) == 6
 
 
 def test_prefill_plan_sinks():
