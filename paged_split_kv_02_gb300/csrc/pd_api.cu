@@ -495,9 +495,9 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   // are more), whose merge is cooperative.  The latter where its CTA's blocks
   // are few beside the window kernel's equal share of the line: a fit to 290
   // batches (4 to 64 sequences, head sizes 64 to 256, 4 to 56 rows, windows of 128 to
-  // 4096), within 1 % of the better on average.  Measured, us, one wave / window
-  // kernel, D = 128: 32 / 8 heads, window 128, 16 sequences 7.6 / 11.9; window 1024,
-  // M = 8, 16 sequences 21 / 34, 64 sequences 76 / 104; 64 of M = 1 44 / 43.
+  // 4096), within 1 % of the better on average.  Measured, us, this kernel / window
+  // kernel, 32 / 8 heads at D = 128: window 128, 16 sequences 6.0 / 9.3, with M = 8
+  // 8.3 / 18.8; window 1024, 16 sequences with M = 8 22 / 34, 64 with M = 1 55 / 46.
   if (sinks > 0 && S > 1 && units * nseg > num_sms) {
     const int64_t fit = std::max<int64_t>(1, num_sms / units), waves = cdiv(units * fit, num_sms);
     const int64_t mine = waves * cdiv(nb_max, fit);
