@@ -1529,17 +1529,30 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : RM && SINK
     {
       // the Q tile: packed rows of this CTA, 16-byte chunks, 128B-swizzled
       const T *qbase = static_cast<const T *>(p.q);
-      for (int idx = tid; idx < NT8 * (D / 8); idx += NC * 32) {
-        const int r = idx / (D / 8), c = idx % (D / 8);
-        const int rr = rr0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (rr < rr1v) {
-          const int i = token_of(rr), j = rr - i * p.G;
-          v = __ldg(reinterpret_cast<const uint4 *>(qbase + (int64_t)(q0 + i) * p.q_s0 +
-                                                    (int64_t)(h * p.G + j) * p.q_s1 + c * 8));
+      // (over a window with sinks a prefill tile is a few stages: kB loads of a
+      // thread are in flight at once, 1427 tokens of 16 / 4 heads of 512 with a
+      // window of 1 and 15 sinks 56 us against 70; at head size 256 the decode
+      // batches lose what they gain)
+      constexpr int kB = SINK && D == 512 ? 8 : 1;
+      for (int idx0 = tid; idx0 < NT8 * (D / 8); idx0 += kB * NC * 32) {
+        uint4 v[kB];
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+          const int idx = idx0 + u * NC * 32, r = idx / (D / 8), c = idx % (D / 8), rr = rr0 + r;
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (r < NT8 && rr < rr1v) {
+            const int i = token_of(rr), j = rr - i * p.G;
+            v[u] = __ldg(reinterpret_cast<const uint4 *>(qbase + (int64_t)(q0 + i) * p.q_s0 +
+                                                         (int64_t)(h * p.G + j) * p.q_s1 + c * 8));
+          }
         }
-        const int tn = r >> 3, rw = r & 7, box = c >> 3, cc = c & 7;
-        *reinterpret_cast<uint4 *>(qs + (tn * NBOX + box) * 1024 + rw * 128 + ((cc ^ rw) << 4)) = v;
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+          const int idx = idx0 + u * NC * 32, r = idx / (D / 8), c = idx % (D / 8);
+          const int tn = r >> 3, rw = r & 7, box = c >> 3, cc = c & 7;
+          if (r < NT8)
+            *reinterpret_cast<uint4 *>(qs + (tn * NBOX + box) * 1024 + rw * 128 + ((cc ^ rw) << 4)) = v[u];
+        }
       }
       asm volatile("bar.sync 1, %0;" ::"r"(NC * 32) : "memory");
     }
@@ -1939,6 +1952,35 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : RM && SINK
       if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem_base, TMEM_COLS);
+      }
+    }
+    if constexpr (SINK && !TC && !TP) {
+      // one warp group and one segment: the rows as they are, normalised, a
+      // warp to a row (the tokens above: 45 us, 56 with the pass below)
+      if (KG == 1 && nseg == 1) {
+        constexpr int kW = D >= 128 ? 4 : 2;  // columns of a lane, kW 32 apart
+        for (int r = warp; r < nrows; r += (int)blockDim.x >> 5) {
+          const float l = lrow[r], inv = l > 0.f ? sfu_rcp(l) : 0.f;
+          T *dst = out_row(r) + kW * lane;
+          const float *src = cp + (size_t)r * D;
+#pragma unroll
+          for (int v = 0; v < D / (32 * kW); ++v) {
+            float o[kW];
+            const float *at = src + psw(32 * kW * v + kW * lane, r);
+            if constexpr (kW == 4) {
+              const float4 x = *reinterpret_cast<const float4 *>(at);
+              o[0] = x.x * inv; o[1] = x.y * inv; o[2] = x.z * inv; o[3] = x.w * inv;
+            } else {
+              const float2 x = *reinterpret_cast<const float2 *>(at);
+              o[0] = x.x * inv; o[1] = x.y * inv;
+            }
+            if constexpr (kW == 4)
+              store4<BF16>(dst + 128 * v, o);
+            else
+              *reinterpret_cast<uint32_t *>(dst + 64 * v) = pack2(o[0], o[1], std::integral_constant<bool, BF16>{});
+          }
+        }
+        return;
       }
     }
     const int DKm = p.coop ? D >> (__ffs(p.mergers) - 1) : D;  // K_max a power of two
