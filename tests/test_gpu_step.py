@@ -44,7 +44,7 @@ def test_a_step_builds_writes_and_attends(early):
         pd.paged_rope_axes_cache_write(q, k, v, pos, slots, cos_sin, axis, q_rot, kc, vc, Hq, Hkv,
                                        D, D, P, W.HND, True)
 
-    def judge(q_rot, out, qd, M, pos, slots):
+    def expect(q_rot, out, qd, M, pos, slots):
         want = B.batch_tables(host["ctx"], qd.tolist(), host["table"], P, q_rot.shape[0], 3,
                               free.tolist(), host["cursor"], delta.tolist())
         for a, b in zip((table, start, lens, pos, slots), want):
@@ -74,7 +74,7 @@ def test_a_step_builds_writes_and_attends(early):
     pd.paged_prefill_attn_sinks(q_rot, kc, vc, table, lens, start, items.cuda(), info, out, Hq, Hkv,
                                 D, P, window, sinks, D ** -0.5, W.HND, pd.prefill_scratch(Hkv, D))
     torch.cuda.synchronize()
-    judge(q_rot, out, qd, max(q_lens), pos, slots)
+    expect(q_rot, out, qd, max(q_lens), pos, slots)
 
     # decode steps of 0..2 tokens per request in a batch padded to 10 rows
     delta.copy_(torch.tensor([0, -3, 0, -60, 5], dtype=torch.int32))
@@ -96,7 +96,7 @@ def test_a_step_builds_writes_and_attends(early):
 
     step()
     torch.cuda.synchronize()
-    judge(q_rot, out, qd, M, pos, slots)
+    expect(q_rot, out, qd, M, pos, slots)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step()
@@ -106,4 +106,4 @@ def test_a_step_builds_writes_and_attends(early):
         qd.copy_(torch.tensor([n % 3, 1, 2, (n + 1) % 2, 1], dtype=torch.int32))
         graph.replay()
         torch.cuda.synchronize()
-        judge(q_rot, out, qd, M, pos, slots)
+        expect(q_rot, out, qd, M, pos, slots)
