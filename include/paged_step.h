@@ -72,7 +72,8 @@ PD_API int paged_decode_plan_sinks(int num_seqs, int num_q_heads, int num_kv_hea
 /* The prefill work list and call with sinks (paged_prefill_plan,
  * paged_prefill_attn; scratch from paged_prefill_scratch_bytes).  The plan's
  * loads are those of the window with sinks; a plan made for another window
- * or sinks gives the same outputs, less evenly spread.  At head sizes 64 to
+ * or sinks gives the same outputs but for their rounding, less evenly spread
+ * (tiles of other rows may be another kernel's).  At head sizes 64 to
  * 256, with up to 128 q heads to a kv head (at 128 at least 5/8 of a power of
  * two), the plan keeps its tiles whole unless they are few and long: the rows
  * of 256 / G' tokens (128 / G' at head size 256), G' the q heads to a kv head
