@@ -553,11 +553,12 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
   if (page_size <= 0 || page_size % kBlockKeys != 0) return PD_EINVAL;
   if (window < 0 || sinks < 0 || !std::isfinite(scale)) return PD_EINVAL;
   if (layout != PD_NHD && layout != PD_HND) return PD_EINVAL;
-  if (seq_lens->ndim != 1 || !seq_lens->data || seq_lens->stride[0] != 1) return PD_EINVAL;
+  if (seq_lens->ndim != 1 || seq_lens->stride[0] != 1) return PD_EINVAL;
   if (!element_dtype_ok(seq_lens, PD_I32) || !element_dtype_ok(block_table, PD_I32)) return PD_EDTYPE;
   const int64_t S = seq_lens->shape[0];
-  if (S < 0) return PD_EINVAL;
-  if (block_table->ndim != 2 || !block_table->data || block_table->shape[0] != S ||
+  // (of no request: any pointer)
+  if (S < 0 || (S > 0 && (!seq_lens->data || !block_table->data))) return PD_EINVAL;
+  if (block_table->ndim != 2 || block_table->shape[0] != S ||
       block_table->shape[1] < 1 || block_table->stride[1] != 1 || block_table->stride[0] < 0)
     return PD_EINVAL;
   // rows of q and out: S * M (uniform), or any count T with query_start
@@ -583,10 +584,13 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
     if (k_cache->shape[i] != v_cache->shape[i]) return PD_EINVAL;
   if (block_table->shape[1] > INT32_MAX || block_table->shape[1] * (int64_t)page_size > INT32_MAX)
     return PD_EINVAL;
-  if (S == 0 || T == 0) return PD_OK;
+  if (T == 0) return PD_OK;
 
   DeviceInfo dev;
   if ((rc = device_info(&dev)) != PD_OK) return rc;
+  // (no request: every row is padding)
+  if (S == 0)
+    return zero_padding(out, static_cast<const int32_t *>(query_start->data), 0, dev.num_sms, stream);
   pd_plan plan;
   rc = make_plan((int)S, num_q_heads, num_kv_heads, head_size, page_size, max_query_len, window,
                  sinks, (int)block_table->shape[1], dev.num_sms, scratch, opts, &plan);

@@ -272,6 +272,12 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
 // device status word.  Returns a pd_status.
 int device_check(int *num_sms, unsigned int **status);
 
+// The rows of out from query_start[num_seqs] on as zeros, in a launch of its own
+// (pd_padding.cu), for a batch whose requests have no rows.  out's rows are
+// checked, and at least one.
+int zero_padding(const pd_tensor *out, const int32_t *query_start, int num_seqs, int num_sms,
+                 void *stream);
+
 // Argument check of a paged cache pool descriptor and of a [rows, Hq, D]
 // token-row descriptor, and the TMA tensor map of a pool (pd_api.cu).
 int check_cache_tensor(const pd_tensor *t, int layout, int Hkv, int P, int D);

@@ -263,13 +263,14 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
       !std::isfinite(scale))
     return PD_EINVAL;
   if (layout != PD_NHD && layout != PD_HND) return PD_EINVAL;
-  if (seq_lens->ndim != 1 || !seq_lens->data || seq_lens->stride[0] != 1) return PD_EINVAL;
+  if (seq_lens->ndim != 1 || seq_lens->stride[0] != 1) return PD_EINVAL;
   if (seq_lens->dtype != PD_I32 || block_table->dtype != PD_I32 || query_start->dtype != PD_I32 ||
       work->dtype != PD_I32)
     return PD_EDTYPE;
   const int64_t S = seq_lens->shape[0];
-  if (S < 0 || S > INT32_MAX) return PD_EINVAL;
-  if (block_table->ndim != 2 || !block_table->data || block_table->shape[0] != S ||
+  // (of no request: any pointer)
+  if (S < 0 || S > INT32_MAX || (S > 0 && (!seq_lens->data || !block_table->data))) return PD_EINVAL;
+  if (block_table->ndim != 2 || block_table->shape[0] != S ||
       block_table->shape[1] < 1 || block_table->stride[1] != 1 || block_table->stride[0] < 0)
     return PD_EINVAL;
   if (block_table->shape[1] * (int64_t)page_size > INT32_MAX) return PD_EINVAL;
@@ -302,11 +303,14 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
       work->stride[1] != 1 || work->stride[0] != 8 || (info->num_items > 0 && !work->data) ||
       (reinterpret_cast<uintptr_t>(work->data) & 15u) != 0)
     return PD_EINVAL;
-  if (S == 0 || T == 0 || info->num_items == 0) return PD_OK;
+  if (T == 0) return PD_OK;
 
   int num_sms = 0;
   unsigned int *status = nullptr;
   if ((rc = device_check(&num_sms, &status)) != PD_OK) return rc;
+  // (no tile: the rows are padding)
+  if (S == 0 || info->num_items == 0)
+    return zero_padding(out, static_cast<const int32_t *>(query_start->data), (int)S, num_sms, stream);
   PrefillShape sh;
   if ((rc = prefill_shape(head_size, sinks > 0 && window > 0, &sh)) != PD_OK) return rc;
 
