@@ -158,7 +158,7 @@ int encode_cache_map(const pd_tensor *t, int layout, CUtensorMap *out, bool one_
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_rows_tensor(const pd_tensor *t, int64_t rows, int Hq, int D) {
-  if (!t || !t->data || t->ndim != 3) return PD_EINVAL;
+  if (!t || t->ndim != 3 || (!t->data && rows != 0)) return PD_EINVAL;  // (empty: any pointer)
   if (t->shape[0] != rows || t->shape[1] != Hq || t->shape[2] != D) return PD_EINVAL;
   if (t->dtype != PD_F16 && t->dtype != PD_BF16) return PD_EDTYPE;
   if (t->stride[2] != 1) return PD_EALIGN;
@@ -569,7 +569,7 @@ int attn_impl(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_c
         query_start->stride[0] != 1)
       return PD_EINVAL;
     if (!element_dtype_ok(query_start, PD_I32)) return PD_EDTYPE;
-    if (!q->data || q->ndim != 3) return PD_EINVAL;
+    if (q->ndim != 3) return PD_EINVAL;
     T = q->shape[0];
     if (T < 0 || T > INT32_MAX) return PD_EINVAL;
   }

@@ -66,3 +66,26 @@ def test_requests_still_need_their_lengths_and_tables():
         kept, descs[k].data = descs[k].data, None
         assert call() == -1, k
         descs[k].data = kept
+
+
+@pytest.mark.parametrize("S", [0, 2])
+def test_no_rows_is_nothing_to_do(S):
+    for sinks in (0, 4):
+        assert _decode(S, 0, sinks) == 0 and _prefill(S, 0, sinks) == 0
+    # max_query_len rows to a request, and no request
+    c, table, lens, _ = _case(0, 0)
+    args = (8, 2, 128, 16, 1, 20)
+    assert pd.paged_decode_attn(c.q, c.k_cache, c.v_cache, table, lens, torch.empty_like(c.q), *args, 0.1, W.HND,
+                                check=False) == 0
+    assert pd.paged_decode_attn_sinks(c.q, c.k_cache, c.v_cache, table, lens, torch.empty_like(c.q), *args, 4, 0.1,
+                                      W.HND, check=False) == 0
+
+
+def test_empty_rows_are_still_checked():
+    c, table, lens, start = _case(2, 0)
+    def call(q, out):
+        return pd.paged_decode_attn_varlen(q, c.k_cache, c.v_cache, table, lens, start, out, 8, 2, 128, 16, 1, 20,
+                                           0.1, W.HND, check=False)
+    assert call(c.q, c.q) == 0
+    assert call(c.q[:, :7], c.q) == -1 and call(c.q, c.q[..., :64]) == -1 and call(c.q, c.q.half()) == -2
+    assert call(c.q, torch.zeros(3, 8, 128, dtype=c.q.dtype)) == -1
