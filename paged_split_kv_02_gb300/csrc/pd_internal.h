@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "paged_decode.h"
+#include "pd_ranges.h"
 
 namespace pd {
 

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : RM && SINK
     pf_split = w1.x;
     pf_slot = w1.y;
     h = hg = blockIdx.y;
-    const bool ok = s >= 0 && s < p.num_seqs && grow >= 0 && grow <= (INT32_MAX - 64) / p.rows_cta &&
+    const bool ok = s >= 0 && s < p.num_seqs && tile_in_range(grow, p.rows_cta) &&
                     pf_nseg >= 1 && pf_nseg <= p.max_parts && seg >= 0 && seg < pf_nseg &&
                     (pf_nseg == 1 || (pf_split >= 0 && pf_split < p.pf_groups && pf_slot >= 0 &&
                                       pf_slot <= p.pf_slots - pf_nseg));

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
     };
     auto good = [&](const int4 &w0) {
       // (this launch has no split tiles: one segment each)
-      return w0.x >= 0 && w0.x < p.num_seqs && w0.y >= 0 && w0.y <= (INT32_MAX - 64) / ROWS &&
+      return w0.x >= 0 && w0.x < p.num_seqs && tile_in_range(w0.y, ROWS) &&
              w0.z == 0 && w0.w == 1;
     };
     auto lengths = [&](const int4 &w0, int &L, int &qa, int &qb) {
