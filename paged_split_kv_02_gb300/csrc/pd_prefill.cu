@@ -298,6 +298,8 @@ int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *
       info->num_split_tiles < 0 || info->num_slots < 0 || info->max_segments != kMaxSegments ||
       (own_rows && info->num_split_tiles != 0))
     return PD_EINVAL;
+  // (packed rows are ints)
+  if (T * (own_rows ? wp_padded(G) : G) > INT32_MAX) return PD_EINVAL;
   if (own_rows && T > 0 && (q->stride[0] == 0 || q->stride[1] == 0)) return PD_EALIGN;
   if (work->ndim != 2 || work->shape[0] != info->num_items || work->shape[1] != 8 ||
       work->stride[1] != 1 || work->stride[0] != 8 || (info->num_items > 0 && !work->data) ||

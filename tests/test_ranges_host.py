@@ -7,8 +7,11 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
+import paged_split_kv_02_gb300 as pd
 from paged_split_kv_02_gb300 import _build
+from paged_split_kv_02_gb300 import workloads as W
 
 INT_MAX = 2 ** 31 - 1
 
@@ -41,3 +44,23 @@ def test_a_tile_that_is_taken_has_rows_that_are_ints(lib, rows):
         if not -INT_MAX - 1 <= tile <= INT_MAX:
             continue
         assert bool(lib.in_range(tile, rows)) == (tile >= 0 and (tile + 1) * rows <= INT_MAX), (tile, rows)
+
+
+def test_prefill_refuses_more_packed_rows_than_an_int():
+    """q and out as one row, broadcast (never read here: the call ends at the
+    missing device)."""
+    if torch.cuda.is_available():
+        pytest.skip("host tensors: for machines without a GPU")
+    pd.build()
+    c = W.make_prefill_case("rows", seed=1, q_lens=[4], contexts=[60], num_q_heads=12, num_kv_heads=2, window=16)
+    narrow = pd.paged_prefill_plan([0, 4], [64], 12, 2, 128, 16, 152)
+    wide = pd.paged_prefill_plan_sinks([0, 4], [64], 12, 2, 128, 16, 4, 152)
+    assert (narrow[1].tile_rows, wide[1].tile_rows) == (256, 192)
+
+    def call(T, plan):
+        q = torch.zeros(1, 12, 128, dtype=c.q.dtype).expand(T, 12, 128)
+        return pd.paged_prefill_attn_sinks(q, c.k_cache, c.v_cache, c.block_table, c.seq_lens, c.query_start,
+                                           plan[0], plan[1], q, 12, 2, 128, 16, 16, 4, 0.1, W.HND, check=False)
+    # six heads to a kv head; padded to eight in the other plan (which wants strides: PD_EALIGN)
+    assert call(INT_MAX // 6, narrow) == -8 and call(INT_MAX // 6 + 1, narrow) == -1
+    assert call(INT_MAX // 8, wide) == -5 and call(INT_MAX // 8 + 1, wide) == -1
