@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
     const int last = min(rr0 + ROWS, t.rows) - 1;
     t.u_lo = t.u_hi = 0;
     if (last >= rr0) {
-      t.u_hi = max(L - ml + (last >> lg_g) + 1, 0);
-      t.u_lo = max(0, max(L - ml + (rr0 >> lg_g) + 1, 0) - p.window);
+      t.u_hi = row_keys(L, ml, last >> lg_g, p.window).hi;
+      t.u_lo = row_keys(L, ml, rr0 >> lg_g, p.window).lo;
     }
     const int first = t.u_lo / kBlockKeys;
     t.sk_nb = (min(p.sinks, t.u_hi) + kBlockKeys - 1) / kBlockKeys;
@@ -391,11 +391,8 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
       const int rr = t.rr0 + kTpRows * X + 32 * (warp & 3) + lane;
       const int rr_q = rr & ((1 << lg_g) - 1);  // q head of the kv head's
       const bool live = rr < t.rows && rr_q < p.G;
-      int lo = 0, hi = 0;
-      if (live) {
-        hi = max(t.L - t.ml + (rr >> lg_g) + 1, 0);
-        lo = max(0, hi - p.window);
-      }
+      const RowKeys keys = live ? row_keys(t.L, t.ml, rr >> lg_g, p.window) : RowKeys{0, 0};
+      const int lo = keys.lo, hi = keys.hi;
       const int ntile = (t.nb + TB - 1) / TB;
       // The run of the tile's blocks leaves this many keys out, behind the
       // sinks: key k past them is the run's k - hole.  (No row sees keys of
@@ -409,9 +406,10 @@ __global__ void __launch_bounds__(wp_threads(D), 1)
       // Stages whose keys every row of the half sees: [0, j_sinks) and [j_lo, j_hi).
       int j_sinks, j_lo, j_hi;
       {
-        const int first = t.rr0 + kTpRows * X, last = min(first + kTpRows, t.rows) - 1;
-        const int h_hi = max(t.L - t.ml + (first >> lg_g) + 1, 0);
-        const int h_lo = max(0, t.L - t.ml + (last >> lg_g) + 1 - p.window);
+        // (a half without rows: any of these)
+        const int last = min(t.rr0 + kTpRows * (X + 1), t.rows) - 1, first = min(t.rr0 + kTpRows * X, last);
+        const int h_hi = row_keys(t.L, t.ml, first >> lg_g, p.window).hi;
+        const int h_lo = row_keys(t.L, t.ml, last >> lg_g, p.window).lo;
         j_sinks = min(p.sinks, h_hi) / SC;
         const int b_lo = max((h_lo + kBlockKeys - 1) / kBlockKeys - t.sk_gap, t.sk_gap > 0 ? t.sk_nb : 0);
         j_lo = (b_lo + TB - 1) / TB;
