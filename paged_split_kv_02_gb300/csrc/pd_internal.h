@@ -8,6 +8,7 @@
 
 #include "paged_decode.h"
 #include "pd_ranges.h"
+#include "pd_smem_limit.h"
 
 namespace pd {
 
@@ -223,6 +224,18 @@ inline int64_t epilogue_floats(int D, int NT, int KG, int CS, int ncl_max) {
   const int64_t final_merge = 2LL * ncl_max * nt8 + nt8 + 16 +
                               16LL * (kMaxThreads > kTpThreads ? kMaxThreads : kTpThreads) + D;
   return combine > final_merge ? combine : final_merge;
+}
+
+// A launch of kern on the current device with this much dynamic shared memory is
+// allowed from here on (limit: the instance's own).
+template <typename Kernel>
+cudaError_t allow_smem(SmemLimit &limit, Kernel kern, int bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= SmemLimit::kDevices)
+    return cudaErrorInvalidDevice;
+  return limit.raise(dev, bytes, [&](int b) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, b);
+  });
 }
 
 // path: 1 = mma.sync consumers, 2 = warp dot products (D <= 256, one 8-row

@@ -652,14 +652,9 @@ template <int D, bool BF16>
 cudaError_t launch_window_prefill_t(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq,
                                     const Params &p, const Launch &l, cudaStream_t stream) {
   auto kern = pd_window_prefill<D, BF16>;
-  static int configured_smem[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (l.smem > configured_smem[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, l.smem);
-    if (e != cudaSuccess) return e;
-    configured_smem[dev] = l.smem;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = allow_smem(limit, kern, l.smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = l.grid;
   cfg.blockDim = l.block;
