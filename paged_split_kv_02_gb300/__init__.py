@@ -223,8 +223,8 @@ def _step(name):
     if _bind is None:
         L = lib()
         if not os.path.exists(_build.BIND):
-            raise RuntimeError(f"{_build.BIND} is missing: build it with "
-                               "paged_split_kv_02_gb300.build()")
+            raise RuntimeError(f"{_build.BIND} is missing (one per Python and torch): build it "
+                               "with paged_split_kv_02_gb300.build()")
         loader = importlib.machinery.ExtensionFileLoader("_bind", _build.BIND)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bind", loader))
         loader.exec_module(m)

@@ -9,14 +9,25 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpaged_decode.so")
-BIND = os.path.join(HERE, "_bind.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
+
+
+def bind_path(python: str = sys.implementation.cache_tag, torch_version: str = torch.__version__) -> str:
+    """The module of the step calls for a Python and a torch: it reads tensors by
+    that torch's headers, so another's is another file."""
+    return os.path.join(HERE, f"_bind.{python}-torch{torch_version}.so")
+
+
+BIND = bind_path()
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fvisibility=hidden"]
@@ -35,25 +46,62 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")) + [BIND_SRC])
+            + glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")))
+
+
+def _bind_deps():
+    return glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")) + [BIND_SRC]
+
+
+def _newer(target, deps) -> bool:
+    """Was the target built after its last dependency changed?"""
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB, _deps())
+
+
+def bind_up_to_date() -> bool:
+    return _newer(BIND, _bind_deps())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every .cu under csrc/ and link libpaged_decode.so."""
-    if not force and up_to_date():
+    """Compile every .cu under csrc/ and link libpaged_decode.so, and compile the
+    step calls' module beside it."""
+    lib, bind = force or not up_to_date(), force or not bind_up_to_date()
+    if not lib and not bind:
         return LIB
     nvcc = _nvcc()
+    inc = ["-I" + os.path.join(os.path.dirname(HERE), "include")]
+    with cf.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
+        bound = ex.submit(_build_bind, nvcc, inc) if bind else None
+        if lib:
+            _build_lib(nvcc, inc, ex, verbose, extra_flags)
+        if bound:
+            bound.result()
+    return LIB
+
+
+def _build_bind(nvcc, inc):
+    root = os.path.dirname(torch.__file__)
+    tmp = BIND + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(cuda, "include"), BIND_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stderr}")
+    os.replace(tmp, BIND)
+
+
+def _build_lib(nvcc, inc, ex, verbose, extra_flags):
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
-    inc = ["-I" + os.path.join(os.path.dirname(HERE), "include")]
 
     def compile_one(pair):
         src, obj = pair
@@ -63,27 +111,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stderr}")
         return r.stderr
 
-    def bind():
-        import torch
-
-        root = os.path.dirname(torch.__file__)
-        libs = os.path.join(root, "lib")
-        tmp = BIND + f".tmp{os.getpid()}"
-        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
-               "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
-               "-isystem", os.path.join(cuda, "include"), BIND_SRC, "-o", tmp, "-L" + libs,
-               "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stderr}")
-        os.replace(tmp, BIND)
-
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        bound = ex.submit(bind)
-        logs = list(ex.map(compile_one, zip(srcs, objs)))
-        bound.result()
+    logs = list(ex.map(compile_one, zip(srcs, objs)))
     if verbose:
         for lg in logs:
             if lg.strip():
@@ -94,10 +122,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose=True))
