@@ -223,8 +223,10 @@ def _step(name):
     if _bind is None:
         L = lib()
         if not os.path.exists(_build.BIND):
+            lacks = _build.bind_missing()
             raise RuntimeError(f"{_build.BIND} is missing (one per Python and torch): build it "
-                               "with paged_split_kv_02_gb300.build()")
+                               "with paged_split_kv_02_gb300.build()"
+                               + (f", which needs {lacks}" if lacks else ""))
         loader = importlib.machinery.ExtensionFileLoader("_bind", _build.BIND)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bind", loader))
         loader.exec_module(m)

@@ -11,6 +11,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 import torch
 
@@ -53,6 +54,23 @@ def _bind_deps():
     return glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")) + [BIND_SRC]
 
 
+def _cxx():
+    return shutil.which("g++") or shutil.which("c++")
+
+
+def bind_missing() -> str:
+    """What the module needs to be compiled and is not here ('' : nothing).  The
+    library is built without it; the step calls then say so."""
+    if not _cxx():
+        return "a C++ compiler (g++ or c++)"
+    for path in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                 os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd",
+                              "python_variable.h")):
+        if not os.path.exists(path):
+            return path
+    return ""
+
+
 def _newer(target, deps) -> bool:
     """Was the target built after its last dependency changed?"""
     return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
@@ -68,8 +86,13 @@ def bind_up_to_date() -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every .cu under csrc/ and link libpaged_decode.so, and compile the
-    step calls' module beside it."""
+    step calls' module beside it (a machine without a C++ compiler or the headers
+    of Python or torch does without)."""
     lib, bind = force or not up_to_date(), force or not bind_up_to_date()
+    missing = bind_missing() if bind else ""
+    if missing:
+        bind = False
+        warnings.warn(f"the step calls are not built: {missing} is missing")
     if not lib and not bind:
         return LIB
     nvcc = _nvcc()
@@ -87,14 +110,14 @@ def _build_bind(nvcc, inc):
     root = os.path.dirname(torch.__file__)
     tmp = BIND + f".tmp{os.getpid()}"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+    cmd = [_cxx(), "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
            "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(cuda, "include"), BIND_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stderr}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed for bind.cpp:\n{r.stderr}")
     os.replace(tmp, BIND)
 
 

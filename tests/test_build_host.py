@@ -39,3 +39,20 @@ def test_another_torch_gets_its_own_module_and_the_library_stays(monkeypatch, tm
     made.clear()
     _build.build()
     assert sorted(made) == ["library", "module"]
+
+
+def test_a_machine_that_cannot_compile_the_module_still_has_the_library(monkeypatch, tmp_path):
+    made = []
+    monkeypatch.setattr(pd, "_bind", None)
+    monkeypatch.setattr(_build, "BIND", str(tmp_path / "_bind.other.so"))
+    monkeypatch.setattr(_build, "_build_lib", lambda *a: made.append("library"))
+    assert _build.bind_missing() == ""
+    monkeypatch.setattr(_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert _build.bind_missing() == str(tmp_path / "Python.h")
+    with pytest.warns(UserWarning, match="Python.h is missing"):
+        assert _build.build(force=True) == _build.LIB
+    assert made == ["library"] and pd.paged_decode_version() > 0
+    with pytest.raises(RuntimeError, match="needs .*Python.h"):
+        pd._step("attn_sinks")
+    monkeypatch.setattr(_build.shutil, "which", lambda name: None)
+    assert "compiler" in _build.bind_missing()
