@@ -13,6 +13,7 @@
 // tiles start in the first wave and the short ones fill the tail.
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <vector>
 
 #include "paged_decode.h"
@@ -169,12 +170,10 @@ int prefill_shape(int D, bool sinks, PrefillShape *sh) {
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
-}  // namespace
-
-int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int num_seqs,
-                      int num_q_heads, int num_kv_heads, int head_size, int window, int sinks,
-                      int num_sms, pd_prefill_item *items, int64_t capacity,
-                      pd_prefill_plan_info *info) {
+// The work list of a plan (paged_prefill_plan_sinks).
+int plan_items(const int32_t *query_start, const int32_t *seq_lens, int num_seqs, int num_q_heads,
+               int num_kv_heads, int head_size, int window, int sinks, int num_sms,
+               pd_prefill_item *items, int64_t capacity, pd_prefill_plan_info *info) {
   if (!info) return PD_EINVAL;
   if (!head_size_ok(head_size)) return PD_EHEAD;
   if (num_sms <= 0) {
@@ -239,6 +238,20 @@ int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int n
     }
   }
   return PD_OK;
+}
+
+}  // namespace
+
+int prefill_plan_call(const int32_t *query_start, const int32_t *seq_lens, int num_seqs,
+                      int num_q_heads, int num_kv_heads, int head_size, int window, int sinks,
+                      int num_sms, pd_prefill_item *items, int64_t capacity,
+                      pd_prefill_plan_info *info) {
+  try {
+    return plan_items(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_size, window,
+                      sinks, num_sms, items, capacity, info);
+  } catch (const std::exception &) {
+    return PD_EINVAL;  // more tiles than the host can list
+  }
 }
 
 int prefill_call(const pd_tensor *q, const pd_tensor *k_cache, const pd_tensor *v_cache,

@@ -1,7 +1,5 @@
 // Entry points of the attention over a window with sinks: the calls of
 // pd_api.cu and pd_prefill.cu with the sinks passed on.
-#include <exception>
-
 #include "paged_step.h"
 #include "pd_internal.h"
 
@@ -35,12 +33,8 @@ PD_API int paged_prefill_plan_sinks(const int32_t *query_start, const int32_t *s
                                     int head_size, int window, int sinks, int num_sms,
                                     pd_prefill_item *items, int64_t capacity,
                                     pd_prefill_plan_info *info) {
-  try {
-    return prefill_plan_call(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_size,
-                             window, sinks, num_sms, items, capacity, info);
-  } catch (const std::exception &) {
-    return PD_EINVAL;  // more tiles than the host can list
-  }
+  return prefill_plan_call(query_start, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                           window, sinks, num_sms, items, capacity, info);
 }
 
 PD_API int paged_prefill_attn_sinks(const pd_tensor *q, const pd_tensor *k_cache,
