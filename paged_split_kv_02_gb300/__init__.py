@@ -490,9 +490,12 @@ def rope_case(case, q_out=None, stream=None):
 
 def _prefill_plan(what, query_start, seq_lens, args):
     """(items int32 [n, 8] as a CPU tensor, info) of a prefill planner of the
-    library: a size query, then the items."""
+    library: a size query, then the items.  The lengths are the host's: a
+    tensor on a device is refused (its copy would wait for the GPU)."""
     qs = torch.as_tensor(query_start, dtype=torch.int32).contiguous()
     sl = torch.as_tensor(seq_lens, dtype=torch.int32).contiguous()
+    if qs.device.type != "cpu" or sl.device.type != "cpu" or qs.dim() != 1 or sl.dim() != 1:
+        raise PagedDecodeError(-1, what)
     S = int(sl.shape[0])
     if qs.shape[0] != S + 1:
         raise PagedDecodeError(-1, what)
