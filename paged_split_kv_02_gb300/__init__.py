@@ -34,6 +34,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import operator
 import os
 import re
 from typing import Optional
@@ -469,10 +470,12 @@ def paged_rope_axes_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache,
     """``paged_rope_cache_write`` with ``positions`` [axes, T]: rotated pair i
     takes its angle at the position of axis ``pair_axis[i]`` (``rot_dim / 2``
     small integers, as ``rope_pair_axis`` gives them)."""
+    if not isinstance(pair_axis, bytes):
+        # (bytes() of a number is as many zeros, of an array its memory)
+        pair_axis = bytes(operator.index(a) for a in pair_axis)
     rc = _step("rope_axes")(
         q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache, num_q_heads,
-        num_kv_heads, head_size, rot_dim, page_size, layout, bool(is_neox), bytes(pair_axis),
-        stream)
+        num_kv_heads, head_size, rot_dim, page_size, layout, bool(is_neox), pair_axis, stream)
     return _checked(rc, "paged_rope_axes_cache_write", check)
 
 
