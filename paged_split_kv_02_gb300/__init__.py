@@ -253,6 +253,13 @@ def options(**kw) -> PdOptions:
     return o
 
 
+def _ints(*values) -> tuple:
+    """The values, if they fit 32 bits (ctypes would keep the lowest 32)."""
+    if not all(-2 ** 31 <= v < 2 ** 31 for v in values):
+        raise OverflowError("an argument does not fit 32 bits")
+    return values
+
+
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
         if not torch.cuda.is_available():
@@ -404,8 +411,9 @@ def paged_decode_plan_sinks(num_seqs, num_q_heads, num_kv_heads, head_size, page
     """The launch plan of ``paged_decode_attn_sinks`` (host only)."""
     plan = PdPlan()
     sd = scratch.desc if scratch is not None else scratch_desc
-    rc = lib().paged_decode_plan_sinks(num_seqs, num_q_heads, num_kv_heads, head_size, page_size,
-                                       max_query_len, window, sinks, block_table_width, num_sms,
+    args = _ints(num_seqs, num_q_heads, num_kv_heads, head_size, page_size, max_query_len, window,
+                 sinks, block_table_width, num_sms)
+    rc = lib().paged_decode_plan_sinks(*args,
                                        ctypes.byref(sd) if sd is not None else None,
                                        ctypes.byref(opts) if opts is not None else None,
                                        ctypes.byref(plan))
@@ -530,8 +538,8 @@ def paged_prefill_plan_sinks(query_start, seq_lens, num_q_heads, num_kv_heads, h
                              sinks, num_sms=0):
     """The work list of ``paged_prefill_attn_sinks``."""
     return _prefill_plan("paged_prefill_plan_sinks", query_start, seq_lens,
-                         (int(num_q_heads), int(num_kv_heads), int(head_size), int(window),
-                          int(sinks), int(num_sms)))
+                         _ints(int(num_q_heads), int(num_kv_heads), int(head_size), int(window),
+                               int(sinks), int(num_sms)))
 
 
 def paged_prefill_scratch_bytes(num_kv_heads, head_size, num_sms) -> int:

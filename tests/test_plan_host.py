@@ -43,3 +43,16 @@ def test_lengths_on_the_gpu_are_refused(plan):
     for a, b in ((q.cuda(), s), (q, s.cuda()), (q.cuda(), s.cuda())):
         with pytest.raises(pd.PagedDecodeError, match="PD_EINVAL"):
             plan(a, b)
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1])
+def test_windows_and_sinks_past_32_bits_are_refused(value):
+    """(as the calls they plan for refuse them)"""
+    for window, sinks in ((value, 4), (64, value)):
+        with pytest.raises(OverflowError):
+            pd.paged_prefill_plan_sinks([0, 300], [900], 8, 2, 128, window, sinks, 152)
+        with pytest.raises(OverflowError):
+            pd.paged_decode_plan_sinks(1, 8, 2, 128, 16, 1, window, sinks, 100, 152)
+    most = 2 ** 31 - 1
+    assert pd.paged_prefill_plan_sinks([0, 300], [900], 8, 2, 128, np.int64(most), most, 152)[1].num_items > 0
+    assert pd.paged_decode_plan_sinks(1, 8, 2, 128, 16, 1, most, most, 100, 152)["path"] == 1
