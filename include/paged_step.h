@@ -2,12 +2,15 @@
  * paged_step.h — the calls around and beside paged_decode.h that a serving
  * step makes: attention over a sliding window whose first tokens stay
  * visible (sinks), the tables of a batch built on the GPU from its requests'
- * lengths, and the rotary embedding with a position per axis.  On one stream
- * and without a host round trip:
+ * lengths, and the rotary embedding with a position per axis.  On one stream:
  *     paged_batch_tables            block tables, starts, lengths, positions, slots
  *     (the model's projections)
  *     paged_rope_axes_cache_write   q, k rotated; k, v stored at the slots
  *     paged_decode_attn_sinks       or paged_prefill_attn_sinks
+ * A decode step makes no host round trip.  A prefill takes a work list that
+ * paged_prefill_plan_sinks makes on the host from the host's copy of the
+ * starts and lengths (known before the tables are: they are the lengths that
+ * paged_batch_tables is given, summed), and that is copied to the device.
  *
  * Types, layouts, scratch, streams, graph capture and errors are those of
  * paged_decode.h: every call is asynchronous on `stream`, allocates nothing,

@@ -143,21 +143,6 @@ __device__ __forceinline__ float exp2_or_zero(float x, float m) {
   return sfu_exp2(x - m);
 }
 
-// Rows at and past the last request's end (padding of a captured batch) see no
-// key: zeros, by the threads of one CTA.
-template <int D>
-__device__ __forceinline__ void zero_padding_rows(const Params &p) {
-  const int t0 = min(max(__ldg(p.query_start + p.num_seqs), 0), p.num_tokens);
-  const int per_row = p.Hq * (D / 8);
-#pragma unroll 1
-  for (int64_t i = threadIdx.x; i < (int64_t)(p.num_tokens - t0) * per_row; i += blockDim.x) {
-    const int t = t0 + (int)(i / per_row), rem = (int)(i - (int64_t)(t - t0) * per_row);
-    const int hq = rem / (D / 8), c = rem - hq * (D / 8);
-    *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(p.out) + (int64_t)t * p.o_s0 +
-                               (int64_t)hq * p.o_s1 + c * 8) = make_uint4(0u, 0u, 0u, 0u);
-  }
-}
-
 template <int D, bool BF16, bool TC, bool DOT, bool RM, bool TP, bool SINK>
 __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : RM && SINK ? kRmThreads : kMaxThreads,
                                   RM && SINK ? 2 : 1)
@@ -316,11 +301,13 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : RM && SINK
                                       pf_slot <= p.pf_slots - pf_nseg));
     if (!ok) {
       if (tid == 0) atomicOr(p.status, 0x80u);
-      if (blockIdx.x == 0 && blockIdx.y == 0) zero_padding_rows<D>(p);
-      return;
+      if (blockIdx.x != 0 || blockIdx.y != 0) return;
+      // (the CTA that writes the padding rows goes on, without rows of its own)
+      s = grow = seg = 0;
+      pf_nseg = 1;
     }
     rr0 = grow * p.rows_cta;
-    rr1 = rr0 + p.rows_cta;
+    rr1 = ok ? rr0 + p.rows_cta : 0;
     tok0 = token_of(rr0);
     tok1 = token_of(rr1 - 1);
     cl_id = seg;
@@ -1770,7 +1757,17 @@ __global__ void __launch_bounds__(TC ? kTcThreads : TP ? kTpThreads : RM && SINK
   };
   const int nrows = max(0, rr1v - rr0);  // valid rows of this CTA
   if (p.query_start && (prefill ? blockIdx.x == 0 && blockIdx.y == 0 : seg == 0 && hg == 0 && s == 0)) {
-    zero_padding_rows<D>(p);
+    // rows at and past the last request's end (padding of a captured batch)
+    // see no key: zeros
+    const int t0 = min(max(__ldg(p.query_start + p.num_seqs), 0), p.num_tokens);
+    const int per_row = p.Hq * (D / 8);
+#pragma unroll 1
+    for (int64_t i = tid; i < (int64_t)(p.num_tokens - t0) * per_row; i += blockDim.x) {
+      const int t = t0 + (int)(i / per_row), rem = (int)(i - (int64_t)(t - t0) * per_row);
+      const int hq = rem / (D / 8), c = rem - hq * (D / 8);
+      *reinterpret_cast<uint4 *>(obase + (int64_t)t * p.o_s0 + (int64_t)hq * p.o_s1 + c * 8) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
   }
 
   const int CS = p.CS;

@@ -33,8 +33,8 @@
 // after 2048, 32 / 8 heads of 128, window 1024, 4 sinks 142 us (206); 2 of 8192,
 // window 4096, 64 sinks 678 us (800), 64 % of the tensor peak; 1276 ragged
 // tokens, 16 / 4 heads of 64, window 700 17.7 us (30.6); 1024 tokens, 32 / 8
-// heads of 256, window 1024 62 us (64 rows on mma.sync 245), 4096 of window 4096
-// 694 (2942).  Not kept: a warp per
+// heads of 256, window 1024 63 us (64 rows on mma.sync 239), 4096 of window 4096
+// 695 (2912).  Not kept: a warp per
 // half for its S and its PV MMAs (the same); S of 128 keys at once, one buffer
 // per half (800 against 700, halves in turn 830); P handed over 32 keys at a
 // time (153 us for 142); O stored without the exchange
