@@ -226,7 +226,8 @@ PD_API int paged_decode_attn_opts(const pd_tensor *q, const pd_tensor *k_cache, 
  * [lo, seq_lens[s] - q_len_s + i + 1) (lo as in paged_decode_attn).  Rows at
  * and past query_start[S] (padding of a captured batch) see no key and are
  * written as zeros.
- *   q, out       [T, Hq, D] for any T >= 0 (T = 0: nothing to do)
+ *   q, out       [T, Hq, D] for any T >= 0 (T = 0: nothing to do; S = 0: every
+ *                row is padding); tensors without elements may be null
  *   query_start  [S + 1] int32 device array, non-decreasing, 0 <= entries <= T
  * The other arguments are those of paged_decode_attn_opts (opts may be
  * NULL; path 3 is not built for this call: PD_EINVAL).  Entries outside
@@ -403,6 +404,8 @@ PD_API size_t paged_prefill_scratch_bytes(int num_kv_heads, int head_size, int n
  *   work         [num_items, 8] int32 device copy of the plan's items
  *   info         the plan's info (host), made for this head_size
  *   scratch      needed when info->num_split_tiles > 0 (else may be NULL)
+ * T times the q heads of a kv head is at most 2^31 - 1.  A plan without items
+ * (every request empty, or none) leaves only the rows past the last request.
  * Items that do not fit the launch (a request, tile, segment or slot out of
  * range) are skipped and reported as PD_DEV_BAD_WORK. */
 PD_API int paged_prefill_attn(const pd_tensor *q, const pd_tensor *k_cache,

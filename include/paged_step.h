@@ -82,7 +82,7 @@ PD_API int paged_decode_plan_sinks(int num_seqs, int num_q_heads, int num_kv_hea
  * of 256 / G' tokens (128 / G' at head size 256), G' the q heads to a kv head
  * rounded up to a power of two, are then a tile (info.tile_rows).  But for
  * PD_PREFILL_TILE_ROWS_D128 at head size 128 such a plan wants q's strides above
- * 0 (else PD_EALIGN). */
+ * 0 (else PD_EALIGN), and T G' of at most 2^31 - 1. */
 PD_API int paged_prefill_plan_sinks(const int32_t *query_start, const int32_t *seq_lens,
                                     int num_seqs, int num_q_heads, int num_kv_heads,
                                     int head_size, int window, int sinks, int num_sms,

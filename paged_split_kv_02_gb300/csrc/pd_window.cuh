@@ -13,7 +13,11 @@
 //
 // The products are those of pd_kernel.cuh's mma.sync consumers: keys on the
 // MMA's M side, S^T = K Q^T and O^T += V^T P^T, Q's fragments in registers (so
-// head sizes up to 256), P rounded to the input type, all sums in fp32.
+// head sizes up to 256), all sums in fp32.  P is rounded to the input type, the
+// one rounding before the output's: the MMA takes 16-bit operands, and a pair of
+// them (P and its remainder) would double the PV products.  It adds a tenth to
+// the output's error, rms against 64 bits of the rms output: 64 sequences,
+// window 1024, bf16 0.00182, of the output's rounding alone 0.00166.
 //
 // Memory-bound: K and V of the visible keys are read once.  Measured with
 // CUDA events over graph replays (32 / 8 heads, D = 128, bf16, P = 16), in us,

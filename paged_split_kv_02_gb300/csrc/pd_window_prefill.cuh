@@ -28,6 +28,12 @@
 // with sinks only a tile's first stage takes a max (a masked stage 1900 cycles,
 // 3000 with its own max and tests); the row sums follow the hand-over of P.
 //
+// P is rounded to the input type, as the MMA's 16-bit operand (two operands, P
+// and its remainder, would double the PV products), and the row sums take it as
+// rounded, so that O is a mean by the weights used.  Error, rms against 64 bits
+// of the rms output: window 1024 bf16 0.00185, of the output's rounding alone
+// 0.00166; window 700 at head size 64 fp16 0.00024 and 0.00021.
+//
 // Measured (CUDA events over graph replays, bf16, P = 16; in brackets a CTA per
 // tile, at head size 64 tiles of 64 rows on mma.sync): 4 requests of 2048 tokens
 // after 2048, 32 / 8 heads of 128, window 1024, 4 sinks 142 us (206); 2 of 8192,
