@@ -27,6 +27,15 @@ and of ``include/paged_step.h``, the calls around them in a serving step:
   positions and cache slots of a batch, built on the GPU from its lengths
 * ``paged_rope_axes_cache_write(...)``: the rotary embedding with a position
   per axis (time, height, width); ``rope_pair_axis`` lays the axes out
+
+and of ``include/paged_quant.h``, the paged cache held in 8 bits:
+
+* ``quant_cache(...)``: empty pools of e4m3 codes and their scales
+* ``paged_rope_quant_cache_write(...)``: rotary embedding of q and k, k and v
+  quantised as they are stored
+* ``paged_quant_cache_read(...)``: requests' pages as 16-bit pages, for prefill
+* ``paged_decode_attn_quant(...)`` / ``paged_decode_plan_quant(...)``: decode
+  attention over the cache
 """
 
 from __future__ import annotations
@@ -56,11 +65,13 @@ DEV_WAIT_TIMEOUT, DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_BAD_QSTART = 0x1, 0x2, 0x4, 
 DEV_BAD_SCRATCH, DEV_BAD_POSITION, DEV_BAD_SLOT, DEV_BAD_WORK = 0x10, 0x20, 0x40, 0x80
 DEV_NO_PAGE = 0x100
 MAX_AXES = 8  # PD_MAX_AXES
+SCALE_TOKENS = 16  # PD_SCALE_TOKENS
 COUNTERS_PER_PAIR = 16  # PD_COUNTERS_PER_PAIR
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "paged_decode.h")
 STEP_HEADER = os.path.join(os.path.dirname(HEADER), "paged_step.h")
+QUANT_HEADER = os.path.join(os.path.dirname(HEADER), "paged_quant.h")
 
 
 class PagedDecodeError(RuntimeError):
@@ -179,13 +190,16 @@ def lib():
         L.paged_prefill_plan_sinks.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, i64,
                                                ctypes.POINTER(PdPrefillPlanInfo)]
         L.paged_prefill_plan_sinks.restype = i32
+        L.paged_decode_plan_quant.argtypes = [i32] * 10 + [ctypes.POINTER(PdScratch),
+                                                           ctypes.POINTER(PdPlan)]
+        L.paged_decode_plan_quant.restype = i32
         _lib = L
     return _lib
 
 
 def declared_symbols(header: str = HEADER) -> list:
-    """Function names a public header declares (paged_decode.h, or
-    ``STEP_HEADER``)."""
+    """Function names a public header declares (paged_decode.h,
+    ``STEP_HEADER`` or ``QUANT_HEADER``)."""
     text = open(header).read()
     return re.findall(r"PD_API\s+[\w\s\*]*?\b(paged_\w+)\s*\(", text)
 
@@ -197,7 +211,8 @@ def _strerror(code: int) -> str:
         return "?"
 
 
-_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.int32: 2, torch.float32: 3}
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.int32: 2, torch.float32: 3,
+           torch.float8_e4m3fn: 4}
 
 
 def tensor_desc(t: torch.Tensor) -> PdTensor:
@@ -216,7 +231,7 @@ _bind = None
 
 
 def _step(name):
-    """A call of paged_step.h as the ``_bind`` module makes it (bind.cpp): its
+    """A call of paged_step.h or paged_quant.h as the ``_bind`` module makes it (bind.cpp): its
     arguments in that file's order.  It returns the status, PD_EINVAL for
     tensors that are not on one CUDA device; a launch goes to the tensors'
     device, whichever is current."""
@@ -235,7 +250,9 @@ def _step(name):
         def address(f):
             return ctypes.cast(f, ctypes.c_void_p).value
         m.setup(address(L.paged_decode_attn_sinks), address(L.paged_prefill_attn_sinks),
-                address(L.paged_batch_tables), address(L.paged_rope_axes_cache_write))
+                address(L.paged_batch_tables), address(L.paged_rope_axes_cache_write),
+                address(L.paged_decode_attn_quant), address(L.paged_quant_cache_read),
+                address(L.paged_rope_quant_cache_write))
         _bind = m
     return getattr(_bind, name)
 
@@ -485,6 +502,87 @@ def paged_rope_axes_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache,
         q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache, num_q_heads,
         num_kv_heads, head_size, rot_dim, page_size, layout, bool(is_neox), pair_axis, stream)
     return _checked(rc, "paged_rope_axes_cache_write", check)
+
+
+def quant_cache(num_blocks, num_kv_heads, head_size, page_size, layout, packed=False, device=None):
+    """(k_cache, v_cache, k_scale, v_scale) of an empty 8-bit cache (see
+    paged_quant.h): e4m3 pools in the layout, K and V side by side if
+    ``packed``, and fp32 scales [num_blocks, page_size / 16, num_kv_heads]."""
+    if page_size <= 0 or page_size % SCALE_TOKENS or layout not in (NHD, HND):
+        raise PagedDecodeError(-1, "quant_cache")
+    shape = ((num_blocks, page_size, num_kv_heads) if layout == NHD
+             else (num_blocks, num_kv_heads, page_size))
+    device = device or "cuda"
+    if packed:
+        pool = torch.zeros(shape + (2 * head_size,), dtype=torch.uint8, device=device)
+        k, v = pool[..., :head_size], pool[..., head_size:]
+    else:
+        k, v = (torch.zeros(shape + (head_size,), dtype=torch.uint8, device=device) for _ in range(2))
+    scales = (num_blocks, page_size // SCALE_TOKENS, num_kv_heads)
+    return (k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn),
+            torch.zeros(scales, device=device), torch.zeros(scales, device=device))
+
+
+def paged_rope_quant_cache_write(q, k, v, positions, slot_mapping, cos_sin_cache, pair_axis, q_out,
+                                 k_cache, v_cache, k_scale, v_scale, num_q_heads, num_kv_heads,
+                                 head_size, rot_dim, page_size, layout, is_neox=True, stream=None,
+                                 check: bool = True) -> int:
+    """``paged_rope_axes_cache_write`` into an 8-bit cache: k and v are stored
+    as e4m3 codes, with a scale for each 16 tokens of a page and kv head (see
+    paged_quant.h).  ``q`` and ``q_out`` may both be None (k and v alone),
+    ``positions`` and ``cos_sin_cache`` with ``rot_dim`` 0, ``pair_axis``
+    for positions on one axis."""
+    if pair_axis is not None and not isinstance(pair_axis, bytes):
+        # (bytes() of a number is as many zeros, of an array its memory)
+        pair_axis = bytes(operator.index(a) for a in pair_axis)
+    rc = _step("quant_write")(
+        q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache, k_scale, v_scale,
+        num_q_heads, num_kv_heads, head_size, rot_dim, page_size, layout, bool(is_neox), pair_axis,
+        stream)
+    return _checked(rc, "paged_rope_quant_cache_write", check)
+
+
+def paged_quant_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out_table,
+                           k_out, v_out, num_kv_heads, head_size, page_size, layout, stream=None,
+                           check: bool = True) -> int:
+    """Requests' pages of an 8-bit cache as pages of the 16-bit pools ``k_out``
+    and ``v_out``: page ``block_table[s][j]`` to page ``out_table[s][j]``,
+    which an attention call then takes as its block table (see
+    paged_quant.h)."""
+    rc = _step("quant_read")(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out_table,
+                             k_out, v_out, num_kv_heads, head_size, page_size, layout, stream)
+    return _checked(rc, "paged_quant_cache_read", check)
+
+
+def paged_decode_attn_quant(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out,
+                            num_q_heads, num_kv_heads, head_size, page_size, max_query_len, window,
+                            sinks, scale, layout, scratch: Optional[Scratch] = None,
+                            query_start=None, stream=None, check: bool = True) -> int:
+    """The decode call over an 8-bit cache (see paged_quant.h): every key, or
+    with ``window`` the newest ones and the first ``sinks``; ``query_start``
+    as in ``paged_decode_attn_varlen``, or None for ``max_query_len`` query
+    tokens per sequence."""
+    rc = _step("quant_attn")(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, out, num_q_heads,
+        num_kv_heads, head_size, page_size, max_query_len, window, sinks, layout, scale,
+        None if scratch is None else ctypes.addressof(scratch.desc), stream)
+    return _checked(rc, "paged_decode_attn_quant", check)
+
+
+def paged_decode_plan_quant(num_seqs, num_q_heads, num_kv_heads, head_size, page_size,
+                            max_query_len, window, sinks, block_table_width, num_sms,
+                            scratch: Optional[Scratch] = None,
+                            scratch_desc: Optional[PdScratch] = None) -> dict:
+    """The launch plan of ``paged_decode_attn_quant`` (host only)."""
+    plan = PdPlan()
+    sd = scratch.desc if scratch is not None else scratch_desc
+    args = _ints(num_seqs, num_q_heads, num_kv_heads, head_size, page_size, max_query_len, window,
+                 sinks, block_table_width, num_sms)
+    rc = lib().paged_decode_plan_quant(*args, ctypes.byref(sd) if sd is not None else None,
+                                       ctypes.byref(plan))
+    if rc != PD_OK:
+        raise PagedDecodeError(rc, "paged_decode_plan_quant")
+    return plan.as_dict()
 
 
 def rope_case(case, q_out=None, stream=None):

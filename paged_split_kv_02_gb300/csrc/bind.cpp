@@ -1,4 +1,4 @@
-/* Argument marshalling of the calls of paged_step.h: tensors to descriptors,
+/* Argument marshalling of the calls of paged_step.h and paged_quant.h: tensors to descriptors,
  * the launch's device and stream, then the library's function.  A serving
  * step makes these calls between kernels of a few microseconds each, and the
  * host's part of a call is more than most of the kernels take: filling ctypes
@@ -16,7 +16,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
-#include "paged_step.h"
+#include "paged_quant.h"
 
 #define MAX_TENSORS 12
 
@@ -33,10 +33,25 @@ typedef int (*tables_fn)(const pd_tensor *, const pd_tensor *, const pd_tensor *
 typedef int (*rope_fn)(const pd_tensor *, const pd_tensor *, const pd_tensor *, const pd_tensor *,
                        const pd_tensor *, const pd_tensor *, const uint8_t *, pd_tensor *,
                        pd_tensor *, pd_tensor *, int, int, int, int, int, int, int, void *);
+typedef int (*quant_attn_fn)(const pd_tensor *, const pd_tensor *, const pd_tensor *,
+                             const pd_tensor *, const pd_tensor *, const pd_tensor *,
+                             const pd_tensor *, const pd_tensor *, pd_tensor *, int, int, int, int,
+                             int, int, int, float, int, pd_scratch *, void *);
+typedef int (*quant_read_fn)(const pd_tensor *, const pd_tensor *, const pd_tensor *,
+                             const pd_tensor *, const pd_tensor *, const pd_tensor *,
+                             const pd_tensor *, pd_tensor *, pd_tensor *, int, int, int, int,
+                             void *);
+typedef int (*quant_write_fn)(const pd_tensor *, const pd_tensor *, const pd_tensor *,
+                              const pd_tensor *, const pd_tensor *, const pd_tensor *,
+                              const uint8_t *, pd_tensor *, pd_tensor *, pd_tensor *, pd_tensor *,
+                              pd_tensor *, int, int, int, int, int, int, int, void *);
 static attn_fn g_attn;
 static prefill_fn g_prefill;
 static tables_fn g_tables;
 static rope_fn g_rope;
+static quant_attn_fn g_quant_attn;
+static quant_read_fn g_quant_read;
+static quant_write_fn g_quant_write;
 
 /* The descriptor of a tensor; its device's index (-1: not CUDA) in *device. */
 static bool fill(PyObject *o, pd_tensor *d, int *device) {
@@ -54,6 +69,7 @@ static bool fill(PyObject *o, pd_tensor *d, int *device) {
     case at::kBFloat16: d->dtype = PD_BF16; break;
     case at::kInt: d->dtype = PD_I32; break;
     case at::kFloat: d->dtype = PD_F32; break;
+    case at::kFloat8_e4m3fn: d->dtype = PD_E4M3; break;
     default: d->dtype = 99; /* a type the library does not take */
   }
   const at::IntArrayRef shape = t.sizes(), stride = t.strides();
@@ -216,13 +232,69 @@ static PyObject *rope_axes(PyObject *const *args, Py_ssize_t n) {
   });
 }
 
-/* setup(addresses of the four functions) */
+/* (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start,
+ *  out, Hq, Hkv, D, P, M, window, sinks, layout, scale, scratch, stream) */
+static PyObject *quant_attn(PyObject *const *args, Py_ssize_t n) {
+  call_args a;
+  int v[8];
+  if (!counted(n, 20) || !ints(args + 9, 8, v)) return NULL;
+  const float scale = (float)PyFloat_AsDouble(args[17]);
+  pd_scratch *scratch = (pd_scratch *)address(args[18]);
+  if (PyErr_Occurred() || !begin(args, 9, args[19], &a)) return NULL;
+  return call(a, [&] {
+    return g_quant_attn(a.p[0], a.p[1], a.p[2], a.p[3], a.p[4], a.p[5], a.p[6], a.p[7], a.p[8],
+                        v[0], v[1], v[2], v[3], v[4], v[5], v[6], scale, v[7], scratch, a.stream);
+  });
+}
+
+/* (k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out_table, k_out,
+ *  v_out, Hkv, D, P, layout, stream) */
+static PyObject *quant_read(PyObject *const *args, Py_ssize_t n) {
+  call_args a;
+  int v[4];
+  if (!counted(n, 14) || !ints(args + 9, 4, v)) return NULL;
+  if (!begin(args, 9, args[13], &a)) return NULL;
+  return call(a, [&] {
+    return g_quant_read(a.p[0], a.p[1], a.p[2], a.p[3], a.p[4], a.p[5], a.p[6], a.p[7], a.p[8],
+                        v[0], v[1], v[2], v[3], a.stream);
+  });
+}
+
+/* (q, k, v, positions, slot_mapping, cos_sin_cache, q_out, k_cache, v_cache,
+ *  k_scale, v_scale, Hq, Hkv, D, rot_dim, page_size, layout, is_neox,
+ *  pair_axis, stream) */
+static PyObject *quant_write(PyObject *const *args, Py_ssize_t n) {
+  call_args a;
+  int v[7];
+  if (!counted(n, 20) || !ints(args + 11, 7, v)) return NULL;
+  char *pairs = NULL;
+  if (args[18] != Py_None) {
+    Py_ssize_t count;
+    if (PyBytes_AsStringAndSize(args[18], &pairs, &count) < 0) return NULL;
+    if (count != v[3] / 2) {
+      PyErr_Format(PyExc_ValueError, "pair_axis has %zd entries, rot_dim / 2 is %d", count,
+                   v[3] / 2);
+      return NULL;
+    }
+  }
+  if (!begin(args, 11, args[19], &a)) return NULL;
+  return call(a, [&] {
+    return g_quant_write(a.p[0], a.p[1], a.p[2], a.p[3], a.p[4], a.p[5], (const uint8_t *)pairs,
+                         a.p[6], a.p[7], a.p[8], a.p[9], a.p[10], v[0], v[1], v[2], v[3], v[4],
+                         v[5], v[6], a.stream);
+  });
+}
+
+/* setup(addresses of the seven functions) */
 static PyObject *setup(PyObject *const *args, Py_ssize_t n) {
-  if (!counted(n, 4)) return NULL;
+  if (!counted(n, 7)) return NULL;
   g_attn = (attn_fn)PyLong_AsVoidPtr(args[0]);
   g_prefill = (prefill_fn)PyLong_AsVoidPtr(args[1]);
   g_tables = (tables_fn)PyLong_AsVoidPtr(args[2]);
   g_rope = (rope_fn)PyLong_AsVoidPtr(args[3]);
+  g_quant_attn = (quant_attn_fn)PyLong_AsVoidPtr(args[4]);
+  g_quant_read = (quant_read_fn)PyLong_AsVoidPtr(args[5]);
+  g_quant_write = (quant_write_fn)PyLong_AsVoidPtr(args[6]);
   if (PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
 }
@@ -240,7 +312,8 @@ static PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))entry<name>, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(setup), METHOD(attn_sinks), METHOD(prefill_sinks),
-                                METHOD(batch_tables), METHOD(rope_axes), {NULL, NULL, 0, NULL}};
+                                METHOD(batch_tables), METHOD(rope_axes), METHOD(quant_attn),
+                                METHOD(quant_read), METHOD(quant_write), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};
 

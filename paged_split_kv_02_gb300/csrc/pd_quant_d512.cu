@@ -1,0 +1,13 @@
+// Decode attention over an 8-bit cache, head size 512.
+#include "pd_quant_attn.cuh"
+
+namespace pd {
+
+cudaError_t launch_quant_d512(bool bf16, int nt, const QuantAttnParams &p, const Launch &l, cudaStream_t stream) {
+  switch (nt) {
+    case 1: return bf16 ? launch_quant_t<512, 1, true>(p, l, stream) : launch_quant_t<512, 1, false>(p, l, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pd

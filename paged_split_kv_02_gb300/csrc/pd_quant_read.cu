@@ -1,0 +1,197 @@
+// Pages of an 8-bit cache as 16-bit pages of a staging pool.
+//
+// A CTA takes 16-token blocks of the requests, one after the other over the grid;
+// a thread turns 16 codes into 16 values at a time, K and V of every head.  The
+// tables and lengths of the next block are on their way while this one's codes
+// are.  Memory-bound: 1 byte read and 2 written a value.
+#include "pd_quant.h"
+#include "pd_rope.cuh"
+
+namespace pd {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCtas = 8;  // of an SM
+
+struct OutPool {
+  unsigned short *data;
+  int64_t page, tok, head;
+};
+
+struct QuantReadParams {
+  QuantPool k, v;
+  OutPool ko, vo;
+  const int32_t *block_table, *out_table, *seq_lens;
+  int64_t bt_stride, ot_stride;
+  int S, width, Hkv, P, lg_row;  // lg_row: log2 of a row's 16-code chunks
+  int num_pages, num_out_pages;
+  unsigned int *status;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) pd_quant_read(const __grid_constant__ QuantReadParams p) {
+  grid_dependency_wait();
+  const int per_page = p.P / PD_SCALE_TOKENS;
+  const int64_t per_seq = (int64_t)p.width * per_page, total = per_seq * p.S;
+  const int n = (PD_SCALE_TOKENS * p.Hkv) << p.lg_row;  // chunks of K (or V) of a block
+  struct Item {
+    int len, src, dst, blk;
+  };
+  auto fetch = [&](int64_t i) -> Item {
+    Item it{0, -1, -1, 0};
+    if (i >= total) return it;
+    const int s = (int)(i / per_seq);
+    it.blk = (int)(i - s * per_seq);
+    it.len = __ldg(p.seq_lens + s);
+    const int j = it.blk / per_page;
+    it.src = __ldg(p.block_table + s * p.bt_stride + j);
+    it.dst = __ldg(p.out_table + s * p.ot_stride + j);
+    return it;
+  };
+  Item it = fetch(blockIdx.x);
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    const Item next = fetch(i + gridDim.x);
+    if (threadIdx.x == 0 && it.blk == 0 && it.len > (int64_t)p.width * p.P)
+      atomicOr(p.status, PD_DEV_BAD_SEQLEN);
+    const int left = it.len - it.blk * PD_SCALE_TOKENS;  // tokens of the block
+    if (left > 0 && it.src >= 0 && it.dst >= 0) {
+      if (it.src >= p.num_pages || it.dst >= p.num_out_pages) {
+        if (threadIdx.x == 0) atomicOr(p.status, PD_DEV_BAD_PAGE);
+      } else {
+        const int sub = it.blk % per_page;
+        constexpr int U = 4;
+        for (int c0 = threadIdx.x; c0 < 2 * n; c0 += U * kThreads) {
+          uint4 w[U];
+          float f[U];
+          unsigned short *to[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            int c = c0 + u * kThreads;
+            to[u] = nullptr;
+            if (c >= 2 * n) continue;
+            const bool is_v = c >= n;
+            if (is_v) c -= n;
+            const int ch = c & ((1 << p.lg_row) - 1), r = c >> p.lg_row;
+            const int tok = r & (PD_SCALE_TOKENS - 1), h = r / PD_SCALE_TOKENS;
+            if (tok >= left) continue;
+            const QuantPool &t = is_v ? p.v : p.k;
+            const OutPool &o = is_v ? p.vo : p.ko;
+            const int row = sub * PD_SCALE_TOKENS + tok;
+            w[u] = __ldcs(reinterpret_cast<const uint4 *>(t.codes + it.src * t.page + row * t.tok +
+                                                          h * t.head + 16 * ch));
+            f[u] = __ldg(t.scale + it.src * t.s_page + sub * t.s_blk + h * t.s_head);
+            to[u] = o.data + it.dst * o.page + row * o.tok + h * o.head + 16 * ch;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (!to[u]) continue;
+            const uint32_t words[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+            uint32_t out[8];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              uint32_t lo, hi;
+              asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+                  " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+                  : "=r"(lo), "=r"(hi)
+                  : "r"(words[z]));
+              const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+              const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+              out[2 * z] = Elem<BF16>::from2(a.x * f[u], a.y * f[u]);
+              out[2 * z + 1] = Elem<BF16>::from2(b.x * f[u], b.y * f[u]);
+            }
+            uint4 *at = reinterpret_cast<uint4 *>(to[u]);
+            at[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            at[1] = make_uint4(out[4], out[5], out[6], out[7]);
+          }
+        }
+      }
+    }
+    it = next;
+  }
+  grid_dependents_launch();
+}
+
+void out_pool(const pd_tensor *t, int layout, OutPool *o) {
+  o->data = static_cast<unsigned short *>(t->data);
+  pool_strides(t, layout, &o->page, &o->tok, &o->head);
+}
+
+}  // namespace
+}  // namespace pd
+
+using namespace pd;
+
+extern "C" PD_API int paged_quant_cache_read(const pd_tensor *k_cache, const pd_tensor *v_cache,
+                                             const pd_tensor *k_scale, const pd_tensor *v_scale,
+                                             const pd_tensor *block_table, const pd_tensor *seq_lens,
+                                             const pd_tensor *out_table, pd_tensor *k_out,
+                                             pd_tensor *v_out, int num_kv_heads, int head_size,
+                                             int page_size, int layout, void *stream) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out_table || !k_out ||
+      !v_out)
+    return PD_EINVAL;
+  if (num_kv_heads <= 0) return PD_EINVAL;
+  if (head_size != 64 && head_size != 128 && head_size != 256 && head_size != 512) return PD_EHEAD;
+  if (page_size <= 0 || page_size % PD_SCALE_TOKENS != 0 || (layout != PD_NHD && layout != PD_HND))
+    return PD_EINVAL;
+  int rc;
+  QuantReadParams p{};
+  if ((rc = quant_pool(k_cache, k_scale, layout, num_kv_heads, page_size, head_size, &p.k)) != PD_OK)
+    return rc;
+  if ((rc = quant_pool(v_cache, v_scale, layout, num_kv_heads, page_size, head_size, &p.v)) != PD_OK)
+    return rc;
+  if (k_cache->shape[0] != v_cache->shape[0]) return PD_EINVAL;
+  if ((rc = check_cache_tensor(k_out, layout, num_kv_heads, page_size, head_size)) != PD_OK) return rc;
+  if ((rc = check_cache_tensor(v_out, layout, num_kv_heads, page_size, head_size)) != PD_OK) return rc;
+  if (k_out->dtype != v_out->dtype) return PD_EDTYPE;
+  if (k_out->shape[0] != v_out->shape[0]) return PD_EINVAL;
+  if (seq_lens->ndim != 1) return PD_EINVAL;
+  const int64_t S = seq_lens->shape[0];
+  if (S < 0 || S > INT32_MAX) return PD_EINVAL;
+  if ((rc = check_i32_vector(seq_lens, S)) != PD_OK) return rc;
+  for (const pd_tensor *t : {block_table, out_table}) {
+    if (t->ndim != 2 || t->shape[0] != S || t->shape[1] < 1 || t->shape[1] != block_table->shape[1] ||
+        t->stride[1] != 1 || t->stride[0] < 0 || (!t->data && S > 0))
+      return PD_EINVAL;
+    if (t->dtype != PD_I32) return PD_EDTYPE;
+  }
+  const int64_t W = block_table->shape[1];
+  if (W > INT32_MAX || W * page_size > INT32_MAX) return PD_EINVAL;
+  // (a block's chunks are ints)
+  if ((int64_t)num_kv_heads * head_size > (1 << 24)) return PD_EINVAL;
+  if (S == 0) return PD_OK;
+  int num_sms = 0;
+  if ((rc = device_check(&num_sms, &p.status)) != PD_OK) return rc;
+  out_pool(k_out, layout, &p.ko);
+  out_pool(v_out, layout, &p.vo);
+  p.block_table = static_cast<const int32_t *>(block_table->data);
+  p.out_table = static_cast<const int32_t *>(out_table->data);
+  p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
+  p.bt_stride = block_table->stride[0];
+  p.ot_stride = out_table->stride[0];
+  p.S = (int)S;
+  p.width = (int)W;
+  p.Hkv = num_kv_heads;
+  p.P = page_size;
+  for (p.lg_row = 0; (16 << p.lg_row) < head_size; ++p.lg_row) {
+  }
+  p.num_pages = (int)k_cache->shape[0];
+  p.num_out_pages = (int)k_out->shape[0];
+  const int64_t items = S * W * (page_size / PD_SCALE_TOKENS);
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(items < (int64_t)kCtas * num_sms ? items : (int64_t)kCtas * num_sms));
+  cfg.blockDim = dim3(kThreads);
+  const cudaError_t e = k_out->dtype == PD_BF16 ? cudaLaunchKernelEx(&cfg, pd_quant_read<true>, p)
+                                                : cudaLaunchKernelEx(&cfg, pd_quant_read<false>, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return PD_ECUDA;
+  }
+  return PD_OK;
+}

@@ -1,0 +1,541 @@
+// The rotary embedding of q and k and the store of k and v into an 8-bit cache.
+//
+// Two kinds of CTAs.  Of q: a token, rotated as in pd_rope_axes.cu (the angles in
+// shared memory once, a thread keeps one 16-byte chunk of dims and walks the heads).
+// Of k and v: the runs of tokens that begin in a few neighbouring tokens; a run
+// is the new tokens of one 16-token block, and a unit of work is a run's K or V
+// of one kv head, 16 rows at most, held in fp32 in the registers of one warp (two at
+// head size 256, four at 512) from the load to the codes: read once, the largest
+// magnitude by shuffles, then scaled and stored, 8 codes a lane.  An appended
+// block's other codes are read and written again where its scale grows.
+//
+// The rotation rounds each product and the sum (no fused multiply-add), so that a
+// code, which sits on a rounding, does not depend on how a compiler pairs them.
+//
+// Memory-bound: every byte is read or written once but for the rescaled codes.
+#include "pd_quant.h"
+#include "pd_rope.cuh"
+
+namespace pd {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kMaxPairs = 256;  // rot_dim / 2 at head size 512
+constexpr int kLeast = -64;     // the exponent of the least scale
+
+struct QuantWriteParams {
+  const void *q, *k, *v;
+  int64_t q_s0, q_s1, k_s0, k_s1, v_s0, v_s1;
+  void *q_out;
+  int64_t qo_s0, qo_s1;
+  QuantPool kc, vc;
+  const int32_t *positions, *slots;
+  int64_t pos_stride;
+  const float *cos_sin;
+  int64_t cs_s0;
+  int max_pos, T, Hq, Hkv, rot, P, axes;
+  int64_t num_slots;
+  int window, slices, units;  // tokens of a k/v CTA, CTAs of a window, units of one
+  int kv_ctas;                // k/v CTAs come first
+  unsigned int *status;
+  uint8_t axis[kMaxPairs];
+};
+
+__device__ __forceinline__ void turn(float a, float b, float c, float s, float &x, float &y) {
+  x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+
+// The angles of token t's pairs to cs (cos, then sin), by n threads.
+__device__ __forceinline__ void load_angles(const QuantWriteParams &p, int t, float *cs, int me, int n,
+                                            bool report) {
+  const int half = p.rot >> 1;
+  if (report && me < p.axes) {
+    const int pos = __ldg(p.positions + me * p.pos_stride + t);
+    if (pos < 0 || pos >= p.max_pos) atomicOr(p.status, PD_DEV_BAD_POSITION);
+  }
+  for (int i = me; i < half; i += n) {
+    const int pos = __ldg(p.positions + p.axis[i] * p.pos_stride + t);
+    const float *row = p.cos_sin + (int64_t)min(max(pos, 0), p.max_pos - 1) * p.cs_s0;
+    cs[i] = __ldg(row + i);
+    cs[half + i] = __ldg(row + half + i);
+  }
+}
+
+// q of kThreads / kGroup tokens, kGroup threads each, kU heads in flight.
+template <int D, bool BF16, bool NEOX, int kGroup, int kU>
+__device__ __forceinline__ void q_tokens(const QuantWriteParams &p, int t0, float *smem) {
+  constexpr int kPairs = NEOX ? 8 : 4;  // pairs of a chunk
+  const int me = threadIdx.x % kGroup, t = t0 + threadIdx.x / kGroup;
+  float *cs = smem + (threadIdx.x / kGroup) * p.rot;
+  const int half = p.rot >> 1, chunks = half / kPairs;
+  const bool live = t < p.T;
+  // (coherent loads: q_out may be q, and a thread reads what it writes, before)
+  auto src = [&](int h, int d) -> const uint4 * {
+    return reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(p.q) + (int64_t)t * p.q_s0 +
+                                           (int64_t)h * p.q_s1 + d);
+  };
+  auto dst = [&](int h, int d) -> uint4 * {
+    return reinterpret_cast<uint4 *>(static_cast<unsigned short *>(p.q_out) + (int64_t)t * p.qo_s0 +
+                                     (int64_t)h * p.qo_s1 + d);
+  };
+  const int wide = max(min(chunks, kGroup), 1);  // chunks taken at a time
+  const int h0 = me / wide, c0 = me - h0 * wide, hs = kGroup / wide;
+  const int first = live && chunks > 0 && h0 < hs ? h0 : p.Hq;
+  uint4 w1[kU], w2[kU];
+  auto load = [&](int hh, int c) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int h = hh + u * hs;
+      w1[u] = w2[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (h >= p.Hq || c >= chunks) continue;
+      w1[u] = *src(h, 8 * c);
+      if (NEOX) w2[u] = *src(h, half + 8 * c);
+    }
+  };
+  load(first, c0);
+  if (live && p.rot > 0) load_angles(p, t, cs, me, kGroup, true);
+  if (live) {
+    // dims past rot_dim
+    constexpr int kW = 4;
+    const int pass = (D - p.rot) / 8, n = p.Hq * pass;
+#pragma unroll 1
+    for (int i0 = me; i0 < n; i0 += kW * kGroup) {
+      uint4 w[kW];
+#pragma unroll
+      for (int u = 0; u < kW; ++u) {
+        const int i = i0 + u * kGroup;
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < n) w[u] = *src(i / pass, p.rot + 8 * (i % pass));
+      }
+#pragma unroll
+      for (int u = 0; u < kW; ++u) {
+        const int i = i0 + u * kGroup;
+        if (i < n) *dst(i / pass, p.rot + 8 * (i % pass)) = w[u];
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int c = c0; c < chunks; c += wide) {
+    if (c != c0) load(first, c);
+    float co[kPairs], si[kPairs];
+#pragma unroll
+    for (int e = 0; e < kPairs; e += 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(cs + kPairs * c + e);
+      const float4 b = *reinterpret_cast<const float4 *>(cs + half + kPairs * c + e);
+      co[e] = a.x; co[e + 1] = a.y; co[e + 2] = a.z; co[e + 3] = a.w;
+      si[e] = b.x; si[e + 1] = b.y; si[e + 2] = b.z; si[e + 3] = b.w;
+    }
+#pragma unroll 1
+    for (int hh = first; hh < p.Hq; hh += kU * hs) {
+      uint4 v1[kU], v2[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        v1[u] = w1[u];
+        v2[u] = w2[u];
+      }
+      if (hh + kU * hs < p.Hq) load(hh + kU * hs, c);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int h = hh + u * hs;
+        if (h >= p.Hq) continue;
+        float x1[8], y1[8];
+        unpack8<BF16>(v1[u], x1);
+        if constexpr (NEOX) {
+          float x2[8], y2[8];
+          unpack8<BF16>(v2[u], x2);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) turn(x1[e], x2[e], co[e], si[e], y1[e], y2[e]);
+          *dst(h, 8 * c) = pack8<BF16>(y1);
+          *dst(h, half + 8 * c) = pack8<BF16>(y2);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) turn(x1[2 * e], x1[2 * e + 1], co[e], si[e], y1[2 * e], y1[2 * e + 1]);
+          *dst(h, 8 * c) = pack8<BF16>(y1);
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ void floats4(uint32_t w, float (&x)[4]) {
+  uint32_t lo, hi;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+
+// The smallest power of two, 2^kLeast at least, under which a is at most 448 =
+// 1.75 x 2^8.
+__device__ __forceinline__ float least_scale(float a) {
+  const uint32_t bits = __float_as_uint(a);
+  const int e = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  return __uint_as_float((uint32_t)(max(e, kLeast) + 127) << 23);
+}
+
+template <int D, bool BF16, bool NEOX>
+__device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, float *smem) {
+  constexpr int WU = D > 128 ? D / 128 : 1;  // warps of a unit
+  constexpr int SLOTS = kThreads / 32 / WU;  // units at a time
+  constexpr int CPR = D / 8;                 // 16-byte chunks of a row
+  constexpr int RPP = 32 * WU / CPR;         // rows that a unit's lanes hold at once
+  constexpr int NP = PD_SCALE_TOKENS / RPP;
+  __shared__ int slot_of[16 + 2 * PD_SCALE_TOKENS];  // of tokens t0 - 1 ..
+  __shared__ float top[kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wi = cta / p.slices, slice = cta - wi * p.slices;
+  const int t0 = wi * p.window;
+  const int u0 = slice * p.units, nu = min(p.units, 2 * p.Hkv - u0);
+  for (int i = tid; i < p.window + 16; i += kThreads) {
+    const int t = t0 - 1 + i;
+    int s = t >= 0 && t < p.T ? __ldg(p.slots + t) : -1;
+    if (s >= 0 && s >= p.num_slots) {
+      if (slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
+      s = -1;
+    }
+    slot_of[i] = s;
+  }
+  __syncthreads();
+  // the runs that begin here: a lane looks at a token
+  int n = 0;
+  uint32_t written = 0;
+  {
+    const int s = lane < p.window ? slot_of[lane + 1] : -1;
+    const int blk = s / PD_SCALE_TOKENS, before = slot_of[min(lane, p.window)];
+    if (s >= 0 && (before < 0 || before / PD_SCALE_TOKENS != blk)) {
+      int last = s;
+      written = 1u << (s & 15);
+      for (n = 1; n < PD_SCALE_TOKENS; ++n) {
+        // (lane + 1 + n <= window + 15)
+        const int next = slot_of[lane + 1 + n];
+        if (next < 0 || next / PD_SCALE_TOKENS != blk) break;
+        if (next <= last) {
+          if (slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
+          break;
+        }
+        last = next;
+        written |= 1u << (next & 15);
+      }
+    }
+  }
+  const uint32_t begins = __ballot_sync(0xffffffffu, n > 0);
+  if (begins == 0) return;  // (every warp alike)
+  const int n_runs = __popc(begins);
+  const int lead0 = __ffs(begins) - 1, lead1 = 31 - __clz(begins);
+  const int t_end = lead1 + __shfl_sync(0xffffffffu, n, lead1);
+  if (u0 < p.Hkv && p.rot > 0) {
+    // (a warp a token)
+    for (int j = lead0 + warp; j < t_end; j += kThreads / 32)
+      load_angles(p, t0 + j, smem + (j - lead0) * p.rot, lane, 32, p.q == nullptr);
+    __syncthreads();
+  }
+  const int half = p.rot >> 1;
+  const int slot = warp / WU, ut = tid - slot * (32 * WU), ch = ut % CPR, r0 = ut / CPR;
+  const int work = n_runs * nu, rounds = (work + SLOTS - 1) / SLOTS;
+#pragma unroll 1
+  for (int it = 0; it < rounds; ++it) {
+    const int e = it * SLOTS + slot;
+    const bool on = e < work;
+    const int run = on ? e / nu : 0, u = u0 + (on ? e - run * nu : 0);
+    const int lead = __fns(begins, 0, run + 1);
+    const int rn = __shfl_sync(0xffffffffu, n, lead);
+    const uint32_t mask = __shfl_sync(0xffffffffu, written, lead);
+    const bool is_k = u < p.Hkv;
+    const int h = is_k ? u : u - p.Hkv;
+    const QuantPool &pool = is_k ? p.kc : p.vc;
+    const int first_slot = slot_of[lead + 1];
+    const int page = first_slot / p.P, sub = (first_slot - page * p.P) / PD_SCALE_TOKENS;
+    float *scale_at = pool.scale + page * pool.s_page + sub * pool.s_blk + h * pool.s_head;
+    unsigned char *codes = pool.codes + page * pool.page + (int64_t)(sub * PD_SCALE_TOKENS) * pool.tok +
+                           h * pool.head + 8 * ch;
+    const unsigned short *src = is_k ? static_cast<const unsigned short *>(p.k) + (int64_t)h * p.k_s1
+                                     : static_cast<const unsigned short *>(p.v) + (int64_t)h * p.v_s1;
+    const int64_t row = is_k ? p.k_s0 : p.v_s0;
+    const int t = t0 + lead;
+    const bool turned = is_k && 8 * ch < p.rot;
+    float x[NP][8];
+    float a = 0.f, old = 0.f;
+    if (on) {
+      old = *scale_at;
+      uint4 w[NP], o[NP];
+      const int other = NEOX ? (8 * ch < half ? 8 * ch + half : 8 * ch - half) : 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int j = r0 + RPP * i;
+        w[i] = o[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (j < rn) {
+          w[i] = __ldg(reinterpret_cast<const uint4 *>(src + (t + j) * row + 8 * ch));
+          if (NEOX && turned) o[i] = __ldg(reinterpret_cast<const uint4 *>(src + (t + j) * row + other));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int j = r0 + RPP * i;
+        unpack8<BF16>(w[i], x[i]);
+        if (turned && j < rn) {
+          const float *cs = smem + (lead - lead0 + j) * p.rot;
+          if constexpr (NEOX) {
+            float y[8];
+            unpack8<BF16>(o[i], y);
+            const bool low = 8 * ch < half;
+            const float *c = cs + (low ? 8 * ch : 8 * ch - half);
+#pragma unroll
+            for (int e4 = 0; e4 < 8; e4 += 4) {
+              const float4 co = *reinterpret_cast<const float4 *>(c + e4);
+              const float4 si = *reinterpret_cast<const float4 *>(c + half + e4);
+              const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                float lo, hi;
+                if (low) {
+                  turn(x[i][e4 + z], y[e4 + z], cc[z], ss[z], lo, hi);
+                  x[i][e4 + z] = lo;
+                } else {
+                  turn(y[e4 + z], x[i][e4 + z], cc[z], ss[z], lo, hi);
+                  x[i][e4 + z] = hi;
+                }
+              }
+            }
+          } else {
+            const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * ch);
+            const float4 si = *reinterpret_cast<const float4 *>(cs + half + 4 * ch);
+            const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              float lo, hi;
+              turn(x[i][2 * z], x[i][2 * z + 1], cc[z], ss[z], lo, hi);
+              x[i][2 * z] = lo;
+              x[i][2 * z + 1] = hi;
+            }
+          }
+        }
+#pragma unroll
+        for (int e8 = 0; e8 < 8; ++e8) {
+          const float m = fabsf(x[i][e8]);
+          a = fmaxf(a, m < INFINITY ? m : 0.f);  // (of finite values)
+        }
+      }
+    }
+    uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(a));  // (>= 0: ordered as integers)
+    if constexpr (WU > 1) {
+      if (lane == 0) top[warp] = __uint_as_float(bits);
+      __syncthreads();  // (and every lane has the old scale)
+      a = top[slot * WU];
+#pragma unroll
+      for (int i = 1; i < WU; ++i) a = fmaxf(a, top[slot * WU + i]);
+      __syncthreads();
+    } else {
+      a = __uint_as_float(bits);
+    }
+    if (!on) continue;  // (whole units)
+    const float need = least_scale(a);
+    const bool had = old > 0.f && old < INFINITY && !(mask & 1u);
+    const bool grown = had && need > old;
+    const float now = had && !grown ? old : need;
+    const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0;
+    const float inv = 1.f / now;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int j = r0 + RPP * i;
+      if (j >= rn) continue;
+      float c[8];
+#pragma unroll
+      for (int e8 = 0; e8 < 8; ++e8) c[e8] = pow2 ? x[i][e8] * inv : __fdiv_rn(x[i][e8], now);
+      const int off = slot_of[lead + 1 + j] & 15;
+      *reinterpret_cast<uint2 *>(codes + off * pool.tok) =
+          make_uint2(codes4(c[0], c[1], c[2], c[3]), codes4(c[4], c[5], c[6], c[7]));
+    }
+    if (grown) {
+      // the block's other codes, to the new scale
+      const float ratio = __fdiv_rn(old, now);
+#pragma unroll 1
+      for (int i = 0; i < NP; ++i) {
+        const int off = r0 + RPP * i;
+        if (mask >> off & 1u) continue;
+        uint2 *at = reinterpret_cast<uint2 *>(codes + off * pool.tok);
+        const uint2 w = *at;
+        float y[4], z[4];
+        floats4(w.x, y);
+        floats4(w.y, z);
+        *at = make_uint2(codes4(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio),
+                         codes4(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio));
+      }
+    }
+    __syncwarp();  // (every lane has the old scale)
+    if (ut == 0 && now != old) *scale_at = now;
+  }
+}
+
+template <int D, bool BF16, bool NEOX, bool FEW>
+__global__ void __launch_bounds__(kThreads) pd_quant_write(const __grid_constant__ QuantWriteParams p) {
+  extern __shared__ __align__(16) float smem_f[];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int b = blockIdx.x;
+  if (b < p.kv_ctas)
+    kv_runs<D, BF16, NEOX>(p, b, smem_f);
+  else if (FEW)
+    q_tokens<D, BF16, NEOX, kThreads, 4>(p, b - p.kv_ctas, smem_f);
+  else
+    q_tokens<D, BF16, NEOX, kThreads / 2, 1>(p, 2 * (b - p.kv_ctas), smem_f);
+}
+
+template <int D>
+cudaError_t launch_write(const QuantWriteParams &p, bool bf16, bool neox, bool few, int ctas, int smem,
+                         cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  auto go = [&](auto kern, SmemLimit &limit) {
+    const cudaError_t e = allow_smem(limit, kern, smem);
+    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, p) : e;
+  };
+  static SmemLimit limits[8];
+  const int which = (bf16 ? 4 : 0) + (neox ? 2 : 0) + (few ? 1 : 0);
+  switch (which) {
+    case 0: return go(pd_quant_write<D, false, false, false>, limits[0]);
+    case 1: return go(pd_quant_write<D, false, false, true>, limits[1]);
+    case 2: return go(pd_quant_write<D, false, true, false>, limits[2]);
+    case 3: return go(pd_quant_write<D, false, true, true>, limits[3]);
+    case 4: return go(pd_quant_write<D, true, false, false>, limits[4]);
+    case 5: return go(pd_quant_write<D, true, false, true>, limits[5]);
+    case 6: return go(pd_quant_write<D, true, true, false>, limits[6]);
+    default: return go(pd_quant_write<D, true, true, true>, limits[7]);
+  }
+}
+
+}  // namespace
+}  // namespace pd
+
+using namespace pd;
+
+extern "C" PD_API int paged_rope_quant_cache_write(
+    const pd_tensor *q, const pd_tensor *k, const pd_tensor *v, const pd_tensor *positions,
+    const pd_tensor *slot_mapping, const pd_tensor *cos_sin_cache, const uint8_t *pair_axis,
+    pd_tensor *q_out, pd_tensor *k_cache, pd_tensor *v_cache, pd_tensor *k_scale, pd_tensor *v_scale,
+    int num_q_heads, int num_kv_heads, int head_size, int rot_dim, int page_size, int layout,
+    int is_neox, void *stream) {
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache || !k_scale || !v_scale || !q != !q_out)
+    return PD_EINVAL;
+  if (num_kv_heads <= 0 || (q && num_q_heads <= 0)) return PD_EINVAL;
+  if (head_size != 64 && head_size != 128 && head_size != 256 && head_size != 512) return PD_EHEAD;
+  if (page_size <= 0 || page_size % PD_SCALE_TOKENS != 0 || (layout != PD_NHD && layout != PD_HND))
+    return PD_EINVAL;
+  if (rot_dim < 0 || rot_dim > head_size || rot_dim % (is_neox ? 16 : 8) != 0) return PD_EINVAL;
+  if ((rot_dim > 0) != (positions != nullptr) || (rot_dim > 0) != (cos_sin_cache != nullptr))
+    return PD_EINVAL;
+  if (k->ndim != 3 || k->shape[0] < 0 || k->shape[0] > INT32_MAX / 2) return PD_EINVAL;
+  const int64_t T = k->shape[0];
+  int rc;
+  if ((rc = check_token_rows(k, T, num_kv_heads, head_size)) != PD_OK) return rc;
+  if ((rc = check_token_rows(v, T, num_kv_heads, head_size)) != PD_OK) return rc;
+  if (k->dtype != v->dtype) return PD_EDTYPE;
+  QuantWriteParams p{};
+  if (q) {
+    if ((rc = check_token_rows(q, T, num_q_heads, head_size)) != PD_OK) return rc;
+    if ((rc = check_token_rows(q_out, T, num_q_heads, head_size)) != PD_OK) return rc;
+    if (q->dtype != k->dtype || q_out->dtype != k->dtype) return PD_EDTYPE;
+    p.q = q->data;
+    p.q_s0 = q->stride[0];
+    p.q_s1 = q->stride[1];
+    p.q_out = q_out->data;
+    p.qo_s0 = q_out->stride[0];
+    p.qo_s1 = q_out->stride[1];
+    p.Hq = num_q_heads;
+  }
+  if ((rc = check_i32_vector(slot_mapping, T)) != PD_OK) return rc;
+  if (rot_dim > 0) {
+    const pd_tensor *ps = positions, *cs = cos_sin_cache;
+    if (ps->ndim != 1 && ps->ndim != 2) return PD_EINVAL;
+    const int at = ps->ndim - 1;
+    const int64_t axes = at ? ps->shape[0] : 1;
+    if (axes < 1 || axes > PD_MAX_AXES || ps->shape[at] != T || (!ps->data && T != 0)) return PD_EINVAL;
+    if (ps->dtype != PD_I32) return PD_EDTYPE;
+    if (T > 1 && ps->stride[at] != 1) return PD_EALIGN;
+    if (at && ps->stride[0] < 0) return PD_EINVAL;
+    if (!cs->data || cs->ndim != 2 || cs->shape[0] < 1 || cs->shape[0] > INT32_MAX ||
+        cs->shape[1] < rot_dim || cs->stride[1] != 1 || cs->stride[0] < rot_dim)
+      return PD_EINVAL;
+    if (cs->dtype != PD_F32) return PD_EDTYPE;
+    if (cs->stride[0] % 4 != 0 || !aligned16(cs->data)) return PD_EALIGN;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+      if (pair_axis && pair_axis[i] >= axes) return PD_EINVAL;
+      p.axis[i] = pair_axis ? pair_axis[i] : 0;
+    }
+    p.positions = static_cast<const int32_t *>(ps->data);
+    p.pos_stride = at ? ps->stride[0] : 0;
+    p.axes = (int)axes;
+    p.cos_sin = static_cast<const float *>(cs->data);
+    p.cs_s0 = cs->stride[0];
+    p.max_pos = (int)cs->shape[0];
+  }
+  if ((rc = quant_pool(k_cache, k_scale, layout, num_kv_heads, page_size, head_size, &p.kc)) != PD_OK)
+    return rc;
+  if ((rc = quant_pool(v_cache, v_scale, layout, num_kv_heads, page_size, head_size, &p.vc)) != PD_OK)
+    return rc;
+  if (k_cache->shape[0] != v_cache->shape[0]) return PD_EINVAL;
+  if (T == 0) return PD_OK;
+  int num_sms = 0;
+  if ((rc = device_check(&num_sms, &p.status)) != PD_OK) return rc;
+  p.k = k->data;
+  p.k_s0 = k->stride[0];
+  p.k_s1 = k->stride[1];
+  p.v = v->data;
+  p.v_s0 = v->stride[0];
+  p.v_s1 = v->stride[1];
+  p.slots = static_cast<const int32_t *>(slot_mapping->data);
+  p.T = (int)T;
+  p.Hkv = num_kv_heads;
+  p.rot = rot_dim;
+  p.P = page_size;
+  p.num_slots = k_cache->shape[0] * (int64_t)page_size;
+  // Tokens of a k/v CTA: 16 of a prompt (a block or two), fewer while that leaves
+  // SMs without one; the angles of its tokens and 15 more lie in shared memory.
+  const int most = head_size == 512 ? 4 : head_size == 256 ? 8 : 16;
+  p.window = 1;
+  while (p.window < most && T >= 4LL * num_sms * p.window) p.window *= 2;
+  const int slots = head_size > 256 ? 1 : head_size > 128 ? 2 : 4;  // units of a CTA at a time
+  p.units = p.window > 4 ? 2 * slots : slots;
+  p.slices = (2 * num_kv_heads + p.units - 1) / p.units;
+  const int64_t windows = (T + p.window - 1) / p.window;
+  const bool few = T * 4 < (int64_t)num_sms * 32;
+  const int64_t q_ctas = q ? (few ? T : (T + 1) / 2) : 0;
+  if (windows * p.slices + q_ctas > INT32_MAX) return PD_EINVAL;
+  p.kv_ctas = (int)(windows * p.slices);
+  const int ctas = p.kv_ctas + (int)q_ctas;
+  const int smem = (p.window + PD_SCALE_TOKENS - 1) * rot_dim * 4;
+  const bool bf16 = k->dtype == PD_BF16;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (head_size) {
+    case 64: e = launch_write<64>(p, bf16, is_neox, few, ctas, smem, st); break;
+    case 128: e = launch_write<128>(p, bf16, is_neox, few, ctas, smem, st); break;
+    case 256: e = launch_write<256>(p, bf16, is_neox, few, ctas, smem, st); break;
+    case 512: e = launch_write<512>(p, bf16, is_neox, few, ctas, smem, st); break;
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return PD_ECUDA;
+  }
+  return PD_OK;
+}
