@@ -9,7 +9,6 @@ namespace pd {
 namespace {
 
 constexpr int kSmemLimit = 232448;  // dynamic shared memory of a CTA at most
-constexpr int kUnitCost = 12;       // kQuantUnitCost of pd_quant_attn.cuh
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -30,21 +29,19 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   while (8 * NT < rows) NT *= 2;
   const int NR = 8 * NT;
   const int64_t HR = Hkv * rg;
-  if (HR > INT32_MAX / kQuantSeqs) return PD_EINVAL;
+  if (HR > 65535) return PD_EINVAL;  // (units of a sequence)
   int64_t nb_max = cdiv((int64_t)bt_width * P, kBlockKeys);
   if (window > 0)
     nb_max = std::min<int64_t>(nb_max, cdiv((int64_t)window + M - 1, kBlockKeys) + 1 +
                                            cdiv(sinks, kBlockKeys));
   // runs of sequences whose line's places fit an int
-  const int64_t per_seq = (nb_max + kUnitCost) * HR;
-  const int64_t fit = (int64_t)INT32_MAX / per_seq;
+  const int64_t per_seq = (nb_max + kQuantUnitCost) * HR;
+  const int64_t fit = ((int64_t)INT32_MAX - (1 << 20)) / per_seq;
   const int seqs = (int)std::min<int64_t>({(int64_t)S, (int64_t)kQuantSeqs, std::max<int64_t>(fit, 1)});
   const int gy = (int)cdiv(S, seqs);
   if (gy > 65535) return PD_EINVAL;
   const int64_t units = S * HR, units_y = seqs * HR;
-  int NW = quant_max_warps(D, NT);
-  const int NS = quant_stages(D, NT);
-  while (NW > 4 && smem_bytes_quant(D, NT, NW, NS, seqs) > kSmemLimit) --NW;
+  if (smem_bytes_quant(D, NT, seqs) > kSmemLimit) return PD_EINVAL;
   // two parts of (acc, m, l) per CTA, behind the counters
   const int64_t per_cta = 2LL * NR * (D + 2) * 4;
   int64_t G = 0;
@@ -66,15 +63,15 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   p.row_groups = (int)rg;
   p.rows_per_cta = rows;
   p.n_tiles = NT;
-  p.key_groups = NW;
-  p.stages = NS;
+  p.key_groups = kQuantWarps;
+  p.stages = quant_slots(D, NT);
   p.seg_blocks = (int)std::min<int64_t>(nb_max, INT32_MAX);
   p.max_segments = p.max_parts = whole ? 0 : (int)G;
   p.cluster = 1;
   p.grid_x = (int)G;
   p.grid_y = gy;
-  p.block_threads = 32 * NW;
-  p.smem_bytes = smem_bytes_quant(D, NT, NW, NS, seqs);
+  p.block_threads = 32 * kQuantWarps;
+  p.smem_bytes = smem_bytes_quant(D, NT, seqs);
   p.scratch_needed = whole ? 0 : G * gy * per_cta + 256;
   return PD_OK;
 }
@@ -219,6 +216,12 @@ PD_API int paged_decode_attn_quant(const pd_tensor *q, const pd_tensor *k_cache,
   p.seqs_y = plan.seqs_y;
   p.whole = plan.whole;
   p.min_share = 8;
+  p.bpp = page_size / kBlockKeys;
+  p.by_units = FastDiv(num_kv_heads * p.rg);
+  p.by_groups = FastDiv(p.rg);
+  p.by_heads = FastDiv(p.G);
+  p.by_page = FastDiv(p.bpp);
+  p.by_ctas = FastDiv(plan.pub.grid_x);
   const int NR = 8 * plan.pub.n_tiles;
   if (!plan.whole) {
     char *base = static_cast<char *>(scratch->data);

@@ -16,6 +16,24 @@ struct QuantPool {
   int64_t s_page, s_blk, s_head;
 };
 
+// Division of whole numbers from 0 to 2^31 - 1 by a number that the host knows.
+struct FastDiv {
+  uint32_t mul = 1u << 31;
+  int shift = 31;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    int l = 0;
+    while ((1ull << l) < d) ++l;
+    // ceil(2^(31 + l) / d), at most d - 1 < 2^l over: n times that stays below 2^(31 + l)
+    shift = 31 + l;
+    mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__
+#endif
+  uint32_t div(int n) const { return (uint32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+
 // Attention over an 8-bit cache (pd_quant_attn.cuh).
 struct QuantAttnParams {
   const void *q;
@@ -28,34 +46,45 @@ struct QuantAttnParams {
   int bt_width;
   const int32_t *seq_lens, *query_start;
   int num_seqs, num_tokens, num_pages;
-  int Hq, Hkv, G, M, P, window, sinks;
+  int Hq, Hkv, G, M, P, bpp, window, sinks;  // bpp: 16-key blocks of a page
   float scale_log2;  // scale x log2(e): the softmax runs on exp2
   int rg, rows_grp;  // row groups of a kv head's packed rows, rows of one
   int seqs_y;        // sequences of one blockIdx.y
   int whole;         // 1: no unit is cut
   int min_share;     // the least share of a CTA
+  FastDiv by_units, by_groups, by_heads, by_page, by_ctas;  // Hkv rg, rg, G, bpp, gridDim.x
   float *part_acc, *part_ml;  // [2 x CTAs][8 NT][D], [..][8 NT][2]
   int *counters;              // parts published of each unit
   unsigned int *status;
 };
 
+// What a unit counts in the line of blocks beside its blocks (its Q, its end).
+constexpr int kQuantUnitCost = 12;
 // Sequences of one line at most (their lengths and places lie in shared memory).
 constexpr int kQuantSeqs = 1024;
-// 16-key blocks of a warp's step, its steps in flight and the warps of a CTA;
+constexpr int kQuantWarps = 8;
+#ifndef QTB
+#define QTB (D == 64 ? (NT <= 2 ? 4 : 2) : D == 128 ? 2 : 1)
+#define QNS (D == 512 ? 3 : 6)
+#endif
+// 16-key blocks of a warp's step; slots of its ring, each K or V of a step;
 // n-tiles of 8 packed rows with their sums in registers.
-constexpr int quant_step_blocks(int D, int NT) { return D == 64 && NT <= 2 ? 2 : 1; }
-constexpr int quant_stages(int D, int NT) { return D == 512 ? 2 : 3; }
+constexpr int quant_step_blocks(int D, int NT) { return QTB; }
+constexpr int quant_slots(int D, int NT) { return QNS; }
 constexpr int quant_max_tiles(int D) { return D == 64 ? 4 : 512 / D; }
-constexpr int quant_max_warps(int D, int NT) { return NT * D >= 512 ? 8 : 12; }
-// passes over the columns when a CTA's warps add their sums
-constexpr int quant_passes(int D, int NT) { return NT * D > 128 ? NT * D / 128 : 1; }
-constexpr int quant_stage_bytes(int D, int NT) { return quant_step_blocks(D, NT) * (32 * D + 16); }
-// Dynamic shared memory: the warps' rings, the sums of one pass, (m, l) of every
-// warp's rows, two sets of Q fragments, row scales and row ends, lengths, first
-// rows and places.
-constexpr int smem_bytes_quant(int D, int NT, int NW, int NS, int seqs) {
-  return 128 + NW * NS * quant_stage_bytes(D, NT) + NW * 8 * NT * (D / quant_passes(D, NT)) * 4 +
-         NW * 8 * NT * 8 + 2 * (NT * 16 * D + 8 * NT * 8) + 4 * (3 * seqs + 2) + 64 * 4;
+constexpr int quant_slot_bytes(int D, int NT) { return quant_step_blocks(D, NT) * 16 * D + 32; }
+// passes over the columns when a CTA's warps add their sums, each in one slot
+constexpr int quant_passes(int D, int NT) {
+  return 2 * NT > quant_step_blocks(D, NT) ? 2 * NT / quant_step_blocks(D, NT) : 1;
+}
+constexpr int kQuantRunBytes = 40, kQuantPieceBytes = 80;
+// Dynamic shared memory: the warps' rings, two sets of Q fragments, row scales and
+// row ends, the warps' (m, l) and weights of the rows and their totals, four
+// pieces, two runs of each warp, sums and flags, lengths, first rows and places.
+constexpr int smem_bytes_quant(int D, int NT, int seqs) {
+  return 128 + kQuantWarps * quant_slots(D, NT) * quant_slot_bytes(D, NT) + 2 * (NT * 16 * D + 8 * NT * 8) +
+         8 * NT * (kQuantWarps * 12 + 8) + 4 * kQuantPieceBytes + kQuantWarps * 2 * kQuantRunBytes +
+         4 * (2 * kQuantWarps + 8) + 4 * (3 * seqs + 1);
 }
 
 cudaError_t launch_quant_d64(bool bf16, int nt, const QuantAttnParams &p, const Launch &l, cudaStream_t stream);

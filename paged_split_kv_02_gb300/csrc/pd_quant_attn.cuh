@@ -16,25 +16,29 @@
 // and O^T += V^T P^T.  The order of the summed dims is free, so that one
 // register of a K row (four codes side by side) gives both halves of an A fragment's
 // row, and the transposed load of two codes a lane gives the even and the odd
-// dims of a V fragment.  bf16 queries are scaled by a power of two per row
+// dims of a V fragment.  (The legacy MMAs of 8-bit floats are no faster: a 16 x 8 x
+// 32 one takes 18.5 clocks of a sub-partition with its operands' conversions
+// inside, two 16 x 8 x 16 of halves 16.2.)  bf16 queries are scaled by a power of two per row
 // into the halves' range, which loses nothing above 2^-31 of the row's largest.
 //
 // The scales stay out of the products: S is scaled by its block's key scale in
 // fp32; V's goes into the weights, a = s + log2(v_scale), p = 2^(a - max a), and
 // out again in the sum l += p / v_scale, so P lies in [0, 2^15] whatever the scales
-// are, and is rounded once, to 11 bits.
+// are.
 #pragma once
 
 #include <cuda_fp16.h>
 
+#include "pd_e4m3.cuh"
 #include "pd_kernel.cuh"
 #include "pd_quant.h"
 
 namespace pd {
 
-// What a unit counts in the line beside its blocks.
-constexpr int kQuantUnitCost = 12;
-constexpr float kQuantTop = 15.f;  // log2 of the largest P
+// P = 2^(a - m), m a reference that follows the largest a: raised where a row's a
+// would pass 2^15 (a half's largest is 2^16), to where the largest is 2^7, so it
+// moves rarely and P loses bits of its 11 below 2^-21 of the largest alone.
+constexpr float kQuantTop = 7.f, kQuantMost = 15.f;
 
 // 4- and 16-byte copies global -> shared by address, and this thread's groups.
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void *src) {
@@ -49,12 +53,13 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Four e4m3 codes as halves: bytes 0, 1 and bytes 2, 3.
-__device__ __forceinline__ void halves_of(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
+// D(16x8, f32) = A(16x16) * B(16x8) of halves.
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // 4 values rounded to 16 bits
@@ -65,12 +70,20 @@ __device__ __forceinline__ void store_four(void *dst, const float4 &v, float inv
       make_uint2(pack2(v.x * inv, v.y * inv, tag{}), pack2(v.z * inv, v.w * inv, tag{}));
 }
 
+__device__ __forceinline__ void add_scaled(float4 &o, float f, const float4 &a) {
+  o.x = fmaf(f, a.x, o.x);
+  o.y = fmaf(f, a.y, o.y);
+  o.z = fmaf(f, a.z, o.z);
+  o.w = fmaf(f, a.w, o.w);
+}
+
 // The keys of a sequence that its rows see, in 16-key blocks.
 struct QuantSeq {
   int L, q0, ml;               // keys, first q / out row, query tokens
-  int u_lo, u_hi, v_lo, v_hi;  // union / intersection of its rows' windows
+  int u_lo, u_hi;              // union of its rows' windows
   int sk_nb, sk_gap;           // blocks of the sinks, blocks left out after them
   int nb;                      // blocks with visible keys
+  int all_lo, all_hi, all_sk;  // of those, [all_lo, all_hi) and [0, all_sk) are seen whole by every row
 };
 
 __device__ __forceinline__ QuantSeq quant_seq(int L, int q0, int ml, int window, int sinks) {
@@ -78,71 +91,125 @@ __device__ __forceinline__ QuantSeq quant_seq(int L, int q0, int ml, int window,
   r.L = L;
   r.q0 = q0;
   r.ml = ml;
-  const int n0 = ml > 0 ? max(L - ml + 1, 0) : 0, n1 = ml > 0 ? L : 0;
+  const int n0 = ml > 0 ? max(L - ml + 1, 0) : 0, n1 = ml > 0 ? L : 0;  // keys of the first, the last row
   r.u_hi = n1;
-  r.v_hi = n0;
   r.u_lo = window > 0 ? max(0, n0 - window) : 0;
-  r.v_lo = window > 0 ? max(0, n1 - window) : 0;
   const int first = r.u_lo / kBlockKeys, last = (n1 + kBlockKeys - 1) / kBlockKeys;
   r.sk_nb = window > 0 ? (min(sinks, n1) + kBlockKeys - 1) / kBlockKeys : 0;
   r.sk_gap = max(0, first - r.sk_nb);
   r.nb = n1 > r.u_lo ? last - r.sk_gap : 0;
+  const int v_lo = window > 0 ? max(0, n1 - window) : 0;
+  const int whole = (v_lo + kBlockKeys - 1) / kBlockKeys - r.sk_gap;
+  r.all_lo = r.sk_gap > 0 ? max(r.sk_nb, whole) : whole;
+  r.all_hi = n0 / kBlockKeys - r.sk_gap;
+  r.all_sk = window > 0 ? min(sinks, n0) / kBlockKeys : 0;
   return r;
 }
 
+// n / d for n >= 0 below 2^31 and a quotient below 2^16 (the approximate one is at
+// most one off).
+__device__ __forceinline__ int div_near(int n, int d) {
+  int q = __float2int_rz(__fdividef((float)n, (float)d));
+  const int r = n - q * d;
+  if (r < 0) --q;
+  if (r >= d) ++q;
+  return q;
+}
+
+// A run of steps of a warp within a piece: its copies' cursor.
+struct QuantRun {
+  int k;                // piece
+  int first, mine;      // the warp's first step of it, and its number of them
+  int base;             // the run's first of those
+  int b0, b1, sk_nb, sk_gap;
+  int s, h;
+};
+
+// A piece of a CTA's share: some or all blocks of one unit.
+struct QuantPiece {
+  QuantSeq r;
+  int i, h, g;          // sequence (of this line), kv head, row group
+  int b0, b1;           // its blocks of the unit
+  int part, parts, first_cta;
+};
+
+static_assert(sizeof(QuantRun) == kQuantRunBytes && sizeof(QuantPiece) <= kQuantPieceBytes, "their shared memory");
+
 template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
-    pd_quant_decode(const __grid_constant__ QuantAttnParams p) {
-  constexpr int TB = quant_step_blocks(D, NT), NS = quant_stages(D, NT);
+__global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __grid_constant__ QuantAttnParams p) {
+  constexpr int NW = kQuantWarps;
+  constexpr int TB = quant_step_blocks(D, NT), NS = quant_slots(D, NT);
   constexpr int BLOCK = 16 * D;               // bytes of K (or V) of a block
-  constexpr int STAGE = quant_stage_bytes(D, NT);  // TB x (K, V, scales)
+  constexpr int SLOT = quant_slot_bytes(D, NT);  // TB blocks of K, and their scales, or of V
   constexpr int CPR = D / 16;                 // 16-byte chunks of a row
   constexpr int RPI = 32 / CPR;               // rows that 32 lanes copy at once (D = 512: 1)
   constexpr int COPIES = D / 32;              // copies of a lane for K (or V) of a block
   constexpr int NR = 8 * NT;                  // rows of the CTA, padded
   constexpr int PASSES = quant_passes(D, NT), DC = D / PASSES, CPP = CPR / PASSES;
+  constexpr int SWIZZLE = DC >= 32 ? 24 : DC - 8;  // of the columns of the warps' sums
   constexpr int SPC = 32 / TB;                // steps whose page ids a warp holds
+  constexpr int NTHR = 32 * NW;
+  constexpr int kPieces = 4;                  // pieces whose place is known at a time
 
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nthr = blockDim.x, NW = nthr >> 5;
-  unsigned char *ring = smem + warp * (NS * STAGE);
-  float *cp = reinterpret_cast<float *>(smem + NW * NS * STAGE);  // [NW][NR][DC] (swizzled)
-  float2 *ml_of = reinterpret_cast<float2 *>(cp + NW * NR * DC);  // [NW][NR] (m, l)
-  uint2 *qfrag = reinterpret_cast<uint2 *>(ml_of + NW * NR);      // [2][CPR][NT][32]
-  float *rowsc = reinterpret_cast<float *>(qfrag + 2 * CPR * NT * 32);  // [2][NR]
-  int *rowhi = reinterpret_cast<int *>(rowsc + 2 * NR);                 // [2][NR]
-  int *sums = rowhi + 2 * NR;                                           // [32]
-  volatile int *flag = sums + 32;                                       // [32]
-  int *lens = sums + 64;                                                // [seqs]
-  int *starts = lens + p.seqs_y;                                        // [seqs + 1]
-  int *place = starts + p.seqs_y + 1;                                   // [seqs + 1]
+  unsigned char *ring = smem + warp * (NS * SLOT);
+  uint2 *qfrag = reinterpret_cast<uint2 *>(smem + NW * NS * SLOT);         // [2][CPR][NT][32]
+  float *rowsc = reinterpret_cast<float *>(qfrag + 2 * CPR * NT * 32);     // [2][NR]
+  int *rowhi = reinterpret_cast<int *>(rowsc + 2 * NR);                    // [2][NR]
+  float2 *ml_of = reinterpret_cast<float2 *>(rowhi + 2 * NR);              // [NR][NW] (m, l) of the warps
+  float *weight = reinterpret_cast<float *>(ml_of + NR * NW);              // [NR][NW]
+  float2 *total = reinterpret_cast<float2 *>(weight + NR * NW);            // [NR] (m, l) of the piece
+  QuantPiece *pieces = reinterpret_cast<QuantPiece *>(total + NR);         // [kPieces]
+  QuantRun *runs = reinterpret_cast<QuantRun *>(reinterpret_cast<unsigned char *>(pieces) +
+                                                kPieces * kQuantPieceBytes) + 2 * warp;  // [NW][2]
+  int *sums = reinterpret_cast<int *>(runs - 2 * warp + 2 * NW);           // [NW]
+  int *free_slot = sums + NW;                                              // [NW]
+  volatile int *flag = free_slot + NW;                                     // [8]: first unit, last unit, merges
+  int *lens = free_slot + NW + 8;                                          // [seqs]
+  int *starts = lens + p.seqs_y;                                           // [seqs + 1]
+  int *place = starts + p.seqs_y + 1;                                      // [seqs]
 
   const int s_first = blockIdx.y * p.seqs_y, S = min(p.seqs_y, p.num_seqs - s_first);
   const int HR = p.Hkv * p.rg;  // units of a sequence
 
   grid_dependency_wait();
 
-  // ---- the lengths, clamped and reported ------------------------------------
+  // ---- the lengths, clamped and reported; their places on the line -----------
+  // (a thread has a run of sequences)
+  const int per = (S + NTHR - 1) / NTHR, i0 = min(tid * per, S), i1 = min(i0 + per, S);
+  int sum = 0;
   {
     const int cap = p.bt_width * p.P;
     unsigned int bad = 0;
-    for (int i = tid; i < S; i += nthr) {
+    for (int i = i0; i < i1; ++i) {
       const int L = __ldg(p.seq_lens + s_first + i);
+      int q0 = (s_first + i) * p.M, ml = p.M;
+      if (p.query_start) {
+        const int a = __ldg(p.query_start + s_first + i), b = __ldg(p.query_start + s_first + i + 1);
+        q0 = min(max(a, 0), p.num_tokens);
+        ml = min(max(min(max(b, 0), p.num_tokens) - q0, 0), p.M);
+        starts[i] = q0;
+        if (i == S - 1) starts[S] = min(max(b, 0), p.num_tokens);
+        if (a < 0 || b > p.num_tokens || b < a || b - a > p.M) bad |= PD_DEV_BAD_QSTART;
+      }
       if (L > cap) bad |= PD_DEV_BAD_SEQLEN;
       lens[i] = min(max(L, 0), cap);
-    }
-    if (p.query_start) {
-      for (int i = tid; i <= S; i += nthr) {
-        const int s = s_first + i;
-        const int a = __ldg(p.query_start + s);
-        const int b = s < p.num_seqs ? __ldg(p.query_start + s + 1) : a;
-        starts[i] = min(max(a, 0), p.num_tokens);
-        if (a < 0 || a > p.num_tokens || b < a || (s < p.num_seqs && b - a > p.M)) bad |= PD_DEV_BAD_QSTART;
-      }
+      sum += (quant_seq(lens[i], q0, ml, p.window, p.sinks).nb + kQuantUnitCost) * HR;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sums[warp] = inc;
+  if (tid == 0) {
+    flag[0] = 1;
+    flag[1] = 0;
   }
   __syncthreads();
   auto seq_of = [&](int i) -> QuantSeq {
@@ -154,76 +221,51 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
     return quant_seq(lens[i], q0, ml, p.window, p.sinks);
   };
 
-  // ---- this CTA's share: units [unit0, unit0 + n_pieces) of the line --------
-  int unit0 = 0, n_pieces = 0;
-  uint32_t x0 = 0, x1 = 0, share = 1;
+  // ---- this CTA's share: units [unit0, unit0 + n_pieces) of the line ---------
+  int unit0, n_pieces;
+  int x0 = 0, x1 = 0, share = 1;
   if (p.whole) {
     const int64_t U = (int64_t)S * HR;
     unit0 = (int)(U * blockIdx.x / gridDim.x);
     n_pieces = (int)(U * (blockIdx.x + 1) / gridDim.x) - unit0;
   } else {
-    // places of the sequences: an exclusive sum over threads of runs of them
-    const int per = (S + nthr - 1) / nthr, i0 = min(tid * per, S), i1 = min(i0 + per, S);
-    int sum = 0;
-    for (int i = i0; i < i1; ++i) sum += (seq_of(i).nb + kQuantUnitCost) * HR;
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
     int base = 0, W = 0;
+#pragma unroll
     for (int i = 0; i < NW; ++i) {
       const int v = sums[i];
       if (i < warp) base += v;
       W += v;
     }
+    share = max(p.min_share, (int)p.by_ctas.div(W + (int)gridDim.x - 1));
+    x0 = (int)min((int64_t)blockIdx.x * share, (int64_t)W);
+    x1 = (int)min((int64_t)x0 + share, (int64_t)W);
+    // the units that its first and its last place are in
     int at = base + inc - sum;
     for (int i = i0; i < i1; ++i) {
       place[i] = at;
-      at += (seq_of(i).nb + kQuantUnitCost) * HR;
-    }
-    if (tid == 0) place[S] = W;
-    __syncthreads();
-    share = max((uint32_t)p.min_share, ((uint32_t)W + gridDim.x - 1) / gridDim.x);
-    x0 = min((uint64_t)blockIdx.x * share, (uint64_t)W);
-    x1 = min((uint64_t)x0 + share, (uint64_t)W);
-    // the unit that a place of the line is in
-    auto unit_at = [&](uint32_t x, bool first) -> int {
-      int lo = 0, hi = S - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((uint32_t)place[mid] <= x) lo = mid; else hi = mid - 1;
+      const int nb = seq_of(i).nb, cost = nb + kQuantUnitCost, next = at + cost * HR;
+      if (x0 < x1 && x0 >= at && x0 < next) {
+        const int k = div_near(x0 - at, cost), in = x0 - at - k * cost;
+        // (a first unit whose blocks, or whose place if it has none, lie before the share)
+        flag[0] = i * HR + k + (in > 0 && in >= nb ? 1 : 0);
       }
-      const uint32_t off = x - (uint32_t)place[lo];
-      const int nb = seq_of(lo).nb, cost = nb + kQuantUnitCost;
-      const int k = (int)(off / (uint32_t)cost), in = (int)(off - (uint32_t)k * cost);
-      // (a first unit whose blocks, or whose place if it has none, lie before the share)
-      return lo * HR + k + (first && in > 0 && in >= nb ? 1 : 0);
-    };
-    if (x1 > x0) {
-      unit0 = unit_at(x0, true);
-      n_pieces = unit_at(x1 - 1, false) - unit0 + 1;
+      if (x0 < x1 && x1 - 1 >= at && x1 - 1 < next) flag[1] = i * HR + div_near(x1 - 1 - at, cost);
+      at = next;
     }
+    __syncthreads();
+    unit0 = flag[0];
+    n_pieces = flag[1] - unit0 + 1;
   }
 
-  // A piece of the share: some or all blocks of one unit.
-  struct Piece {
-    QuantSeq r;
-    int i, h, g;          // sequence (of this line), kv head, row group
-    int b0, b1;           // its blocks of the unit
-    int part, parts, first_cta;
-  };
+  using Piece = QuantPiece;
   // A unit that goes on behind the share comes first, so that its part is out early.
   bool tail = false;
   auto piece_at = [&](int k) -> Piece {
     const int u = unit0 + (tail ? (k == 0 ? n_pieces - 1 : k - 1) : k);
     Piece q;
-    q.i = u / HR;
+    q.i = p.by_units.div(u);
     const int hr = u - q.i * HR;
-    q.h = hr / p.rg;
+    q.h = p.rg == 1 ? hr : (int)p.by_groups.div(hr);
     q.g = hr - q.h * p.rg;
     q.r = seq_of(q.i);
     q.b0 = 0;
@@ -232,13 +274,13 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
     q.parts = 1;
     q.first_cta = blockIdx.x;
     if (!p.whole) {
-      const uint32_t a = (uint32_t)place[q.i] + (uint32_t)hr * (q.r.nb + kQuantUnitCost);
-      if (x0 > a) q.b0 = (int)(x0 - a);
-      if (x1 < a + q.r.nb) q.b1 = (int)(x1 - a);
+      const int a = place[q.i] + hr * (q.r.nb + kQuantUnitCost);
+      if (x0 > a) q.b0 = x0 - a;
+      if (x1 - a < q.r.nb) q.b1 = x1 - a;
       if (q.b1 - q.b0 < q.r.nb) {
-        q.first_cta = (int)(a / share);
+        q.first_cta = div_near(a, share);
         q.part = (int)blockIdx.x - q.first_cta;
-        q.parts = (int)((a + q.r.nb - 1) / share) - q.first_cta + 1;
+        q.parts = div_near(a + q.r.nb - 1, share) - q.first_cta + 1;
       }
     }
     return q;
@@ -251,22 +293,17 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
   // ---- the copies: a cursor over the steps of this warp ----------------------
   // Step st of a piece is blocks b0 + st TB ..; a warp takes steps first, first +
   // NW, .., the first one moving on with the pieces so that odd ones are spread.
-  struct Cursor {
-    int k;                // piece
-    int first, mine;      // of its steps
-    int at, base;         // next step of mine, the first whose page ids are held
-    int b0, b1, sk_nb, sk_gap;
-    int s, h;
-  };
-  auto enter = [&](Cursor &c, int k) {
+  // The page ids of a run of up to SPC steps are held, one block a lane; the run
+  // after it is looked up while this one is copied.  What a run does not change
+  // from step to step lies in shared memory: registers are for the products.
+  auto enter = [&](QuantRun &c, int k) {
     c.k = k;
-    c.at = c.base = 0;
-    c.mine = 0;
+    c.base = c.mine = 0;
     if (k >= n_pieces) return;
     const Piece q = piece_at(k);
     const int steps = (q.b1 - q.b0 + TB - 1) / TB;
     c.first = (warp + k) % NW;
-    c.mine = c.first < steps ? (steps - 1 - c.first) / NW + 1 : 0;
+    c.mine = (steps + NW - 1 - c.first) / NW;
     c.b0 = q.b0;
     c.b1 = q.b1;
     c.sk_nb = q.r.sk_nb;
@@ -274,149 +311,190 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
     c.s = s_first + q.i;
     c.h = q.h;
   };
-  const int bpp = p.P / kBlockKeys;  // blocks of a page
-  const int lg_bpp = (bpp & (bpp - 1)) == 0 ? __ffs(bpp) - 1 : -1;
-  // the page ids of the cursor's next SPC steps, one block a lane
-  auto fetch_ids = [&](const Cursor &c) -> int {
+  // (16-key blocks of a page)
+  auto fetch_ids = [&](const QuantRun &c) -> int {
     if (c.k >= n_pieces) return 0;
     const int b = c.b0 + (c.first + (c.base + lane / TB) * NW) * TB + lane % TB;
     if (c.base + lane / TB >= c.mine || b >= c.b1) return 0;
     const int sb = b >= c.sk_nb ? b + c.sk_gap : b;
-    return __ldg(p.block_table + (int64_t)c.s * p.bt_stride + (lg_bpp >= 0 ? sb >> lg_bpp : sb / bpp));
+    return __ldg(p.block_table + (int64_t)c.s * p.bt_stride + p.by_page.div(sb));
   };
-  // the next run of steps with page ids: of this piece, or of the next one
-  // that has a step for this warp
-  auto next_run = [&](Cursor &c) {
+  int which = 0;                      // the present run; the next one lies beside it
+  int at = 0, end = 0, next_blk = 0;  // steps of it, and the next one's first block
+  int ids = 0, ids_ahead = 0;
+  bool look = true;                   // the next run is still to be looked up
+  auto put = [&](int i, const QuantRun &c) {
+    __syncwarp();
+    if (lane == 0) runs[i] = c;
+    __syncwarp();
+  };
+  auto begin_run = [&](const QuantRun &c) {
+    at = 0;
+    end = c.k < n_pieces ? min(SPC, c.mine - c.base) : 0;
+    next_blk = c.b0 + (c.first + c.base * NW) * TB;
+  };
+  // the run after the present one: of its piece, or of the next one that has a step for this warp
+  auto look_ahead = [&]() {
+    QuantRun c = runs[which];
     c.base += SPC;
-    c.at = c.base;
     while (c.k < n_pieces && c.base >= c.mine) enter(c, c.k + 1);
+    ids_ahead = fetch_ids(c);
+    put(which ^ 1, c);
   };
-  Cursor cur, ahead;
-  enter(cur, 0);
-  while (cur.k < n_pieces && cur.mine == 0) enter(cur, cur.k + 1);
-  int ids = fetch_ids(cur);
-  ahead = cur;
-  next_run(ahead);
-  int ids_ahead = fetch_ids(ahead);
+  {
+    QuantRun c;
+    enter(c, 0);
+    while (c.k < n_pieces && c.mine == 0) enter(c, c.k + 1);
+    ids = fetch_ids(c);
+    put(0, c);
+    begin_run(c);
+  }
   const int c_row = lane / CPR, c_ch = lane % CPR;  // (D = 512: row 0, chunk = lane)
   const int64_t k_off = c_row * p.k.tok + c_ch * 16, v_off = c_row * p.v.tok + c_ch * 16;
   auto place_of = [&](int row, int ch) -> uint32_t {
     return D >= 128 ? row * D + ((ch ^ (row & 7)) << 4) : row * D + ((ch ^ ((row >> 1) & 3)) << 4);
   };
-  int in_slot = 0;  // the slot that the next step goes to
+  int in_slot = 0;  // the slot that the next copies go to
   const uint32_t ring_at = smem_u32(ring);
-  auto issue = [&]() {
-    if (cur.k < n_pieces) {
-      const int blk = cur.b0 + (cur.first + cur.at * NW) * TB;
+  // the next slot's copies: the present step's K and scales, or its V and on to the next step
+  auto issue = [&](bool is_v) {
+    if (at < end) {
+      const QuantRun &c = runs[which];
+      const QuantPool &t = is_v ? p.v : p.k;
+      const int b1 = c.b1, sk_nb = c.sk_nb, sk_gap = c.sk_gap, h = c.h;
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        int page = __shfl_sync(0xffffffffu, ids, (cur.at - cur.base) * TB + b);
-        if (blk + b < cur.b1) {
-          const int sb = blk + b >= cur.sk_nb ? blk + b + cur.sk_gap : blk + b;
-          const int sub = lg_bpp >= 0 ? sb & (bpp - 1) : sb % bpp;
+        int page = __shfl_sync(0xffffffffu, ids, at * TB + b);
+        const int i = next_blk + b;
+        if (i < b1) {
+          const int sb = i >= sk_nb ? i + sk_gap : i;
+          const int sub = sb - (int)p.by_page.div(sb) * p.bpp;
           if ((unsigned)page >= (unsigned)p.num_pages) {
             if (lane == 0) atomicOr(p.status, PD_DEV_BAD_PAGE);  // report, read page 0
             page = 0;
           }
-          const uint32_t dst = ring_at + in_slot * STAGE + b * (2 * BLOCK);
-          const unsigned char *ksrc = p.k.codes + page * p.k.page + (int64_t)(sub * kBlockKeys) * p.k.tok +
-                                      cur.h * p.k.head + k_off;
-          const unsigned char *vsrc = p.v.codes + page * p.v.page + (int64_t)(sub * kBlockKeys) * p.v.tok +
-                                      cur.h * p.v.head + v_off;
+          const uint32_t dst = ring_at + in_slot * SLOT + b * BLOCK;
+          const unsigned char *src = t.codes + page * t.page + (int64_t)(sub * kBlockKeys) * t.tok + h * t.head +
+                                     (is_v ? v_off : k_off);
+          if (t.tok == D) {
+            // (rows one after the other: offsets are constants)
 #pragma unroll
-          for (int i = 0; i < COPIES; ++i)
-            copy_async16(dst + place_of(c_row + i * RPI, c_ch), ksrc + (int64_t)(i * RPI) * p.k.tok);
+            for (int j = 0; j < COPIES; ++j) copy_async16(dst + place_of(c_row + j * RPI, c_ch), src + j * (RPI * D));
+          } else {
 #pragma unroll
-          for (int i = 0; i < COPIES; ++i)
-            copy_async16(dst + BLOCK + place_of(c_row + i * RPI, c_ch), vsrc + (int64_t)(i * RPI) * p.v.tok);
-          if (lane < 2) {
-            const QuantPool &t = lane ? p.v : p.k;
-            copy_async4(ring_at + in_slot * STAGE + TB * (2 * BLOCK) + b * 8 + lane * 4,
-                        t.scale + page * t.s_page + sub * t.s_blk + cur.h * t.s_head);
+            for (int j = 0; j < COPIES; ++j)
+              copy_async16(dst + place_of(c_row + j * RPI, c_ch), src + (int64_t)(j * RPI) * t.tok);
+          }
+          if (!is_v && lane < 2) {
+            const QuantPool &u = lane ? p.v : p.k;
+            copy_async4(ring_at + in_slot * SLOT + TB * BLOCK + b * 8 + lane * 4,
+                        u.scale + page * u.s_page + sub * u.s_blk + h * u.s_head);
           }
         }
       }
       if (++in_slot == NS) in_slot = 0;
-      if (++cur.at - cur.base == SPC || cur.at == cur.mine) {
-        cur = ahead;
-        ids = ids_ahead;
-        if (ahead.k < n_pieces) next_run(ahead);
-        ids_ahead = fetch_ids(ahead);
+      if (is_v) {
+        next_blk += NW * TB;
+        ++at;
+        if (look) {
+          look_ahead();
+          look = false;
+        }
+        if (at == end) {
+          which ^= 1;
+          ids = ids_ahead;
+          begin_run(runs[which]);
+          look = true;
+        }
       }
+    } else if (++in_slot == NS) {
+      in_slot = 0;
     }
     copy_commit();
   };
-#pragma unroll
-  for (int i = 0; i < NS - 1; ++i) issue();
 
   // ---- Q of a piece: halves in fragment order, row scales, row ends ----------
   using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
   const T *qbase = static_cast<const T *>(p.q);
   T *obase = static_cast<T *>(p.out);
   constexpr int QV = D >= 128 ? D / 128 : 1;
-  const int lg_g = (p.G & (p.G - 1)) == 0 ? __ffs(p.G) - 1 : -1;
-  auto token_of = [&](int r) { return lg_g >= 0 ? r >> lg_g : r / p.G; };  // packed row -> token
   auto row_live = [&](const Piece &q, int rr) {
     return rr < p.rows_grp && q.g * p.rows_grp + rr < q.r.ml * p.G;
   };
-  auto load_q = [&](const Piece &q, int buf) {
-    for (int rr = warp; rr < NR; rr += NW) {
+  uint2 qw[NT][QV];  // a warp's rows: warp, warp + NW, ..
+  static_assert(NW == 8, "a warp has NT rows of Q");
+  auto fetch_q = [&](const Piece &q) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int rr = warp + NW * n;
       const bool live = row_live(q, rr);
       const int pr = q.g * p.rows_grp + rr;
-      const int t = live ? token_of(pr) : 0, jq = live ? pr - t * p.G : 0;
+      const int t = live ? (int)p.by_heads.div(pr) : 0, jq = live ? pr - t * p.G : 0;
       const uint2 *src = reinterpret_cast<const uint2 *>(
           qbase + (int64_t)(q.r.q0 + t) * p.q_s0 + (int64_t)(q.h * p.G + jq) * p.q_s1);
-      uint2 w[QV];
 #pragma unroll
       for (int v = 0; v < QV; ++v)
-        w[v] = live && (D >= 128 || lane < D / 4) ? __ldg(src + v * 32 + lane) : make_uint2(0u, 0u);
+        qw[n][v] = live && (D >= 128 || lane < D / 4) ? __ldg(src + v * 32 + lane) : make_uint2(0u, 0u);
+    }
+  };
+  auto put_q = [&](const Piece &q, int buf) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int rr = warp + NW * n;
       float f = 1.f;
       if constexpr (BF16) {
         // the row's largest magnitude to [2^14, 2^15)
         uint32_t top = 0;
 #pragma unroll
         for (int v = 0; v < QV; ++v)
-          top = max(max(max(w[v].x & 0x7fffu, (w[v].x >> 16) & 0x7fffu),
-                        max(w[v].y & 0x7fffu, (w[v].y >> 16) & 0x7fffu)), top);
+          top = max(max(max(qw[n][v].x & 0x7fffu, (qw[n][v].x >> 16) & 0x7fffu),
+                        max(qw[n][v].y & 0x7fffu, (qw[n][v].y >> 16) & 0x7fffu)), top);
         top = __reduce_max_sync(0xffffffffu, top);
         // 2^(14 - e), e the exponent of the largest, within fp32's range
         const int e = min(max((int)(top >> 7) - 127, -100), 127);
         const float up = __int_as_float((14 - e + 127) << 23);
         f = __int_as_float((e - 14 + 127) << 23);
+        auto halves = [&](uint32_t b) -> uint32_t {
+          return pack2(__uint_as_float(b << 16) * up, __uint_as_float(b & 0xffff0000u) * up,
+                       std::integral_constant<bool, false>{});
+        };
 #pragma unroll
-        for (int v = 0; v < QV; ++v) {
-          auto half2_of = [&](uint32_t b) -> uint32_t {
-            const float lo = __uint_as_float(b << 16) * up, hi = __uint_as_float(b & 0xffff0000u) * up;
-            return pack2(lo, hi, std::integral_constant<bool, false>{});
-          };
-          w[v] = make_uint2(half2_of(w[v].x), half2_of(w[v].y));
-        }
+        for (int v = 0; v < QV; ++v) qw[n][v] = make_uint2(halves(qw[n][v].x), halves(qw[n][v].y));
       }
 #pragma unroll
       for (int v = 0; v < QV; ++v) {
         const int d4 = v * 32 + lane;  // dims 4 d4 ..
         if (D >= 128 || lane < D / 4)
-          qfrag[((buf * CPR + (d4 >> 2)) * NT + (rr >> 3)) * 32 + (rr & 7) * 4 + (d4 & 3)] = w[v];
+          qfrag[((buf * CPR + (d4 >> 2)) * NT + n) * 32 + warp * 4 + (d4 & 3)] = qw[n][v];
       }
       if (lane == 0) {
         rowsc[buf * NR + rr] = f * p.scale_log2;
-        rowhi[buf * NR + rr] = live ? max(q.r.L - q.r.ml + t + 1, 0) : 0;
+        rowhi[buf * NR + rr] =
+            row_live(q, rr) ? max(q.r.L - q.r.ml + (int)p.by_heads.div(q.g * p.rows_grp + rr) + 1, 0) : 0;
       }
     }
   };
+  if (n_pieces > 0) {
+    const Piece q = piece_at(0);
+    if (tid == 0) pieces[0] = q;
+    if (tid == 32 && n_pieces > 1) pieces[1] = piece_at(1);
+    fetch_q(q);
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i) issue(i & 1);
+    put_q(q, 0);
+  }
+  __syncthreads();
 
   const int g8 = lane >> 2, t4 = lane & 3;
   const int a_row = lane & 15, a_hi = lane >> 4;  // the rows and chunk of ldmatrix's addresses
   auto sees = [&](int key, int lo, int hi) { return key < hi && (key >= lo || key < p.sinks); };
-  int out_slot = 0;   // the slot of the next step to compute on
+  int out_slot = 0;   // the slot of the next step's K
   int n_cut = 0;      // cut units of this share whose part is out
-  int cut_k[2], cut_old[2];
-  cut_k[0] = cut_k[1] = 0;
-  cut_old[0] = cut_old[1] = 0;
+  int cut_k0 = 0, cut_k1 = 0, cut_old0 = 0, cut_old1 = 0;
 
   // the rows of a unit in q and out, and the scratch slot of a part of it
   auto out_row = [&](const Piece &q, int rr) -> T * {
-    const int pr = q.g * p.rows_grp + rr, t = token_of(pr), jq = pr - t * p.G;
+    const int pr = q.g * p.rows_grp + rr, t = p.by_heads.div(pr), jq = pr - t * p.G;
     return obase + (int64_t)(q.r.q0 + t) * p.o_s0 + (int64_t)(q.h * p.G + jq) * p.o_s1;
   };
   auto slot_of = [&](const Piece &q, int part) -> int64_t {
@@ -424,134 +502,170 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
     return part == 0 ? 2 * c + 1 : 2 * c;
   };
 
-  if (n_pieces > 0) load_q(piece_at(0), 0);
-  __syncthreads();
-
+#pragma unroll 1
   for (int k = 0; k < n_pieces; ++k) {
-    const Piece q = piece_at(k);
     const int buf = k & 1;
+    const Piece &q = pieces[k & (kPieces - 1)];
     const uint2 *qf = qfrag + buf * CPR * NT * 32 + lane;
-    const int steps = (q.b1 - q.b0 + TB - 1) / TB;
-    const int first = (warp + k) % NW;
-    const int mine = first < steps ? (steps - 1 - first) / NW + 1 : 0;
+    const int first = (warp + k) % NW, mine = ((q.b1 - q.b0 + TB - 1) / TB + NW - 1 - first) / NW;
     float acc[CPR][NT][4];
 #pragma unroll
     for (int c = 0; c < CPR; ++c)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[c][n][0] = acc[c][n][1] = acc[c][n][2] = acc[c][n][3] = 0.f;
-    // rows 8 n + 2 t4, + 1 of this thread
-    float m[NT][2], l[NT][2], rs[NT][2];
+    // rows 8 n + 2 t4, + 1 of this thread: P's reference (m - kQuantTop; a row
+    // without one yet, 0), its sum, the scale of its scores
+    float mu[NT][2], l[NT][2], rs[NT][2];
+    bool has[NT][2];
+    constexpr bool QREG = NT * CPR <= 16;  // Q's fragments in registers
+    uint2 qr[QREG ? CPR : 1][NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float2 r = *reinterpret_cast<const float2 *>(rowsc + buf * NR + 8 * n + 2 * t4);
+      const int2 hi = *reinterpret_cast<const int2 *>(rowhi + buf * NR + 8 * n + 2 * t4);
       rs[n][0] = r.x;
       rs[n][1] = r.y;
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
+      has[n][0] = hi.x <= 0;  // (a row without keys needs none)
+      has[n][1] = hi.y <= 0;
+      mu[n][0] = mu[n][1] = l[n][0] = l[n][1] = 0.f;
+      if constexpr (QREG) {
+#pragma unroll
+        for (int c = 0; c < CPR; ++c) qr[c][n] = qf[(c * NT + n) * 32];
+      }
     }
+    bool settled = false;  // every row has its reference
 #pragma unroll 1
     for (int st = 0; st < mine; ++st) {
       copy_wait<NS - 2>();
       __syncwarp();
-      issue();
-      const uint32_t stage = ring_at + out_slot * STAGE;
-      const float2 *scales = reinterpret_cast<const float2 *>(ring + out_slot * STAGE + TB * (2 * BLOCK));
+      issue((NS - 1) & 1);
+      const uint32_t kb = ring_at + out_slot * SLOT;
+      const float2 *scales = reinterpret_cast<const float2 *>(ring + out_slot * SLOT + TB * BLOCK);
       if (++out_slot == NS) out_slot = 0;
       const int blk = q.b0 + (first + st * NW) * TB;
-      const int nbt = min(TB, q.b1 - blk);
 
-      // S^T = K Q^T
-      float sc[TB][NT][4];
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sc[b][n][0] = sc[b][n][1] = sc[b][n][2] = sc[b][n][3] = 0.f;
+      // S^T = K Q^T (in two sums where few products are independent)
+      constexpr bool TWO = TB * NT <= 2;
+      float sc[TB][NT][4], sd[TB][NT][4];
 #pragma unroll
       for (int c = 0; c < CPR; c += 2) {
         uint2 qa[NT], qb[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          qa[n] = qf[(c * NT + n) * 32];
-          qb[n] = qf[((c + 1) * NT + n) * 32];
+          qa[n] = QREG ? qr[QREG ? c : 0][n] : qf[(c * NT + n) * 32];
+          qb[n] = QREG ? qr[QREG ? c + 1 : 0][n] : qf[((c + 1) * NT + n) * 32];
         }
+        uint32_t x[TB][4], y[TB][4];
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
-          if (b < nbt) {
-            // (rows 0-7, 8-15) of chunk c, then of chunk c + 1
-            uint32_t w[4];
-            ldsm_x4(stage + b * (2 * BLOCK) + place_of(a_row, c + a_hi), w);
-            uint32_t x[4], y[4];
-            halves_of(w[0], x[0], x[2]);
-            halves_of(w[1], x[1], x[3]);
-            halves_of(w[2], y[0], y[2]);
-            halves_of(w[3], y[1], y[3]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_16816<false>(sc[b][n], x, qa[n].x, qa[n].y);
-              mma_16816<false>(sc[b][n], y, qb[n].x, qb[n].y);
-            }
-          }
+          // (rows 0-7, 8-15) of chunk c, then of chunk c + 1
+          uint32_t w[4];
+          ldsm_x4(kb + b * BLOCK + place_of(a_row, c + a_hi), w);
+          halves_of(w[0], x[b][0], x[b][2]);
+          halves_of(w[1], x[b][1], x[b][3]);
+          halves_of(w[2], y[b][0], y[b][2]);
+          halves_of(w[3], y[b][1], y[b][3]);
         }
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (c == 0)
+              mma_first(sc[b][n], x[b], qa[n].x, qa[n].y);
+            else
+              mma_16816<false>(sc[b][n], x[b], qa[n].x, qa[n].y);
+          }
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (!TWO)
+              mma_16816<false>(sc[b][n], y[b], qb[n].x, qb[n].y);
+            else if (c == 0)
+              mma_first(sd[b][n], y[b], qb[n].x, qb[n].y);
+            else
+              mma_16816<false>(sd[b][n], y[b], qb[n].x, qb[n].y);
+          }
+      }
+      if constexpr (TWO) {
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[b][n][e] += sd[b][n][e];
       }
 
-      // scale, mask, running maximum of a = s + log2(v_scale)
-      float mx[NT][2], inv[TB];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-      int key0[TB];
+      // x = a - mu = log2 of P
+      float inv[TB];
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        const int i = blk + b;
-        key0[b] = (i >= q.r.sk_nb ? i + q.r.sk_gap : i) * kBlockKeys;
-        inv[b] = 0.f;
-        if (b >= nbt) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) sc[b][n][0] = sc[b][n][1] = sc[b][n][2] = sc[b][n][3] = -INFINITY;
-          continue;
-        }
         const float2 kv = scales[b];
         const float lg = __log2f(kv.y);
         inv[b] = sfu_rcp(kv.y);
-        // (does every row see all 16 keys)
-        const bool all = key0[b] + kBlockKeys <= q.r.v_hi &&
-                         (key0[b] >= q.r.v_lo || key0[b] + kBlockKeys <= p.sinks);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float f0 = rs[n][0] * kv.x, f1 = rs[n][1] * kv.x;
-          sc[b][n][0] = fmaf(sc[b][n][0], f0, lg);
-          sc[b][n][1] = fmaf(sc[b][n][1], f1, lg);
-          sc[b][n][2] = fmaf(sc[b][n][2], f0, lg);
-          sc[b][n][3] = fmaf(sc[b][n][3], f1, lg);
-          if (!all) {
+          const float f0 = rs[n][0] * kv.x, f1 = rs[n][1] * kv.x, g0 = lg - mu[n][0], g1 = lg - mu[n][1];
+          sc[b][n][0] = fmaf(sc[b][n][0], f0, g0);
+          sc[b][n][1] = fmaf(sc[b][n][1], f1, g1);
+          sc[b][n][2] = fmaf(sc[b][n][2], f0, g0);
+          sc[b][n][3] = fmaf(sc[b][n][3], f1, g1);
+        }
+      }
+      // blocks that some row does not see whole, or that the piece does not have
+      const bool whole = blk + TB <= q.b1 && ((blk >= q.r.all_lo && blk + TB <= q.r.all_hi) || blk + TB <= q.r.all_sk);
+      if (!whole) {
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+          const int i = blk + b;
+          const bool there = i < q.b1;
+          const int ka = (i >= q.r.sk_nb ? i + q.r.sk_gap : i) * kBlockKeys + g8, kb8 = ka + 8;
+          if (!there) inv[b] = 0.f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
             const int2 hi = *reinterpret_cast<const int2 *>(rowhi + buf * NR + 8 * n + 2 * t4);
             const int lo0 = p.window > 0 ? max(0, hi.x - p.window) : 0;
             const int lo1 = p.window > 0 ? max(0, hi.y - p.window) : 0;
-            const int ka = key0[b] + g8, kb = ka + 8;
-            if (!sees(ka, lo0, hi.x)) sc[b][n][0] = -INFINITY;
-            if (!sees(ka, lo1, hi.y)) sc[b][n][1] = -INFINITY;
-            if (!sees(kb, lo0, hi.x)) sc[b][n][2] = -INFINITY;
-            if (!sees(kb, lo1, hi.y)) sc[b][n][3] = -INFINITY;
+            if (!there || !sees(ka, lo0, hi.x)) sc[b][n][0] = -INFINITY;
+            if (!there || !sees(ka, lo1, hi.y)) sc[b][n][1] = -INFINITY;
+            if (!there || !sees(kb8, lo0, hi.x)) sc[b][n][2] = -INFINITY;
+            if (!there || !sees(kb8, lo1, hi.y)) sc[b][n][3] = -INFINITY;
           }
-          mx[n][0] = fmaxf(mx[n][0], fmaxf(sc[b][n][0], sc[b][n][2]));
-          mx[n][1] = fmaxf(mx[n][1], fmaxf(sc[b][n][1], sc[b][n][3]));
         }
       }
-      bool grew = false;
-      float mu[NT][2], al[NT][2];
+      float top = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int b = 0; b < TB; ++b)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int n = 0; n < NT; ++n)
+          top = fmaxf(fmaxf(top, fmaxf(sc[b][n][0], sc[b][n][1])), fmaxf(sc[b][n][2], sc[b][n][3]));
+      if (!settled || __any_sync(0xffffffffu, top > kQuantMost)) {
+        // the rows' references up to their largest a
+        float al[NT][2];
+        bool all = true;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
-          const float mn = fmaxf(m[n][e], mx[n][e]);
-          mu[n][e] = (mn == -INFINITY ? 0.f : mn) - kQuantTop;
-          al[n][e] = sfu_exp2(m[n][e] - (mn == -INFINITY ? 0.f : mn));  // m = -inf -> 0
-          grew |= al[n][e] != 1.f;
-          m[n][e] = mn;
-          l[n][e] *= al[n][e];
-        }
-      if (__any_sync(0xffffffffu, grew)) {
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < TB; ++b) mx = fmaxf(mx, fmaxf(sc[b][n][e], sc[b][n][e + 2]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const bool any = mx > -INFINITY;
+            const float up = !any ? 0.f : has[n][e] ? fmaxf(mx - kQuantTop, 0.f) : mx - kQuantTop;
+            al[n][e] = has[n][e] ? sfu_exp2(-up) : 1.f;  // (nothing summed before the first)
+            has[n][e] |= any;
+            all &= has[n][e];
+            mu[n][e] += up;
+            l[n][e] *= al[n][e];
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+              sc[b][n][e] -= up;
+              sc[b][n][e + 2] -= up;
+            }
+          }
+        settled = __all_sync(0xffffffffu, all);
 #pragma unroll
         for (int c = 0; c < CPR; ++c)
 #pragma unroll
@@ -562,57 +676,62 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
             acc[c][n][3] *= al[n][1];
           }
       }
-
-      // P, then O^T += V^T P^T
+      // P
+      uint32_t pb[TB][NT][2];
 #pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        if (b >= nbt) continue;
-        uint32_t pb[NT][2];
+      for (int b = 0; b < TB; ++b)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float p0 = sfu_exp2(sc[b][n][0] - mu[n][0]), p1 = sfu_exp2(sc[b][n][1] - mu[n][1]);
-          const float p2 = sfu_exp2(sc[b][n][2] - mu[n][0]), p3 = sfu_exp2(sc[b][n][3] - mu[n][1]);
+          const float p0 = sfu_exp2(sc[b][n][0]), p1 = sfu_exp2(sc[b][n][1]);
+          const float p2 = sfu_exp2(sc[b][n][2]), p3 = sfu_exp2(sc[b][n][3]);
           l[n][0] = fmaf(p0 + p2, inv[b], l[n][0]);
           l[n][1] = fmaf(p1 + p3, inv[b], l[n][1]);
-          pb[n][0] = movmatrix_trans(pack2(p0, p1, std::integral_constant<bool, false>{}));
-          pb[n][1] = movmatrix_trans(pack2(p2, p3, std::integral_constant<bool, false>{}));
+          pb[b][n][0] = movmatrix_trans(pack2(p0, p1, std::integral_constant<bool, false>{}));
+          pb[b][n][1] = movmatrix_trans(pack2(p2, p3, std::integral_constant<bool, false>{}));
         }
-        // zero V of keys that no row sees (stale or NaN slots)
-        const bool vmask = !(key0[b] >= q.r.u_lo && key0[b] + kBlockKeys <= q.r.u_hi);
-        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
-        if (vmask) {
-          const int ke = key0[b] + 2 * t4;
-          mlo = (sees(ke, q.r.u_lo, q.r.u_hi) ? 0x0000ffffu : 0u) |
-                (sees(ke + 1, q.r.u_lo, q.r.u_hi) ? 0xffff0000u : 0u);
-          mhi = (sees(ke + 8, q.r.u_lo, q.r.u_hi) ? 0x0000ffffu : 0u) |
-                (sees(ke + 9, q.r.u_lo, q.r.u_hi) ? 0xffff0000u : 0u);
+
+      // O^T += V^T P^T
+      copy_wait<NS - 2>();
+      __syncwarp();
+      issue(NS & 1);
+      const uint32_t vb = ring_at + out_slot * SLOT;
+      if (!whole) {
+        // V of keys that no row sees (stale or NaN slots), or that are not there: zeros
+#pragma unroll 1
+        for (int j = lane; j < TB * kBlockKeys * CPR; j += 32) {
+          const int i = blk + j / (kBlockKeys * CPR), tok = j / CPR % kBlockKeys;
+          const int key = (i >= q.r.sk_nb ? i + q.r.sk_gap : i) * kBlockKeys + tok;
+          if (i >= q.b1 || !sees(key, q.r.u_lo, q.r.u_hi))
+            *reinterpret_cast<uint4 *>(ring + out_slot * SLOT + j * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
-        const uint32_t vb = stage + b * (2 * BLOCK) + BLOCK;
+        __syncwarp();
+      }
+      if (++out_slot == NS) out_slot = 0;
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
 #pragma unroll
         for (int c = 0; c < CPR; c += 2) {
           // (keys 0-7, 8-15) of chunk c, then of chunk c + 1: two keys' codes of
           // dims 2 g8, 2 g8 + 1 a register
           uint32_t w[4];
-          ldsm_x4_trans(vb + place_of(a_row, c + a_hi), w);
+          ldsm_x4_trans(vb + b * BLOCK + place_of(a_row, c + a_hi), w);
           uint32_t x[4], y[4];
           halves_of(__byte_perm(w[0], 0u, 0x3120), x[0], x[1]);
           halves_of(__byte_perm(w[1], 0u, 0x3120), x[2], x[3]);
           halves_of(__byte_perm(w[2], 0u, 0x3120), y[0], y[1]);
           halves_of(__byte_perm(w[3], 0u, 0x3120), y[2], y[3]);
-          if (vmask) {
-            x[0] &= mlo; x[1] &= mlo; x[2] &= mhi; x[3] &= mhi;
-            y[0] &= mlo; y[1] &= mlo; y[2] &= mhi; y[3] &= mhi;
-          }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_16816<false>(acc[c][n], x, pb[n][0], pb[n][1]);
-            mma_16816<false>(acc[c + 1][n], y, pb[n][0], pb[n][1]);
-          }
+          for (int n = 0; n < NT; ++n) mma_16816<false>(acc[c][n], x, pb[b][n][0], pb[b][n][1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816<false>(acc[c + 1][n], y, pb[b][n][0], pb[b][n][1]);
         }
-      }
     }
 
     // ---- the piece's end: the warps' sums added, rows stored or published ----
+    // A warp's sums go to its ring's free slot (the one that the next copies are
+    // for), DC columns at a time.
+    const bool more = k + 1 < n_pieces;
+    if (more) fetch_q(pieces[(k + 1) & (kPieces - 1)]);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -621,53 +740,68 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
         for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
       }
       if (lane < 4) {
-        ml_of[warp * NR + 8 * n + 2 * lane] = make_float2(m[n][0], l[n][0]);
-        ml_of[warp * NR + 8 * n + 2 * lane + 1] = make_float2(m[n][1], l[n][1]);
+        // (of a row without a visible key here: no maximum)
+        ml_of[(8 * n + 2 * lane) * NW + warp] = make_float2(l[n][0] > 0.f ? mu[n][0] : -INFINITY, l[n][0]);
+        ml_of[(8 * n + 2 * lane + 1) * NW + warp] = make_float2(l[n][1] > 0.f ? mu[n][1] : -INFINITY, l[n][1]);
       }
     }
+    if (lane == 0) free_slot[warp] = (warp * NS + in_slot) * SLOT;
     const bool cut = q.parts > 1;
+    __syncwarp();  // (every lane has read the slot)
 #pragma unroll
     for (int ps = 0; ps < PASSES; ++ps) {
-      // column d of row r at d ^ 8 (r / 2 % 4): a warp's stores hit every bank once
-      float *mine_at = cp + warp * (NR * DC);
+      // column d of row r at d ^ 8 (r / 2 % 4) (but for few columns): a warp's stores hit
+      // every bank once
+      float *mine_at = reinterpret_cast<float *>(ring + in_slot * SLOT);
 #pragma unroll
       for (int c = 0; c < CPP; ++c)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const int r0 = 8 * n + 2 * t4, d = (16 * c + 2 * g8) ^ (t4 << 3);
+          const int r0 = 8 * n + 2 * t4, d = (16 * c + 2 * g8) ^ ((t4 << 3) & SWIZZLE);
           const float(&a)[4] = acc[ps * CPP + c][n];
           *reinterpret_cast<float2 *>(mine_at + r0 * DC + d) = make_float2(a[0], a[2]);
           *reinterpret_cast<float2 *>(mine_at + (r0 + 1) * DC + d) = make_float2(a[1], a[3]);
         }
       __syncthreads();
-      if (ps == 0 && k + 1 < n_pieces) load_q(piece_at(k + 1), buf ^ 1);
-      for (int it = tid; it < NR * (DC / 4); it += nthr) {
+      if (ps == 0) {
+        // a row's weights of the warps' sums: eight lanes
+        if (tid < NR * NW) {
+          const float2 t = ml_of[tid];
+          float M = t.x;
+#pragma unroll
+          for (int o = 1; o < NW; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          const float f = exp2_or_zero(t.x, M == -INFINITY ? 0.f : M);
+          float ls = f * t.y;
+#pragma unroll
+          for (int o = 1; o < NW; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+          weight[tid] = f;
+          if (tid % NW == 0) total[tid / NW] = make_float2(M, ls);
+        }
+        __syncthreads();
+      }
+#pragma unroll 1
+      for (int it = tid; it < NR * (DC / 4); it += NTHR) {
         const int rr = it / (DC / 4), d4 = it - rr * (DC / 4);
         if (!row_live(q, rr)) continue;
-        float M = -INFINITY;
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, ml_of[w * NR + rr].x);
-        const float mm = M == -INFINITY ? 0.f : M;
+        const float2 t = total[rr];
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float ls = 0.f;
-        for (int w = 0; w < NW; ++w) {
-          const float2 t = ml_of[w * NR + rr];
-          const float f = exp2_or_zero(t.x, mm);
-          const float4 a = *reinterpret_cast<const float4 *>(cp + (w * NR + rr) * DC +
-                                                              ((4 * d4) ^ (((rr >> 1) & 3) << 3)));
-          ls = fmaf(f, t.y, ls);
-          o.x = fmaf(f, a.x, o.x);
-          o.y = fmaf(f, a.y, o.y);
-          o.z = fmaf(f, a.z, o.z);
-          o.w = fmaf(f, a.w, o.w);
-        }
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          add_scaled(o, weight[rr * NW + w],
+                     *reinterpret_cast<const float4 *>(smem + free_slot[w] +
+                                                       4 * (rr * DC + ((4 * d4) ^ (((rr >> 1 & 3) << 3) & SWIZZLE)))));
         const int d = ps * DC + 4 * d4;
         if (!cut) {
-          store_four<BF16>(out_row(q, rr) + d, o, ls > 0.f ? 1.f / ls : 0.f);
+          store_four<BF16>(out_row(q, rr) + d, o, t.y > 0.f ? 1.f / t.y : 0.f);
         } else {
-          const int64_t at = slot_of(q, q.part) * NR + rr;
-          __stcg(reinterpret_cast<float4 *>(p.part_acc + at * D + d), o);
-          if (d == 0) __stcg(reinterpret_cast<float2 *>(p.part_ml + at * 2), make_float2(M, ls));
+          const int64_t to = slot_of(q, q.part) * NR + rr;
+          __stcg(reinterpret_cast<float4 *>(p.part_acc + to * D + d), o);
+          if (d == 0) __stcg(reinterpret_cast<float2 *>(p.part_ml + to * 2), t);
         }
+      }
+      if (ps == PASSES - 1) {
+        if (more) put_q(pieces[(k + 1) & (kPieces - 1)], buf ^ 1);
+        if (tid == NTHR - 1 && k + 2 < n_pieces) pieces[(k + 2) & (kPieces - 1)] = piece_at(k + 2);
       }
       __syncthreads();
     }
@@ -677,32 +811,36 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
       if (tid == 0) {
         const int u = ((s_first + q.i) * p.Hkv + q.h) * p.rg + q.g;
         const int old = atomic_add_acq_rel_gpu(p.counters + u, 1);
-        if (n_cut == 0) cut_old[0] = old; else cut_old[1] = old;
+        if (n_cut == 0) cut_old0 = old; else cut_old1 = old;
       }
-      if (n_cut == 0) cut_k[0] = k; else cut_k[1] = k;
+      if (n_cut == 0) cut_k0 = k; else cut_k1 = k;
       ++n_cut;
     }
   }
   grid_dependents_launch();
 
   // ---- cut units whose last part is this CTA's: merged ------------------------
-  for (int c = 0; c < n_cut; ++c) {
-    const Piece q = piece_at(c == 0 ? cut_k[0] : cut_k[1]);
+  if (n_cut > 0) {
     if (tid == 0) {
-      const int old = c == 0 ? cut_old[0] : cut_old[1];
-      if (old < 0 || old >= q.parts) atomicOr(p.status, PD_DEV_BAD_SCRATCH);  // not zero at the start
-      flag[c] = old == q.parts - 1;
-      if (old == q.parts - 1) {
-        const int u = ((s_first + q.i) * p.Hkv + q.h) * p.rg + q.g;
-        atomicExch(p.counters + u, 0);
+      for (int c = 0; c < n_cut; ++c) {
+        const Piece q = piece_at(c == 0 ? cut_k0 : cut_k1);
+        const int old = c == 0 ? cut_old0 : cut_old1;
+        if (old < 0 || old >= q.parts) atomicOr(p.status, PD_DEV_BAD_SCRATCH);  // not zero at the start
+        flag[2 + c] = old == q.parts - 1;
+        if (old == q.parts - 1) atomicExch(p.counters + ((s_first + q.i) * p.Hkv + q.h) * p.rg + q.g, 0);
       }
     }
     __syncthreads();
-    if (!flag[c]) continue;
+  }
+#pragma unroll 1
+  for (int c = 0; c < n_cut; ++c) {
+    if (!flag[2 + c]) continue;
+    const Piece q = piece_at(c == 0 ? cut_k0 : cut_k1);
     constexpr int CH = 8;  // parts whose loads are in flight
-    for (int it = tid; it < NR * (D / 4); it += nthr) {
+    const int rows = min(p.rows_grp, q.r.ml * p.G - q.g * p.rows_grp), items = rows * (D / 4);
+#pragma unroll 1
+    for (int it = tid; it < items; it += NTHR) {
       const int rr = it / (D / 4), d = 4 * (it - rr * (D / 4));
-      if (!row_live(q, rr)) continue;
       float M = -INFINITY, ls = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int c0 = 0; c0 < q.parts; c0 += CH) {
@@ -710,9 +848,9 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
         float4 a[CH];
 #pragma unroll
         for (int w = 0; w < CH; ++w) {
-          const int64_t at = slot_of(q, min(c0 + w, q.parts - 1)) * NR + rr;
-          t[w] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at * 2));
-          a[w] = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + at * D + d));
+          const int64_t from = slot_of(q, min(c0 + w, q.parts - 1)) * NR + rr;
+          t[w] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + from * 2));
+          a[w] = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + from * D + d));
           if (c0 + w >= q.parts) t[w] = make_float2(-INFINITY, 0.f);
         }
         float mn = M;
@@ -727,10 +865,7 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
         for (int w = 0; w < CH; ++w) {
           const float f = exp2_or_zero(t[w].x, mm);
           ls = fmaf(f, t[w].y, ls);
-          o.x = fmaf(f, a[w].x, o.x);
-          o.y = fmaf(f, a[w].y, o.y);
-          o.z = fmaf(f, a[w].z, o.z);
-          o.w = fmaf(f, a[w].w, o.w);
+          add_scaled(o, f, a[w]);
         }
       }
       store_four<BF16>(out_row(q, rr) + d, o, ls > 0.f ? 1.f / ls : 0.f);
@@ -742,7 +877,7 @@ __global__ void __launch_bounds__(32 * quant_max_warps(D, NT), 1)
     // see no key: zeros
     const int t0 = starts[S], per_row = p.Hq * (D / 8);
     const int64_t n = (int64_t)(p.num_tokens - t0) * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * nthr + tid; i < n; i += (int64_t)gridDim.x * nthr) {
+    for (int64_t i = (int64_t)blockIdx.x * NTHR + tid; i < n; i += (int64_t)gridDim.x * NTHR) {
       const int t = t0 + (int)(i / per_row), rem = (int)(i - (int64_t)(t - t0) * per_row);
       const int hq = rem / (D / 8), c = rem - hq * (D / 8);
       *reinterpret_cast<uint4 *>(obase + (int64_t)t * p.o_s0 + (int64_t)hq * p.o_s1 + c * 8) =

@@ -4,6 +4,7 @@
 // a thread turns 16 codes into 16 values at a time, K and V of every head.  The
 // tables and lengths of the next block are on their way while this one's codes
 // are.  Memory-bound: 1 byte read and 2 written a value.
+#include "pd_e4m3.cuh"
 #include "pd_quant.h"
 #include "pd_rope.cuh"
 
@@ -89,15 +90,10 @@ __global__ void __launch_bounds__(kThreads) pd_quant_read(const __grid_constant_
             uint32_t out[8];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-              uint32_t lo, hi;
-              asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
-                  " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-                  : "=r"(lo), "=r"(hi)
-                  : "r"(words[z]));
-              const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-              const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-              out[2 * z] = Elem<BF16>::from2(a.x * f[u], a.y * f[u]);
-              out[2 * z + 1] = Elem<BF16>::from2(b.x * f[u], b.y * f[u]);
+              float x[4];
+              floats4(words[z], x);
+              out[2 * z] = Elem<BF16>::from2(x[0] * f[u], x[1] * f[u]);
+              out[2 * z + 1] = Elem<BF16>::from2(x[2] * f[u], x[3] * f[u]);
             }
             uint4 *at = reinterpret_cast<uint4 *>(to[u]);
             at[0] = make_uint4(out[0], out[1], out[2], out[3]);

@@ -13,6 +13,7 @@
 // code, which sits on a rounding, does not depend on how a compiler pairs them.
 //
 // Memory-bound: every byte is read or written once but for the rescaled codes.
+#include "pd_e4m3.cuh"
 #include "pd_quant.h"
 #include "pd_rope.cuh"
 
@@ -157,25 +158,6 @@ __device__ __forceinline__ void q_tokens(const QuantWriteParams &p, int t0, floa
       }
     }
   }
-}
-
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
-      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
-      : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-__device__ __forceinline__ void floats4(uint32_t w, float (&x)[4]) {
-  uint32_t lo, hi;
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
 
 // The smallest power of two, 2^kLeast at least, under which a is at most 448 =
