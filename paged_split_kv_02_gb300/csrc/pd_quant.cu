@@ -216,6 +216,8 @@ PD_API int paged_decode_attn_quant(const pd_tensor *q, const pd_tensor *k_cache,
   p.seqs_y = plan.seqs_y;
   p.whole = plan.whole;
   p.min_share = 8;
+  p.min_part = 8;
+  p.align_slack = 30 * 128 / head_size;
   p.bpp = page_size / kBlockKeys;
   p.by_units = FastDiv(num_kv_heads * p.rg);
   p.by_groups = FastDiv(p.rg);

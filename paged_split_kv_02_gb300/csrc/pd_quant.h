@@ -52,6 +52,8 @@ struct QuantAttnParams {
   int seqs_y;        // sequences of one blockIdx.y
   int whole;         // 1: no unit is cut
   int min_share;     // the least share of a CTA
+  int min_part;      // the fewest blocks of a part of an aligned unit
+  int align_slack;   // what parts of single units may be longer than equal shares
   FastDiv by_units, by_groups, by_heads, by_page, by_ctas;  // Hkv rg, rg, G, bpp, gridDim.x
   float *part_acc, *part_ml;  // [2 x CTAs][8 NT][D], [..][8 NT][2]
   int *counters;              // parts published of each unit
@@ -61,7 +63,7 @@ struct QuantAttnParams {
 // What a unit counts in the line of blocks beside its blocks (its Q, its end).
 constexpr int kQuantUnitCost = 12;
 // Sequences of one line at most (their lengths and places lie in shared memory).
-constexpr int kQuantSeqs = 1024;
+constexpr int kQuantSeqs = 512;
 constexpr int kQuantWarps = 8;
 #ifndef QTB
 #define QTB (D == 64 ? (NT <= 2 ? 4 : 2) : D == 128 ? 2 : 1)
@@ -77,14 +79,17 @@ constexpr int quant_slot_bytes(int D, int NT) { return quant_step_blocks(D, NT) 
 constexpr int quant_passes(int D, int NT) {
   return 2 * NT > quant_step_blocks(D, NT) ? 2 * NT / quant_step_blocks(D, NT) : 1;
 }
-constexpr int kQuantRunBytes = 40, kQuantPieceBytes = 80;
+// pieces of a share whose place is known at a time (a power of two): a warp looks
+// at most four runs of its own ahead, and one of eight pieces has one
+constexpr int kQuantPieces = 64;
+constexpr int kQuantRunBytes = 40, kQuantPieceBytes = 76;
 // Dynamic shared memory: the warps' rings, two sets of Q fragments, row scales and
-// row ends, the warps' (m, l) and weights of the rows and their totals, four
-// pieces, two runs of each warp, sums and flags, lengths, first rows and places.
+// row ends, the warps' (m, l) of the rows, the pieces, two runs of each warp, sums
+// and flags, lengths, first rows, order and places.
 constexpr int smem_bytes_quant(int D, int NT, int seqs) {
   return 128 + kQuantWarps * quant_slots(D, NT) * quant_slot_bytes(D, NT) + 2 * (NT * 16 * D + 8 * NT * 8) +
-         8 * NT * (kQuantWarps * 12 + 8) + 4 * kQuantPieceBytes + kQuantWarps * 2 * kQuantRunBytes +
-         4 * (2 * kQuantWarps + 8) + 4 * (3 * seqs + 1);
+         8 * NT * kQuantWarps * 8 + (kQuantPieces + 2) * kQuantPieceBytes + kQuantWarps * 2 * kQuantRunBytes +
+         4 * (3 * kQuantWarps + 8) + 4 * (4 * seqs + 1);
 }
 
 cudaError_t launch_quant_d64(bool bf16, int nt, const QuantAttnParams &p, const Launch &l, cudaStream_t stream);

@@ -128,7 +128,7 @@ struct QuantRun {
 // A piece of a CTA's share: some or all blocks of one unit.
 struct QuantPiece {
   QuantSeq r;
-  int i, h, g;          // sequence (of this line), kv head, row group
+  int s, h, g;          // sequence, kv head, row group
   int b0, b1;           // its blocks of the unit
   int part, parts, first_cta;
 };
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   constexpr int SWIZZLE = DC >= 32 ? 24 : DC - 8;  // of the columns of the warps' sums
   constexpr int SPC = 32 / TB;                // steps whose page ids a warp holds
   constexpr int NTHR = 32 * NW;
-  constexpr int kPieces = 4;                  // pieces whose place is known at a time
+  constexpr int kPieces = kQuantPieces;       // pieces whose place is known at a time
 
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
@@ -159,17 +159,17 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   float *rowsc = reinterpret_cast<float *>(qfrag + 2 * CPR * NT * 32);     // [2][NR]
   int *rowhi = reinterpret_cast<int *>(rowsc + 2 * NR);                    // [2][NR]
   float2 *ml_of = reinterpret_cast<float2 *>(rowhi + 2 * NR);              // [NR][NW] (m, l) of the warps
-  float *weight = reinterpret_cast<float *>(ml_of + NR * NW);              // [NR][NW]
-  float2 *total = reinterpret_cast<float2 *>(weight + NR * NW);            // [NR] (m, l) of the piece
-  QuantPiece *pieces = reinterpret_cast<QuantPiece *>(total + NR);         // [kPieces]
-  QuantRun *runs = reinterpret_cast<QuantRun *>(reinterpret_cast<unsigned char *>(pieces) +
-                                                kPieces * kQuantPieceBytes) + 2 * warp;  // [NW][2]
-  int *sums = reinterpret_cast<int *>(runs - 2 * warp + 2 * NW);           // [NW]
-  int *free_slot = sums + NW;                                              // [NW]
-  volatile int *flag = free_slot + NW;                                     // [8]: first unit, last unit, merges
+  QuantPiece *pieces = reinterpret_cast<QuantPiece *>(ml_of + NR * NW);    // [kPieces], by piece % kPieces
+  QuantPiece *cut_piece = pieces + kPieces;                                // [2]
+  QuantRun *runs = reinterpret_cast<QuantRun *>(cut_piece + 2) + 2 * warp;  // [NW][2]
+  int *sums = reinterpret_cast<int *>(runs - 2 * warp + 2 * NW);           // [2 NW]
+  int *free_slot = sums + 2 * NW;                                              // [NW]
+  volatile int *flag = free_slot + NW;                                     // [8]
   int *lens = free_slot + NW + 8;                                          // [seqs]
   int *starts = lens + p.seqs_y;                                           // [seqs + 1]
-  int *place = starts + p.seqs_y + 1;                                      // [seqs]
+  // of the sequences with a visible key, in order: which, and their places on the line
+  int *order = starts + p.seqs_y + 1;                                      // [seqs]
+  int *place = order + p.seqs_y;                                           // [seqs]
 
   const int s_first = blockIdx.y * p.seqs_y, S = min(p.seqs_y, p.num_seqs - s_first);
   const int HR = p.Hkv * p.rg;  // units of a sequence
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   // ---- the lengths, clamped and reported; their places on the line -----------
   // (a thread has a run of sequences)
   const int per = (S + NTHR - 1) / NTHR, i0 = min(tid * per, S), i1 = min(i0 + per, S);
-  int sum = 0;
+  int sum = 0, full = 0;  // its places, and its sequences with a visible key
   {
     const int cap = p.bt_width * p.P;
     unsigned int bad = 0;
@@ -196,20 +196,32 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
       }
       if (L > cap) bad |= PD_DEV_BAD_SEQLEN;
       lens[i] = min(max(L, 0), cap);
-      sum += (quant_seq(lens[i], q0, ml, p.window, p.sinks).nb + kQuantUnitCost) * HR;
+      const int nb = quant_seq(lens[i], q0, ml, p.window, p.sinks).nb;
+      if (nb > 0) {
+        sum += (nb + kQuantUnitCost) * HR;
+        ++full;
+      }
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
   }
-  int inc = sum;
+  // an inclusive sum over the CTA's threads (of values that a scan needs) and a total
+  auto scan = [&](int v) -> int {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  int inc = scan(sum);
+  const int inc_full = scan(full);
+  if (lane == 31) {
+    sums[warp] = inc;
+    sums[NW + warp] = inc_full;
   }
-  if (lane == 31) sums[warp] = inc;
   if (tid == 0) {
     flag[0] = 1;
-    flag[1] = 0;
+    flag[1] = flag[2] = 0;
   }
   __syncthreads();
   auto seq_of = [&](int i) -> QuantSeq {
@@ -221,74 +233,134 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     return quant_seq(lens[i], q0, ml, p.window, p.sinks);
   };
 
-  // ---- this CTA's share: units [unit0, unit0 + n_pieces) of the line ---------
-  int unit0, n_pieces;
-  int x0 = 0, x1 = 0, share = 1;
-  if (p.whole) {
-    const int64_t U = (int64_t)S * HR;
-    unit0 = (int)(U * blockIdx.x / gridDim.x);
-    n_pieces = (int)(U * (blockIdx.x + 1) / gridDim.x) - unit0;
-  } else {
-    int base = 0, W = 0;
+  // ---- this CTA's share -------------------------------------------------------
+  // whole: a unit to a CTA (no scratch for parts).  aligned: a unit is cut into parts
+  // of its own, one to a CTA, where units are few and that costs little: no CTA then
+  // ends two units.  Else a length of the line, from any place of a unit.
+  int unit0 = 0, n_pieces = 0, x0 = 0, x1 = 0, share = 1;
+  bool tail = false, aligned = false;
+  const int G = gridDim.x;
+  int base = 0, W = 0, rank = inc_full - full, U = 0;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int v = sums[i];
-      if (i < warp) base += v;
-      W += v;
+  for (int i = 0; i < NW; ++i) {
+    if (i < warp) {
+      base += sums[i];
+      rank += sums[NW + i];
     }
-    share = max(p.min_share, (int)p.by_ctas.div(W + (int)gridDim.x - 1));
-    x0 = (int)min((int64_t)blockIdx.x * share, (int64_t)W);
-    x1 = (int)min((int64_t)x0 + share, (int64_t)W);
-    // the units that its first and its last place are in
-    int at = base + inc - sum;
-    for (int i = i0; i < i1; ++i) {
-      place[i] = at;
-      const int nb = seq_of(i).nb, cost = nb + kQuantUnitCost, next = at + cost * HR;
-      if (x0 < x1 && x0 >= at && x0 < next) {
-        const int k = div_near(x0 - at, cost), in = x0 - at - k * cost;
-        // (a first unit whose blocks, or whose place if it has none, lie before the share)
-        flag[0] = i * HR + k + (in > 0 && in >= nb ? 1 : 0);
+    W += sums[i];
+    U += sums[NW + i];
+  }
+  U *= HR;  // units with blocks
+  if (!p.whole) {
+    share = max(p.min_share, (int)p.by_ctas.div(W + G - 1));
+    if (U > 0 && 2 * U <= G) {
+      // parts of s blocks take N / s + U CTAs at most; of one sequence, whose units are alike, no more than G
+      // (approximate quotients, rounded up past their error)
+      const float N = (float)(W - U * kQuantUnitCost);
+      const int s = max(p.min_part, (int)(1.f + 1.00001f * (S == 1 ? __fdividef(N, (float)(U * div_near(G, U)))
+                                                        : __fdividef(N, (float)(G - U)))));
+      if (s + kQuantUnitCost <= share + p.align_slack) {
+        aligned = true;
+        share = s;  // (blocks of a part)
+        sum = 0;
+        for (int i = i0; i < i1; ++i) {
+          const int nb = seq_of(i).nb;
+          if (nb > 0) sum += (div_near(nb - 1, s) + 1) * HR;
+        }
+        if (S == 1) {
+          // (thread 0 has it)
+          inc = sum;
+          base = 0;
+          W = __shfl_sync(0xffffffffu, sum, 0);
+          if (warp > 0) W = (div_near(seq_of(0).nb - 1, s) + 1) * HR;
+        } else {
+          __syncthreads();  // (the sums are read)
+          inc = scan(sum);
+          if (lane == 31) sums[warp] = inc;
+          __syncthreads();
+          base = W = 0;
+#pragma unroll
+          for (int i = 0; i < NW; ++i) {
+            if (i < warp) base += sums[i];
+            W += sums[i];
+          }
+        }
       }
-      if (x0 < x1 && x1 - 1 >= at && x1 - 1 < next) flag[1] = i * HR + div_near(x1 - 1 - at, cost);
-      at = next;
     }
-    __syncthreads();
+    // (aligned: a place is a CTA)
+    x0 = (int)min((int64_t)blockIdx.x * (aligned ? 1 : share), (int64_t)W);
+    x1 = (int)min((int64_t)x0 + (aligned ? 1 : share), (int64_t)W);
+  }
+  // the sequences' places, and the units that the share's first and last place are in
+  int place_at = base + inc - sum;
+  for (int i = i0; i < i1; ++i) {
+    const int nb = seq_of(i).nb;
+    if (nb == 0) continue;
+    order[rank] = i;
+    place[rank] = place_at;
+    const int cost = aligned ? div_near(nb - 1, share) + 1 : nb + kQuantUnitCost;
+    const int next = place_at + cost * HR;
+    if (x0 < x1 && x0 >= place_at && x0 < next) {
+      const int k = div_near(x0 - place_at, cost), in = x0 - place_at - k * cost;
+      // (not a first unit whose blocks lie before the share)
+      flag[0] = rank * HR + k + (!aligned && in >= nb ? 1 : 0);
+    }
+    if (x0 < x1 && x1 - 1 >= place_at && x1 - 1 < next) {
+      const int k = div_near(x1 - 1 - place_at, cost), in = x1 - 1 - place_at - k * cost;
+      flag[1] = rank * HR + k;
+      flag[2] = !aligned && in + 1 < nb;  // it goes on behind the share
+    }
+    place_at = next;
+    ++rank;
+  }
+  __syncthreads();
+  if (p.whole) {
+    unit0 = (int)((int64_t)U * blockIdx.x / G);
+    n_pieces = (int)((int64_t)U * (blockIdx.x + 1) / G) - unit0;
+  } else {
     unit0 = flag[0];
     n_pieces = flag[1] - unit0 + 1;
+    // a unit that goes on behind the share comes first, so that its part is out early
+    tail = n_pieces > 1 && flag[2];
   }
 
   using Piece = QuantPiece;
-  // A unit that goes on behind the share comes first, so that its part is out early.
-  bool tail = false;
   auto piece_at = [&](int k) -> Piece {
     const int u = unit0 + (tail ? (k == 0 ? n_pieces - 1 : k - 1) : k);
     Piece q;
-    q.i = p.by_units.div(u);
-    const int hr = u - q.i * HR;
-    q.h = p.rg == 1 ? hr : (int)p.by_groups.div(hr);
+    const int j = p.by_units.div(u), hr = u - j * HR, i = order[j];
+    q.s = s_first + i;
+    q.h = p.by_groups.div(hr);
     q.g = hr - q.h * p.rg;
-    q.r = seq_of(q.i);
+    q.r = seq_of(i);
+    const int nb = q.r.nb;
     q.b0 = 0;
-    q.b1 = q.r.nb;
+    q.b1 = nb;
     q.part = 0;
     q.parts = 1;
     q.first_cta = blockIdx.x;
-    if (!p.whole) {
-      const int a = place[q.i] + hr * (q.r.nb + kQuantUnitCost);
+    if (aligned) {
+      q.parts = div_near(nb - 1, share) + 1;
+      q.first_cta = place[j] + hr * q.parts;
+      q.part = (int)blockIdx.x - q.first_cta;
+      // (parts of share blocks; what the last one lacks is shared by all)
+      const int fewer = div_near(q.parts * share - nb, q.parts), rest = q.parts * share - nb - fewer * q.parts;
+      q.b0 = q.part * (share - fewer) - min(q.part, rest);
+      q.b1 = q.b0 + share - fewer - (q.part < rest ? 1 : 0);
+    } else if (!p.whole) {
+      const int a = place[j] + hr * (nb + kQuantUnitCost);
       if (x0 > a) q.b0 = x0 - a;
-      if (x1 - a < q.r.nb) q.b1 = x1 - a;
-      if (q.b1 - q.b0 < q.r.nb) {
+      if (x1 - a < nb) q.b1 = x1 - a;
+      if (q.b1 - q.b0 < nb) {
         q.first_cta = div_near(a, share);
         q.part = (int)blockIdx.x - q.first_cta;
-        q.parts = div_near(a + q.r.nb - 1, share) - q.first_cta + 1;
+        q.parts = div_near(a + nb - 1, share) - q.first_cta + 1;
       }
     }
     return q;
   };
-  if (!p.whole && n_pieces > 1) {
-    const Piece q = piece_at(n_pieces - 1);
-    tail = q.b1 < q.r.nb;
-  }
+  for (int k = tid; k < min(n_pieces, kPieces - 1); k += NTHR) pieces[k] = piece_at(k);
+  __syncthreads();
 
   // ---- the copies: a cursor over the steps of this warp ----------------------
   // Step st of a piece is blocks b0 + st TB ..; a warp takes steps first, first +
@@ -300,18 +372,17 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     c.k = k;
     c.base = c.mine = 0;
     if (k >= n_pieces) return;
-    const Piece q = piece_at(k);
+    const Piece &q = pieces[k & (kPieces - 1)];
     const int steps = (q.b1 - q.b0 + TB - 1) / TB;
-    c.first = (warp + k) % NW;
+    c.first = (warp + k) & (NW - 1);
     c.mine = (steps + NW - 1 - c.first) / NW;
     c.b0 = q.b0;
     c.b1 = q.b1;
     c.sk_nb = q.r.sk_nb;
     c.sk_gap = q.r.sk_gap;
-    c.s = s_first + q.i;
+    c.s = q.s;
     c.h = q.h;
   };
-  // (16-key blocks of a page)
   auto fetch_ids = [&](const QuantRun &c) -> int {
     if (c.k >= n_pieces) return 0;
     const int b = c.b0 + (c.first + (c.base + lane / TB) * NW) * TB + lane % TB;
@@ -319,97 +390,97 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     const int sb = b >= c.sk_nb ? b + c.sk_gap : b;
     return __ldg(p.block_table + (int64_t)c.s * p.bt_stride + p.by_page.div(sb));
   };
-  int which = 0;                      // the present run; the next one lies beside it
-  int at = 0, end = 0, next_blk = 0;  // steps of it, and the next one's first block
-  int ids = 0, ids_ahead = 0;
-  bool look = true;                   // the next run is still to be looked up
-  auto put = [&](int i, const QuantRun &c) {
-    __syncwarp();
-    if (lane == 0) runs[i] = c;
-    __syncwarp();
-  };
-  auto begin_run = [&](const QuantRun &c) {
-    at = 0;
-    end = c.k < n_pieces ? min(SPC, c.mine - c.base) : 0;
-    next_blk = c.b0 + (c.first + c.base * NW) * TB;
-  };
-  // the run after the present one: of its piece, or of the next one that has a step for this warp
-  auto look_ahead = [&]() {
-    QuantRun c = runs[which];
+  int which = 0;        // the present run; the next one lies beside it
+  int at = 0, end = 0;  // steps of it
+  int ids_ahead = 0;
+  bool look = false;    // the next run is still to be looked up
+  // of the present run, a block a lane: where its K, V and their scales are (K at -1: there is none)
+  int64_t k_at = -1, v_at = -1, ks_at = 0, vs_at = 0;
+  // the run after c: of its piece, or of the next one that has a step for this warp (a
+  // piece has a block, so one of NW pieces has: kPieces cover all that a warp looks ahead)
+  auto look_ahead = [&](QuantRun c) {
     c.base += SPC;
     while (c.k < n_pieces && c.base >= c.mine) enter(c, c.k + 1);
     ids_ahead = fetch_ids(c);
-    put(which ^ 1, c);
+    __syncwarp();
+    if (lane == 0) runs[which ^ 1] = c;
+    __syncwarp();
+  };
+  auto next_run = [&]() {
+    which ^= 1;
+    const QuantRun &c = runs[which];
+    at = 0;
+    end = c.k < n_pieces ? min(SPC, c.mine - c.base) : 0;
+    look = true;
+    const int b = c.b0 + (c.first + (c.base + lane / TB) * NW) * TB + lane % TB;
+    k_at = v_at = -1;
+    if (lane / TB < end && b < c.b1) {
+      int page = ids_ahead;
+      if ((unsigned)page >= (unsigned)p.num_pages) {
+        atomicOr(p.status, PD_DEV_BAD_PAGE);  // report, read page 0
+        page = 0;
+      }
+      const int sb = b >= c.sk_nb ? b + c.sk_gap : b;
+      const int sub = sb - (int)p.by_page.div(sb) * p.bpp;
+      k_at = page * p.k.page + c.h * p.k.head + (sub * kBlockKeys) * p.k.tok;
+      v_at = page * p.v.page + c.h * p.v.head + (sub * kBlockKeys) * p.v.tok;
+      ks_at = page * p.k.s_page + sub * p.k.s_blk + c.h * p.k.s_head;
+      vs_at = page * p.v.s_page + sub * p.v.s_blk + c.h * p.v.s_head;
+    }
   };
   {
-    QuantRun c;
-    enter(c, 0);
-    while (c.k < n_pieces && c.mine == 0) enter(c, c.k + 1);
-    ids = fetch_ids(c);
-    put(0, c);
-    begin_run(c);
+    QuantRun c{};
+    c.k = n_pieces > 0 ? -1 : 0;
+    look_ahead(c);
+    next_run();
   }
   const int c_row = lane / CPR, c_ch = lane % CPR;  // (D = 512: row 0, chunk = lane)
-  const int64_t k_off = c_row * p.k.tok + c_ch * 16, v_off = c_row * p.v.tok + c_ch * 16;
   auto place_of = [&](int row, int ch) -> uint32_t {
     return D >= 128 ? row * D + ((ch ^ (row & 7)) << 4) : row * D + ((ch ^ ((row >> 1) & 3)) << 4);
   };
-  int in_slot = 0;  // the slot that the next copies go to
+  const unsigned char *k_lane = p.k.codes + c_row * p.k.tok + c_ch * 16;
+  const unsigned char *v_lane = p.v.codes + c_row * p.v.tok + c_ch * 16;
+  int in_slot = 0;     // the slot that the next copies go to
   const uint32_t ring_at = smem_u32(ring);
   // the next slot's copies: the present step's K and scales, or its V and on to the next step
   auto issue = [&](bool is_v) {
     if (at < end) {
-      const QuantRun &c = runs[which];
-      const QuantPool &t = is_v ? p.v : p.k;
-      const int b1 = c.b1, sk_nb = c.sk_nb, sk_gap = c.sk_gap, h = c.h;
+      const int64_t tok = is_v ? p.v.tok : p.k.tok;
+      const uint32_t slot = ring_at + in_slot * SLOT;
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        int page = __shfl_sync(0xffffffffu, ids, at * TB + b);
-        const int i = next_blk + b;
-        if (i < b1) {
-          const int sb = i >= sk_nb ? i + sk_gap : i;
-          const int sub = sb - (int)p.by_page.div(sb) * p.bpp;
-          if ((unsigned)page >= (unsigned)p.num_pages) {
-            if (lane == 0) atomicOr(p.status, PD_DEV_BAD_PAGE);  // report, read page 0
-            page = 0;
-          }
-          const uint32_t dst = ring_at + in_slot * SLOT + b * BLOCK;
-          const unsigned char *src = t.codes + page * t.page + (int64_t)(sub * kBlockKeys) * t.tok + h * t.head +
-                                     (is_v ? v_off : k_off);
-          if (t.tok == D) {
+        const int64_t from = __shfl_sync(0xffffffffu, is_v ? v_at : k_at, at * TB + b);
+        if (from >= 0) {
+          const unsigned char *src = (is_v ? v_lane : k_lane) + from;
+          if (tok == D) {
             // (rows one after the other: offsets are constants)
 #pragma unroll
-            for (int j = 0; j < COPIES; ++j) copy_async16(dst + place_of(c_row + j * RPI, c_ch), src + j * (RPI * D));
+            for (int j = 0; j < COPIES; ++j)
+              copy_async16(slot + b * BLOCK + place_of(c_row + j * RPI, c_ch), src + j * (RPI * D));
           } else {
 #pragma unroll
             for (int j = 0; j < COPIES; ++j)
-              copy_async16(dst + place_of(c_row + j * RPI, c_ch), src + (int64_t)(j * RPI) * t.tok);
-          }
-          if (!is_v && lane < 2) {
-            const QuantPool &u = lane ? p.v : p.k;
-            copy_async4(ring_at + in_slot * SLOT + TB * BLOCK + b * 8 + lane * 4,
-                        u.scale + page * u.s_page + sub * u.s_blk + h * u.s_head);
+              copy_async16(slot + b * BLOCK + place_of(c_row + j * RPI, c_ch), src + (int64_t)(j * RPI) * tok);
           }
         }
       }
-      if (++in_slot == NS) in_slot = 0;
-      if (is_v) {
-        next_blk += NW * TB;
+      if (!is_v) {
+        // a lane a scale: K's and V's of a block side by side
+        const int from = at * TB + (lane >> 1) % TB;
+        const int64_t there = __shfl_sync(0xffffffffu, k_at, from);
+        const int64_t ks = __shfl_sync(0xffffffffu, ks_at, from), vs = __shfl_sync(0xffffffffu, vs_at, from);
+        if (lane < 2 * TB && there >= 0)
+          copy_async4(slot + TB * BLOCK + lane * 4, lane & 1 ? p.v.scale + vs : p.k.scale + ks);
+      } else {
         ++at;
         if (look) {
-          look_ahead();
+          look_ahead(runs[which]);
           look = false;
         }
-        if (at == end) {
-          which ^= 1;
-          ids = ids_ahead;
-          begin_run(runs[which]);
-          look = true;
-        }
+        if (at == end) next_run();
       }
-    } else if (++in_slot == NS) {
-      in_slot = 0;
     }
+    if (++in_slot == NS) in_slot = 0;
     copy_commit();
   };
 
@@ -474,23 +545,12 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
       }
     }
   };
-  if (n_pieces > 0) {
-    const Piece q = piece_at(0);
-    if (tid == 0) pieces[0] = q;
-    if (tid == 32 && n_pieces > 1) pieces[1] = piece_at(1);
-    fetch_q(q);
-#pragma unroll 1
-    for (int i = 0; i < NS - 1; ++i) issue(i & 1);
-    put_q(q, 0);
-  }
-  __syncthreads();
-
   const int g8 = lane >> 2, t4 = lane & 3;
   const int a_row = lane & 15, a_hi = lane >> 4;  // the rows and chunk of ldmatrix's addresses
   auto sees = [&](int key, int lo, int hi) { return key < hi && (key >= lo || key < p.sinks); };
   int out_slot = 0;   // the slot of the next step's K
   int n_cut = 0;      // cut units of this share whose part is out
-  int cut_k0 = 0, cut_k1 = 0, cut_old0 = 0, cut_old1 = 0;
+  int cut_old0 = 0, cut_old1 = 0;
 
   // the rows of a unit in q and out, and the scratch slot of a part of it
   auto out_row = [&](const Piece &q, int rr) -> T * {
@@ -502,12 +562,17 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     return part == 0 ? 2 * c + 1 : 2 * c;
   };
 
+  // (from -1 on: the first copies and the first Q)
 #pragma unroll 1
-  for (int k = 0; k < n_pieces; ++k) {
+  for (int k = n_pieces > 0 ? -1 : 0; k < n_pieces; ++k) {
     const int buf = k & 1;
     const Piece &q = pieces[k & (kPieces - 1)];
     const uint2 *qf = qfrag + buf * CPR * NT * 32 + lane;
-    const int first = (warp + k) % NW, mine = ((q.b1 - q.b0 + TB - 1) / TB + NW - 1 - first) / NW;
+    const int first = (warp + k) & (NW - 1);
+    const int mine = k < 0 ? 0 : ((q.b1 - q.b0 + TB - 1) / TB + NW - 1 - first) / NW;
+    const bool more = k + 1 < n_pieces;
+    constexpr bool EARLY = NT * QV <= 2;  // the next Q is fetched while this piece runs
+    if (more && (EARLY || k < 0)) fetch_q(pieces[(k + 1) & (kPieces - 1)]);
     float acc[CPR][NT][4];
 #pragma unroll
     for (int c = 0; c < CPR; ++c)
@@ -534,15 +599,22 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
       }
     }
     bool settled = false;  // every row has its reference
+    uint32_t pb[TB][NT][2];
+    if (k < 0) {
+#pragma unroll 1
+      for (int i = 0; i < NS - 1; ++i) issue(i & 1);
+    }
 #pragma unroll 1
     for (int st = 0; st < mine; ++st) {
       copy_wait<NS - 2>();
       __syncwarp();
       issue((NS - 1) & 1);
       const uint32_t kb = ring_at + out_slot * SLOT;
+      const int blk = q.b0 + (first + st * NW) * TB;
+      // (else some row does not see them whole, or the piece does not have them)
+      const bool whole = blk + TB <= q.b1 && ((blk >= q.r.all_lo && blk + TB <= q.r.all_hi) || blk + TB <= q.r.all_sk);
       const float2 *scales = reinterpret_cast<const float2 *>(ring + out_slot * SLOT + TB * BLOCK);
       if (++out_slot == NS) out_slot = 0;
-      const int blk = q.b0 + (first + st * NW) * TB;
 
       // S^T = K Q^T (in two sums where few products are independent)
       constexpr bool TWO = TB * NT <= 2;
@@ -612,8 +684,6 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
           sc[b][n][3] = fmaf(sc[b][n][3], f1, g1);
         }
       }
-      // blocks that some row does not see whole, or that the piece does not have
-      const bool whole = blk + TB <= q.b1 && ((blk >= q.r.all_lo && blk + TB <= q.r.all_hi) || blk + TB <= q.r.all_sk);
       if (!whole) {
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
@@ -677,7 +747,6 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
           }
       }
       // P
-      uint32_t pb[TB][NT][2];
 #pragma unroll
       for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -690,11 +759,11 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
           pb[b][n][1] = movmatrix_trans(pack2(p2, p3, std::integral_constant<bool, false>{}));
         }
 
-      // O^T += V^T P^T
       copy_wait<NS - 2>();
       __syncwarp();
       issue(NS & 1);
       const uint32_t vb = ring_at + out_slot * SLOT;
+      // O^T += V^T P^T
       if (!whole) {
         // V of keys that no row sees (stale or NaN slots), or that are not there: zeros
 #pragma unroll 1
@@ -730,8 +799,12 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     // ---- the piece's end: the warps' sums added, rows stored or published ----
     // A warp's sums go to its ring's free slot (the one that the next copies are
     // for), DC columns at a time.
-    const bool more = k + 1 < n_pieces;
-    if (more) fetch_q(pieces[(k + 1) & (kPieces - 1)]);
+    if (more && !EARLY && k >= 0) fetch_q(pieces[(k + 1) & (kPieces - 1)]);
+    if (k < 0) {
+      put_q(pieces[0], 0);
+      __syncthreads();
+      continue;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -763,45 +836,44 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
           *reinterpret_cast<float2 *>(mine_at + (r0 + 1) * DC + d) = make_float2(a[1], a[3]);
         }
       __syncthreads();
-      if (ps == 0) {
-        // a row's weights of the warps' sums: eight lanes
-        if (tid < NR * NW) {
-          const float2 t = ml_of[tid];
-          float M = t.x;
-#pragma unroll
-          for (int o = 1; o < NW; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          const float f = exp2_or_zero(t.x, M == -INFINITY ? 0.f : M);
-          float ls = f * t.y;
-#pragma unroll
-          for (int o = 1; o < NW; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-          weight[tid] = f;
-          if (tid % NW == 0) total[tid / NW] = make_float2(M, ls);
-        }
-        __syncthreads();
-      }
 #pragma unroll 1
       for (int it = tid; it < NR * (DC / 4); it += NTHR) {
         const int rr = it / (DC / 4), d4 = it - rr * (DC / 4);
         if (!row_live(q, rr)) continue;
-        const float2 t = total[rr];
+        // the row's (m, l) of the warps, their weights and their sum
+        float2 t[NW];
+#pragma unroll
+        for (int w = 0; w < NW; w += 2) {
+          const float4 x = *reinterpret_cast<const float4 *>(ml_of + rr * NW + w);
+          t[w] = make_float2(x.x, x.y);
+          t[w + 1] = make_float2(x.z, x.w);
+        }
+        float M = t[0].x, ls = 0.f;
+#pragma unroll
+        for (int w = 1; w < NW; ++w) M = fmaxf(M, t[w].x);
+        const float mm = M == -INFINITY ? 0.f : M;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
-          add_scaled(o, weight[rr * NW + w],
+        for (int w = 0; w < NW; ++w) {
+          const float f = exp2_or_zero(t[w].x, mm);
+          ls = fmaf(f, t[w].y, ls);
+          add_scaled(o, f,
                      *reinterpret_cast<const float4 *>(smem + free_slot[w] +
                                                        4 * (rr * DC + ((4 * d4) ^ (((rr >> 1 & 3) << 3) & SWIZZLE)))));
+        }
         const int d = ps * DC + 4 * d4;
         if (!cut) {
-          store_four<BF16>(out_row(q, rr) + d, o, t.y > 0.f ? 1.f / t.y : 0.f);
+          store_four<BF16>(out_row(q, rr) + d, o, ls > 0.f ? sfu_rcp(ls) : 0.f);
         } else {
           const int64_t to = slot_of(q, q.part) * NR + rr;
           __stcg(reinterpret_cast<float4 *>(p.part_acc + to * D + d), o);
-          if (d == 0) __stcg(reinterpret_cast<float2 *>(p.part_ml + to * 2), t);
+          if (d == 0) __stcg(reinterpret_cast<float2 *>(p.part_ml + to * 2), make_float2(M, ls));
         }
       }
       if (ps == PASSES - 1) {
         if (more) put_q(pieces[(k + 1) & (kPieces - 1)], buf ^ 1);
-        if (tid == NTHR - 1 && k + 2 < n_pieces) pieces[(k + 2) & (kPieces - 1)] = piece_at(k + 2);
+        // (the place of the piece before this one is free)
+        if (tid == NTHR - 1 && k + kPieces - 1 < n_pieces) pieces[(k - 1) & (kPieces - 1)] = piece_at(k + kPieces - 1);
       }
       __syncthreads();
     }
@@ -809,11 +881,10 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
       // every thread's stores, the barrier above, one release by one thread; the
       // count's answer is looked at when the share is done
       if (tid == 0) {
-        const int u = ((s_first + q.i) * p.Hkv + q.h) * p.rg + q.g;
-        const int old = atomic_add_acq_rel_gpu(p.counters + u, 1);
+        const int old = atomic_add_acq_rel_gpu(p.counters + ((q.s * p.Hkv + q.h) * p.rg + q.g), 1);
         if (n_cut == 0) cut_old0 = old; else cut_old1 = old;
       }
-      if (n_cut == 0) cut_k0 = k; else cut_k1 = k;
+      if (tid == 32) cut_piece[n_cut] = q;  // (read behind later barriers)
       ++n_cut;
     }
   }
@@ -821,21 +892,22 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
 
   // ---- cut units whose last part is this CTA's: merged ------------------------
   if (n_cut > 0) {
+    __syncthreads();
     if (tid == 0) {
       for (int c = 0; c < n_cut; ++c) {
-        const Piece q = piece_at(c == 0 ? cut_k0 : cut_k1);
+        const Piece &q = cut_piece[c];
         const int old = c == 0 ? cut_old0 : cut_old1;
         if (old < 0 || old >= q.parts) atomicOr(p.status, PD_DEV_BAD_SCRATCH);  // not zero at the start
-        flag[2 + c] = old == q.parts - 1;
-        if (old == q.parts - 1) atomicExch(p.counters + ((s_first + q.i) * p.Hkv + q.h) * p.rg + q.g, 0);
+        flag[4 + c] = old == q.parts - 1;
+        if (old == q.parts - 1) atomicExch(p.counters + ((q.s * p.Hkv + q.h) * p.rg + q.g), 0);
       }
     }
     __syncthreads();
   }
 #pragma unroll 1
   for (int c = 0; c < n_cut; ++c) {
-    if (!flag[2 + c]) continue;
-    const Piece q = piece_at(c == 0 ? cut_k0 : cut_k1);
+    if (!flag[4 + c]) continue;
+    const Piece &q = cut_piece[c];
     constexpr int CH = 8;  // parts whose loads are in flight
     const int rows = min(p.rows_grp, q.r.ml * p.G - q.g * p.rows_grp), items = rows * (D / 4);
 #pragma unroll 1
@@ -868,22 +940,29 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
           add_scaled(o, f, a[w]);
         }
       }
-      store_four<BF16>(out_row(q, rr) + d, o, ls > 0.f ? 1.f / ls : 0.f);
+      store_four<BF16>(out_row(q, rr) + d, o, ls > 0.f ? sfu_rcp(ls) : 0.f);
     }
   }
 
-  if (p.query_start && blockIdx.y == gridDim.y - 1) {
-    // rows at and past the last request's end (padding of a captured batch)
-    // see no key: zeros
-    const int t0 = starts[S], per_row = p.Hq * (D / 8);
-    const int64_t n = (int64_t)(p.num_tokens - t0) * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * NTHR + tid; i < n; i += (int64_t)gridDim.x * NTHR) {
+  // rows of sequences without a visible key, and those at and past the last request's
+  // end (padding of a captured batch): zeros
+  auto zero_rows = [&](int t0, int t1, int first, int step) {
+    const int per_row = p.Hq * (D / 8);
+    const int64_t n = (int64_t)(t1 - t0) * per_row;
+    for (int64_t i = first; i < n; i += step) {
       const int t = t0 + (int)(i / per_row), rem = (int)(i - (int64_t)(t - t0) * per_row);
       const int hq = rem / (D / 8), c = rem - hq * (D / 8);
       *reinterpret_cast<uint4 *>(obase + (int64_t)t * p.o_s0 + (int64_t)hq * p.o_s1 + c * 8) =
           make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+#pragma unroll 1
+  for (int i = blockIdx.x; i < S; i += G) {
+    const QuantSeq r = seq_of(i);
+    if (r.nb == 0) zero_rows(r.q0, r.q0 + r.ml, tid, NTHR);
   }
+  if (p.query_start && blockIdx.y == gridDim.y - 1)
+    zero_rows(starts[S], p.num_tokens, blockIdx.x * NTHR + tid, G * NTHR);
 }
 
 template <int D, int NT, bool BF16>
