@@ -230,6 +230,8 @@ PD_API int paged_decode_attn_quant(const pd_tensor *q, const pd_tensor *k_cache,
     const int64_t cbytes = (scratch->counter_slots * 4 + 255) / 256 * 256;
     const int64_t parts = 2LL * plan.pub.grid_x * plan.pub.grid_y;
     p.counters = reinterpret_cast<int *>(base);
+    p.unit_counters = (int)std::min<int64_t>(64, scratch->counter_slots / (S * num_kv_heads * p.rg));
+    p.merge_bytes = 160 << 10;
     p.part_acc = reinterpret_cast<float *>(base + cbytes);
     p.part_ml = reinterpret_cast<float *>(base + cbytes + parts * NR * head_size * 4);
   }

@@ -56,7 +56,9 @@ struct QuantAttnParams {
   int align_slack;   // what parts of single units may be longer than equal shares
   FastDiv by_units, by_groups, by_heads, by_page, by_ctas;  // Hkv rg, rg, G, bpp, gridDim.x
   float *part_acc, *part_ml;  // [2 x CTAs][8 NT][D], [..][8 NT][2]
-  int *counters;              // parts published of each unit
+  int *counters;              // [units][unit_counters]: parts published, of a unit and of its groups
+  int unit_counters;
+  int merge_bytes;            // of a unit's parts that one CTA merges at once
   unsigned int *status;
 };
 

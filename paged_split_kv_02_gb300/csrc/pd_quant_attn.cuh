@@ -557,6 +557,19 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     const int pr = q.g * p.rows_grp + rr, t = p.by_heads.div(pr), jq = pr - t * p.G;
     return obase + (int64_t)(q.r.q0 + t) * p.o_s0 + (int64_t)(q.h * p.G + jq) * p.o_s1;
   };
+  // Parts of a unit are merged in groups, and then the groups, where they are many: one
+  // CTA pulls parts at about 80 GB/s, so 152 parts of 16 KiB take it 30 us, in 13
+  // groups two times 2.5.  Each group has a counter beside the unit's.
+  auto group_size = [&](const Piece &q) -> int {
+    if (p.unit_counters < 3 || q.parts * (NR * D / 32) <= p.merge_bytes / 128) return q.parts;
+    int g = 2;
+    while (g * g < q.parts) ++g;
+    return max(g, (q.parts + p.unit_counters - 2) / (p.unit_counters - 1));
+  };
+  auto counter_of = [&](const Piece &q, int group) -> int * {
+    const int64_t unit = (int64_t)((q.s * p.Hkv + q.h) * p.rg + q.g) * p.unit_counters;
+    return p.counters + unit + (group_size(q) < q.parts ? 1 + group : 0);
+  };
   auto slot_of = [&](const Piece &q, int part) -> int64_t {
     const int64_t c = (int64_t)blockIdx.y * gridDim.x + q.first_cta + part;
     return part == 0 ? 2 * c + 1 : 2 * c;
@@ -881,7 +894,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
       // every thread's stores, the barrier above, one release by one thread; the
       // count's answer is looked at when the share is done
       if (tid == 0) {
-        const int old = atomic_add_acq_rel_gpu(p.counters + ((q.s * p.Hkv + q.h) * p.rg + q.g), 1);
+        const int old = atomic_add_acq_rel_gpu(counter_of(q, q.part / group_size(q)), 1);
         if (n_cut == 0) cut_old0 = old; else cut_old1 = old;
       }
       if (tid == 32) cut_piece[n_cut] = q;  // (read behind later barriers)
@@ -891,56 +904,115 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   grid_dependents_launch();
 
   // ---- cut units whose last part is this CTA's: merged ------------------------
-  if (n_cut > 0) {
-    __syncthreads();
-    if (tid == 0) {
-      for (int c = 0; c < n_cut; ++c) {
-        const Piece &q = cut_piece[c];
-        const int old = c == 0 ? cut_old0 : cut_old1;
-        if (old < 0 || old >= q.parts) atomicOr(p.status, PD_DEV_BAD_SCRATCH);  // not zero at the start
-        flag[4 + c] = old == q.parts - 1;
-        if (old == q.parts - 1) atomicExch(p.counters + ((q.s * p.Hkv + q.h) * p.rg + q.g), 0);
+  // n parts from part `from` on, `step` apart: to the output, or back as part `from`.
+  // IT items (a row's 4 columns) of a thread, CH parts of them in flight; `slices`
+  // neighbouring lanes take turns at an item's parts.
+  auto merge = [&](auto it_c, auto ch_c, const Piece &q, int rows, int from, int n, int step, bool last) {
+    constexpr int IT = decltype(it_c)::value, CH = decltype(ch_c)::value;
+    const int items = rows * (D / 4), slices = items * 8 <= NTHR ? 8 : items * 4 <= NTHR ? 4 : items * 2 <= NTHR ? 2 : 1;
+    const int lg = slices == 8 ? 3 : slices >> 1, slice = tid & (slices - 1), stride = NTHR >> lg;
+#pragma unroll 1
+    for (int it0 = tid >> lg; it0 < items; it0 += IT * stride) {
+      float M[IT], ls[IT];
+      float4 o[IT];
+#pragma unroll
+      for (int j = 0; j < IT; ++j) {
+        M[j] = -INFINITY;
+        ls[j] = 0.f;
+        o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      for (int c0 = slice; c0 < n; c0 += CH * slices) {
+        float2 t[IT][CH];
+        float4 a[IT][CH];
+#pragma unroll
+        for (int j = 0; j < IT; ++j)
+#pragma unroll
+          for (int w = 0; w < CH; ++w) {
+            const int it = it0 + j * stride, rr = it / (D / 4), d = 4 * (it - rr * (D / 4)), c = c0 + w * slices;
+            t[j][w] = make_float2(-INFINITY, 0.f);
+            a[j][w] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (it < items && c < n) {
+              const int64_t at = slot_of(q, from + c * step) * NR + rr;
+              t[j][w] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at * 2));
+              a[j][w] = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + at * D + d));
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < IT; ++j) {
+          float mn = M[j];
+#pragma unroll
+          for (int w = 0; w < CH; ++w) mn = fmaxf(mn, t[j][w].x);
+          const float mm = mn == -INFINITY ? 0.f : mn, al = exp2_or_zero(M[j], mm);
+          M[j] = mn;
+          ls[j] *= al;
+          o[j] = make_float4(o[j].x * al, o[j].y * al, o[j].z * al, o[j].w * al);
+#pragma unroll
+          for (int w = 0; w < CH; ++w) {
+            const float f = exp2_or_zero(t[j][w].x, mm);
+            ls[j] = fmaf(f, t[j][w].y, ls[j]);
+            add_scaled(o[j], f, a[j][w]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < IT; ++j) {
+        for (int k = 1; k < slices; k *= 2) {
+          // (items beyond the last one are so for all slices)
+          const float Mo = __shfl_xor_sync(0xffffffffu, M[j], k), lo = __shfl_xor_sync(0xffffffffu, ls[j], k);
+          const float4 b = make_float4(__shfl_xor_sync(0xffffffffu, o[j].x, k), __shfl_xor_sync(0xffffffffu, o[j].y, k),
+                                       __shfl_xor_sync(0xffffffffu, o[j].z, k), __shfl_xor_sync(0xffffffffu, o[j].w, k));
+          const float mn = fmaxf(M[j], Mo), mm = mn == -INFINITY ? 0.f : mn;
+          // (both lanes alike: the lower slice's first)
+          const bool low = !(slice & k);
+          const float f0 = exp2_or_zero(low ? M[j] : Mo, mm), f1 = exp2_or_zero(low ? Mo : M[j], mm);
+          const float4 x = low ? o[j] : b, y = low ? b : o[j];
+          ls[j] = fmaf(f1, low ? lo : ls[j], f0 * (low ? ls[j] : lo));
+          o[j] = make_float4(f0 * x.x, f0 * x.y, f0 * x.z, f0 * x.w);
+          add_scaled(o[j], f1, y);
+          M[j] = mn;
+        }
+        const int it = it0 + j * stride, rr = it / (D / 4), d = 4 * (it - rr * (D / 4));
+        if (it >= items || slice != 0) continue;
+        if (last) {
+          store_four<BF16>(out_row(q, rr) + d, o[j], ls[j] > 0.f ? sfu_rcp(ls[j]) : 0.f);
+        } else {
+          __stcg(reinterpret_cast<float4 *>(p.part_acc + (slot_of(q, from) * NR + rr) * D + d), o[j]);
+          if (d == 0) ml_of[rr] = make_float2(M[j], ls[j]);  // (others still read the part's)
+        }
       }
     }
-    __syncthreads();
-  }
+  };
+  if (n_cut > 0) __syncthreads();
 #pragma unroll 1
   for (int c = 0; c < n_cut; ++c) {
-    if (!flag[4 + c]) continue;
-    const Piece &q = cut_piece[c];
-    constexpr int CH = 8;  // parts whose loads are in flight
-    const int rows = min(p.rows_grp, q.r.ml * p.G - q.g * p.rows_grp), items = rows * (D / 4);
+    const int g = group_size(cut_piece[c]), parts = cut_piece[c].parts, group = cut_piece[c].part / g;
+    const bool grouped = g < parts;
+    int old = c == 0 ? cut_old0 : cut_old1;
 #pragma unroll 1
-    for (int it = tid; it < items; it += NTHR) {
-      const int rr = it / (D / 4), d = 4 * (it - rr * (D / 4));
-      float M = -INFINITY, ls = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c0 = 0; c0 < q.parts; c0 += CH) {
-        float2 t[CH];
-        float4 a[CH];
-#pragma unroll
-        for (int w = 0; w < CH; ++w) {
-          const int64_t from = slot_of(q, min(c0 + w, q.parts - 1)) * NR + rr;
-          t[w] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + from * 2));
-          a[w] = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + from * D + d));
-          if (c0 + w >= q.parts) t[w] = make_float2(-INFINITY, 0.f);
-        }
-        float mn = M;
-#pragma unroll
-        for (int w = 0; w < CH; ++w) mn = fmaxf(mn, t[w].x);
-        const float mm = mn == -INFINITY ? 0.f : mn;
-        const float al = exp2_or_zero(M, mm);
-        ls *= al;
-        o.x *= al; o.y *= al; o.z *= al; o.w *= al;
-        M = mn;
-#pragma unroll
-        for (int w = 0; w < CH; ++w) {
-          const float f = exp2_or_zero(t[w].x, mm);
-          ls = fmaf(f, t[w].y, ls);
-          add_scaled(o, f, a[w]);
-        }
+    for (int level = grouped ? 0 : 1; level < 2; ++level) {
+      const Piece &q = cut_piece[c];
+      const int n = !grouped ? parts : level == 0 ? min(g, parts - group * g) : (parts + g - 1) / g;
+      __syncthreads();
+      if (tid == 0) {
+        if (old < 0 || old >= n) atomicOr(p.status, PD_DEV_BAD_SCRATCH);  // not zero at the start
+        flag[4] = old == n - 1;
+        if (old == n - 1) atomicExch(level == 0 ? counter_of(q, group) : counter_of(q, -1), 0);
       }
-      store_four<BF16>(out_row(q, rr) + d, o, ls > 0.f ? sfu_rcp(ls) : 0.f);
+      __syncthreads();
+      if (!flag[4]) break;
+      const int rows = min(p.rows_grp, q.r.ml * p.G - q.g * p.rows_grp);
+      const int from = level == 0 ? group * g : 0, step = grouped && level == 1 ? g : 1;
+      if (n > 4)
+        merge(std::integral_constant<int, 1>{}, std::integral_constant<int, 12>{}, q, rows, from, n, step, level == 1);
+      else
+        merge(std::integral_constant<int, 3>{}, std::integral_constant<int, 4>{}, q, rows, from, n, step, level == 1);
+      if (level == 0) {
+        __syncthreads();
+        if (tid < rows)
+          __stcg(reinterpret_cast<float2 *>(p.part_ml + (slot_of(q, from) * NR + tid) * 2), ml_of[tid]);
+        __syncthreads();
+        if (tid == 0) old = atomic_add_acq_rel_gpu(counter_of(q, -1), 1);
+      }
     }
   }
 

@@ -105,10 +105,12 @@ def test_any_scratch(splits, D, heads, M):
     _checked(_case([2100, 13, 800], D=D, heads=heads, M=M), splits=splits)
 
 
-@pytest.mark.parametrize("D", [128, 256])
-def test_one_long_context(D):
-    case = _case([20000], D=D, heads=(8, 2), M=2)
-    _checked(case, splits=256, rows=sample_rows(case, 12))
+@pytest.mark.parametrize("D,heads,M", [(128, (8, 2), 2), (256, (8, 2), 2), (512, (8, 1), 1), (64, (4, 1), 8), (128, (32, 1), 1)])
+@pytest.mark.parametrize("splits", [20, 256])
+def test_one_long_context(D, heads, M, splits):
+    # (up to 152 parts of a unit, merged in groups)
+    case = _case([20000], D=D, heads=heads, M=M)
+    _checked(case, splits=splits, rows=sample_rows(case, 12))
 
 
 def test_scales_of_any_size():
