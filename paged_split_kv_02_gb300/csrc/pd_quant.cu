@@ -36,7 +36,7 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
                                            cdiv(sinks, kBlockKeys));
   // runs of sequences whose line's places fit an int
   const int64_t per_seq = (nb_max + kQuantUnitCost) * HR;
-  const int64_t fit = ((int64_t)INT32_MAX - (1 << 20)) / per_seq;
+  const int64_t fit = (int64_t)(INT32_MAX / 4) / per_seq;
   const int seqs = (int)std::min<int64_t>({(int64_t)S, (int64_t)kQuantSeqs, std::max<int64_t>(fit, 1)});
   const int gy = (int)cdiv(S, seqs);
   if (gy > 65535) return PD_EINVAL;

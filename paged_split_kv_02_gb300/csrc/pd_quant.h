@@ -65,7 +65,7 @@ struct QuantAttnParams {
 // What a unit counts in the line of blocks beside its blocks (its Q, its end).
 constexpr int kQuantUnitCost = 12;
 // Sequences of one line at most (their lengths and places lie in shared memory).
-constexpr int kQuantSeqs = 512;
+constexpr int kQuantSeqs = 448;
 constexpr int kQuantWarps = 8;
 #ifndef QTB
 #define QTB (D == 64 ? (NT <= 2 ? 4 : 2) : D == 128 ? 2 : 1)
@@ -87,11 +87,11 @@ constexpr int kQuantPieces = 64;
 constexpr int kQuantRunBytes = 40, kQuantPieceBytes = 76;
 // Dynamic shared memory: the warps' rings, two sets of Q fragments, row scales and
 // row ends, the warps' (m, l) of the rows, the pieces, two runs of each warp, sums
-// and flags, lengths, first rows, order and places.
+// and flags, lengths, first rows, blocks, order and places.
 constexpr int smem_bytes_quant(int D, int NT, int seqs) {
   return 128 + kQuantWarps * quant_slots(D, NT) * quant_slot_bytes(D, NT) + 2 * (NT * 16 * D + 8 * NT * 8) +
          8 * NT * kQuantWarps * 8 + (kQuantPieces + 2) * kQuantPieceBytes + kQuantWarps * 2 * kQuantRunBytes +
-         4 * (3 * kQuantWarps + 8) + 4 * (4 * seqs + 1);
+         4 * (2 * kQuantWarps + 8) + 4 * (5 * seqs + 1);
 }
 
 cudaError_t launch_quant_d64(bool bf16, int nt, const QuantAttnParams &p, const Launch &l, cudaStream_t stream);

@@ -162,13 +162,14 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   QuantPiece *pieces = reinterpret_cast<QuantPiece *>(ml_of + NR * NW);    // [kPieces], by piece % kPieces
   QuantPiece *cut_piece = pieces + kPieces;                                // [2]
   QuantRun *runs = reinterpret_cast<QuantRun *>(cut_piece + 2) + 2 * warp;  // [NW][2]
-  int *sums = reinterpret_cast<int *>(runs - 2 * warp + 2 * NW);           // [2 NW]
-  int *free_slot = sums + 2 * NW;                                              // [NW]
+  int *sums = reinterpret_cast<int *>(runs - 2 * warp + 2 * NW);           // [NW]
+  int *free_slot = sums + NW;                                              // [NW]
   volatile int *flag = free_slot + NW;                                     // [8]
   int *lens = free_slot + NW + 8;                                          // [seqs]
   int *starts = lens + p.seqs_y;                                           // [seqs + 1]
-  // of the sequences with a visible key, in order: which, and their places on the line
-  int *order = starts + p.seqs_y + 1;                                      // [seqs]
+  int *blocks = starts + p.seqs_y + 1;                                     // [seqs] with visible keys
+  // of the sequences that have some, in order: which, and their places on the line
+  int *order = blocks + p.seqs_y;                                          // [seqs]
   int *place = order + p.seqs_y;                                           // [seqs]
 
   const int s_first = blockIdx.y * p.seqs_y, S = min(p.seqs_y, p.num_seqs - s_first);
@@ -179,51 +180,55 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   // ---- the lengths, clamped and reported; their places on the line -----------
   // (a thread has a run of sequences)
   const int per = (S + NTHR - 1) / NTHR, i0 = min(tid * per, S), i1 = min(i0 + per, S);
-  int sum = 0, full = 0;  // its places, and its sequences with a visible key
+  const int G = gridDim.x;
+  int sum = 0, full = 0;  // its blocks, and its sequences that have some
   {
     const int cap = p.bt_width * p.P;
     unsigned int bad = 0;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      const int L = __ldg(p.seq_lens + s_first + i);
-      int q0 = (s_first + i) * p.M, ml = p.M;
+      int L = __ldg(p.seq_lens + s_first + i), ml = p.M;
       if (p.query_start) {
         const int a = __ldg(p.query_start + s_first + i), b = __ldg(p.query_start + s_first + i + 1);
-        q0 = min(max(a, 0), p.num_tokens);
-        ml = min(max(min(max(b, 0), p.num_tokens) - q0, 0), p.M);
+        const int q0 = min(max(a, 0), p.num_tokens), q1 = min(max(b, 0), p.num_tokens);
+        ml = min(max(q1 - q0, 0), p.M);
         starts[i] = q0;
-        if (i == S - 1) starts[S] = min(max(b, 0), p.num_tokens);
+        starts[i + 1] = q1;  // (what the next one writes there too)
         if (a < 0 || b > p.num_tokens || b < a || b - a > p.M) bad |= PD_DEV_BAD_QSTART;
       }
       if (L > cap) bad |= PD_DEV_BAD_SEQLEN;
-      lens[i] = min(max(L, 0), cap);
-      const int nb = quant_seq(lens[i], q0, ml, p.window, p.sinks).nb;
-      if (nb > 0) {
-        sum += (nb + kQuantUnitCost) * HR;
-        ++full;
-      }
+      L = min(max(L, 0), cap);
+      const int nb = quant_seq(L, 0, ml, p.window, p.sinks).nb;
+      lens[i] = L;
+      blocks[i] = nb;
+      sum += nb;
+      full += nb > 0;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
   }
-  // an inclusive sum over the CTA's threads (of values that a scan needs) and a total
-  auto scan = [&](int v) -> int {
+  // sums over the CTA's threads: inclusive, and of all
+  auto scan = [&](int v, int *all) -> int {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += y;
     }
+    __syncthreads();
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if (i == warp) v += total;
+      total += sums[i];
+    }
+    *all = total;
     return v;
   };
-  int inc = scan(sum);
-  const int inc_full = scan(full);
-  if (lane == 31) {
-    sums[warp] = inc;
-    sums[NW + warp] = inc_full;
-  }
   if (tid == 0) {
     flag[0] = 1;
     flag[1] = flag[2] = 0;
   }
-  __syncthreads();
   auto seq_of = [&](int i) -> QuantSeq {
     int q0 = (s_first + i) * p.M, ml = p.M;
     if (p.query_start) {
@@ -234,83 +239,49 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   };
 
   // ---- this CTA's share -------------------------------------------------------
-  // whole: a unit to a CTA (no scratch for parts).  aligned: a unit is cut into parts
-  // of its own, one to a CTA, where units are few and that costs little: no CTA then
-  // ends two units.  Else a length of the line, from any place of a unit.
-  int unit0 = 0, n_pieces = 0, x0 = 0, x1 = 0, share = 1;
-  bool tail = false, aligned = false;
-  const int G = gridDim.x;
-  int base = 0, W = 0, rank = inc_full - full, U = 0;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    if (i < warp) {
-      base += sums[i];
-      rank += sums[NW + i];
-    }
-    W += sums[i];
-    U += sums[NW + i];
+  // A length of the line, from any place of a unit to any of another (a unit counts
+  // kQuantUnitCost beside its blocks); or, where units are few and it costs little, of a
+  // line on which every unit has a whole number of shares: no CTA then ends two units.
+  // (whole: a CTA has a unit, there being no scratch for parts.)
+  int U, N, unit0, n_pieces;
+  int rank = scan(full, &U) - full;
+  scan(sum, &N);
+  U *= HR;  // units with blocks, and the blocks
+  N *= HR;
+  int share = p.by_ctas.div(N + U * kQuantUnitCost + G - 1), even = 0;
+  if (2 * U <= G && U > 0) {
+    // parts of s blocks take N / s + U CTAs at most; of one sequence, whose units are alike, no more than
+    // G (approximate quotients, rounded up past their error)
+    const int m = S == 1 ? U * div_near(G, U) : G - U;
+    const int s = max(p.min_part, (int)(1.f + 1.00001f * __fdividef((float)N, (float)m)));
+    if (s + kQuantUnitCost <= share + p.align_slack) even = s;
   }
-  U *= HR;  // units with blocks
-  if (!p.whole) {
-    share = max(p.min_share, (int)p.by_ctas.div(W + G - 1));
-    if (U > 0 && 2 * U <= G) {
-      // parts of s blocks take N / s + U CTAs at most; of one sequence, whose units are alike, no more than G
-      // (approximate quotients, rounded up past their error)
-      const float N = (float)(W - U * kQuantUnitCost);
-      const int s = max(p.min_part, (int)(1.f + 1.00001f * (S == 1 ? __fdividef(N, (float)(U * div_near(G, U)))
-                                                        : __fdividef(N, (float)(G - U)))));
-      if (s + kQuantUnitCost <= share + p.align_slack) {
-        aligned = true;
-        share = s;  // (blocks of a part)
-        sum = 0;
-        for (int i = i0; i < i1; ++i) {
-          const int nb = seq_of(i).nb;
-          if (nb > 0) sum += (div_near(nb - 1, s) + 1) * HR;
-        }
-        if (S == 1) {
-          // (thread 0 has it)
-          inc = sum;
-          base = 0;
-          W = __shfl_sync(0xffffffffu, sum, 0);
-          if (warp > 0) W = (div_near(seq_of(0).nb - 1, s) + 1) * HR;
-        } else {
-          __syncthreads();  // (the sums are read)
-          inc = scan(sum);
-          if (lane == 31) sums[warp] = inc;
-          __syncthreads();
-          base = W = 0;
-#pragma unroll
-          for (int i = 0; i < NW; ++i) {
-            if (i < warp) base += sums[i];
-            W += sums[i];
-          }
-        }
-      }
-    }
-    // (aligned: a place is a CTA)
-    x0 = (int)min((int64_t)blockIdx.x * (aligned ? 1 : share), (int64_t)W);
-    x1 = (int)min((int64_t)x0 + (aligned ? 1 : share), (int64_t)W);
-  }
+  share = even > 0 ? even : max(share, p.min_share);
+  auto cost_of = [&](int nb) { return even > 0 ? (div_near(nb - 1, share) + 1) * share : nb + kQuantUnitCost; };
+  sum = 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i)
+    if (blocks[i] > 0) sum += cost_of(blocks[i]) * HR;
+  int W, line_at = scan(sum, &W) - sum;
+  const int x0 = (int)min((int64_t)blockIdx.x * share, (int64_t)W), x1 = (int)min((int64_t)x0 + share, (int64_t)W);
   // the sequences' places, and the units that the share's first and last place are in
-  int place_at = base + inc - sum;
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) {
-    const int nb = seq_of(i).nb;
+    const int nb = blocks[i];
     if (nb == 0) continue;
     order[rank] = i;
-    place[rank] = place_at;
-    const int cost = aligned ? div_near(nb - 1, share) + 1 : nb + kQuantUnitCost;
-    const int next = place_at + cost * HR;
-    if (x0 < x1 && x0 >= place_at && x0 < next) {
-      const int k = div_near(x0 - place_at, cost), in = x0 - place_at - k * cost;
-      // (not a first unit whose blocks lie before the share)
-      flag[0] = rank * HR + k + (!aligned && in >= nb ? 1 : 0);
+    place[rank] = line_at;
+    const int cost = cost_of(nb), next = line_at + cost * HR;
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      const int x = e ? x1 - 1 : x0;
+      if (x0 >= x1 || x < line_at || x >= next) continue;
+      const int k = div_near(x - line_at, cost), in = x - line_at - k * cost;
+      // (not a first unit whose blocks lie before the share; and does the last one go on behind it)
+      flag[e] = rank * HR + k + (!e && in >= nb ? 1 : 0);
+      if (e) flag[2] = in + 1 < nb;
     }
-    if (x0 < x1 && x1 - 1 >= place_at && x1 - 1 < next) {
-      const int k = div_near(x1 - 1 - place_at, cost), in = x1 - 1 - place_at - k * cost;
-      flag[1] = rank * HR + k;
-      flag[2] = !aligned && in + 1 < nb;  // it goes on behind the share
-    }
-    place_at = next;
+    line_at = next;
     ++rank;
   }
   __syncthreads();
@@ -320,9 +291,9 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   } else {
     unit0 = flag[0];
     n_pieces = flag[1] - unit0 + 1;
-    // a unit that goes on behind the share comes first, so that its part is out early
-    tail = n_pieces > 1 && flag[2];
   }
+  // a unit that goes on behind the share comes first, so that its part is out early
+  const bool tail = n_pieces > 1 && flag[2] && !p.whole;
 
   using Piece = QuantPiece;
   auto piece_at = [&](int k) -> Piece {
@@ -339,18 +310,10 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     q.part = 0;
     q.parts = 1;
     q.first_cta = blockIdx.x;
-    if (aligned) {
-      q.parts = div_near(nb - 1, share) + 1;
-      q.first_cta = place[j] + hr * q.parts;
-      q.part = (int)blockIdx.x - q.first_cta;
-      // (parts of share blocks; what the last one lacks is shared by all)
-      const int fewer = div_near(q.parts * share - nb, q.parts), rest = q.parts * share - nb - fewer * q.parts;
-      q.b0 = q.part * (share - fewer) - min(q.part, rest);
-      q.b1 = q.b0 + share - fewer - (q.part < rest ? 1 : 0);
-    } else if (!p.whole) {
-      const int a = place[j] + hr * (nb + kQuantUnitCost);
-      if (x0 > a) q.b0 = x0 - a;
-      if (x1 - a < nb) q.b1 = x1 - a;
+    if (!p.whole) {
+      const int a = place[j] + hr * cost_of(nb);
+      q.b0 = max(x0 - a, 0);
+      q.b1 = min(x1 - a, nb);
       if (q.b1 - q.b0 < nb) {
         q.first_cta = div_near(a, share);
         q.part = (int)blockIdx.x - q.first_cta;
@@ -359,7 +322,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
     }
     return q;
   };
-  for (int k = tid; k < min(n_pieces, kPieces - 1); k += NTHR) pieces[k] = piece_at(k);
+  if (tid < min(n_pieces, kPieces - 1)) pieces[tid] = piece_at(tid);
   __syncthreads();
 
   // ---- the copies: a cursor over the steps of this warp ----------------------
@@ -905,80 +868,67 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
 
   // ---- cut units whose last part is this CTA's: merged ------------------------
   // n parts from part `from` on, `step` apart: to the output, or back as part `from`.
-  // IT items (a row's 4 columns) of a thread, CH parts of them in flight; `slices`
-  // neighbouring lanes take turns at an item's parts.
-  auto merge = [&](auto it_c, auto ch_c, const Piece &q, int rows, int from, int n, int step, bool last) {
-    constexpr int IT = decltype(it_c)::value, CH = decltype(ch_c)::value;
-    const int items = rows * (D / 4), slices = items * 8 <= NTHR ? 8 : items * 4 <= NTHR ? 4 : items * 2 <= NTHR ? 2 : 1;
-    const int lg = slices == 8 ? 3 : slices >> 1, slice = tid & (slices - 1), stride = NTHR >> lg;
+  // Neighbouring lanes take turns at the parts of an item (a row's 4 columns).
+  auto merge = [&](const Piece &q, int rows, int from, int n, int step, bool last) {
+    constexpr int CH = 8;  // parts whose loads are in flight
+    const int items = rows * (D / 4);
+    int lg = 0;
+    while (lg < 3 && (items << lg) * 2 <= NTHR) ++lg;
+    const int slices = 1 << lg, slice = tid & (slices - 1);
 #pragma unroll 1
-    for (int it0 = tid >> lg; it0 < items; it0 += IT * stride) {
-      float M[IT], ls[IT];
-      float4 o[IT];
-#pragma unroll
-      for (int j = 0; j < IT; ++j) {
-        M[j] = -INFINITY;
-        ls[j] = 0.f;
-        o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    for (int it = tid >> lg; it < items; it += NTHR >> lg) {
+      const int rr = it / (D / 4), d = 4 * (it - rr * (D / 4));
+      float M = -INFINITY, ls = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
       for (int c0 = slice; c0 < n; c0 += CH * slices) {
-        float2 t[IT][CH];
-        float4 a[IT][CH];
+        float2 t[CH];
+        float4 a[CH];
 #pragma unroll
-        for (int j = 0; j < IT; ++j)
-#pragma unroll
-          for (int w = 0; w < CH; ++w) {
-            const int it = it0 + j * stride, rr = it / (D / 4), d = 4 * (it - rr * (D / 4)), c = c0 + w * slices;
-            t[j][w] = make_float2(-INFINITY, 0.f);
-            a[j][w] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (it < items && c < n) {
-              const int64_t at = slot_of(q, from + c * step) * NR + rr;
-              t[j][w] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at * 2));
-              a[j][w] = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + at * D + d));
-            }
+        for (int w = 0; w < CH; ++w) {
+          const int c = c0 + w * slices;
+          t[w] = make_float2(-INFINITY, 0.f);
+          a[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < n) {
+            const int64_t at = slot_of(q, from + c * step) * NR + rr;
+            t[w] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at * 2));
+            a[w] = __ldcg(reinterpret_cast<const float4 *>(p.part_acc + at * D + d));
           }
+        }
+        float mn = M;
 #pragma unroll
-        for (int j = 0; j < IT; ++j) {
-          float mn = M[j];
+        for (int w = 0; w < CH; ++w) mn = fmaxf(mn, t[w].x);
+        const float mm = mn == -INFINITY ? 0.f : mn, al = exp2_or_zero(M, mm);
+        M = mn;
+        ls *= al;
+        o = make_float4(o.x * al, o.y * al, o.z * al, o.w * al);
 #pragma unroll
-          for (int w = 0; w < CH; ++w) mn = fmaxf(mn, t[j][w].x);
-          const float mm = mn == -INFINITY ? 0.f : mn, al = exp2_or_zero(M[j], mm);
-          M[j] = mn;
-          ls[j] *= al;
-          o[j] = make_float4(o[j].x * al, o[j].y * al, o[j].z * al, o[j].w * al);
-#pragma unroll
-          for (int w = 0; w < CH; ++w) {
-            const float f = exp2_or_zero(t[j][w].x, mm);
-            ls[j] = fmaf(f, t[j][w].y, ls[j]);
-            add_scaled(o[j], f, a[j][w]);
-          }
+        for (int w = 0; w < CH; ++w) {
+          const float f = exp2_or_zero(t[w].x, mm);
+          ls = fmaf(f, t[w].y, ls);
+          add_scaled(o, f, a[w]);
         }
       }
-#pragma unroll
-      for (int j = 0; j < IT; ++j) {
-        for (int k = 1; k < slices; k *= 2) {
-          // (items beyond the last one are so for all slices)
-          const float Mo = __shfl_xor_sync(0xffffffffu, M[j], k), lo = __shfl_xor_sync(0xffffffffu, ls[j], k);
-          const float4 b = make_float4(__shfl_xor_sync(0xffffffffu, o[j].x, k), __shfl_xor_sync(0xffffffffu, o[j].y, k),
-                                       __shfl_xor_sync(0xffffffffu, o[j].z, k), __shfl_xor_sync(0xffffffffu, o[j].w, k));
-          const float mn = fmaxf(M[j], Mo), mm = mn == -INFINITY ? 0.f : mn;
-          // (both lanes alike: the lower slice's first)
-          const bool low = !(slice & k);
-          const float f0 = exp2_or_zero(low ? M[j] : Mo, mm), f1 = exp2_or_zero(low ? Mo : M[j], mm);
-          const float4 x = low ? o[j] : b, y = low ? b : o[j];
-          ls[j] = fmaf(f1, low ? lo : ls[j], f0 * (low ? ls[j] : lo));
-          o[j] = make_float4(f0 * x.x, f0 * x.y, f0 * x.z, f0 * x.w);
-          add_scaled(o[j], f1, y);
-          M[j] = mn;
-        }
-        const int it = it0 + j * stride, rr = it / (D / 4), d = 4 * (it - rr * (D / 4));
-        if (it >= items || slice != 0) continue;
-        if (last) {
-          store_four<BF16>(out_row(q, rr) + d, o[j], ls[j] > 0.f ? sfu_rcp(ls[j]) : 0.f);
-        } else {
-          __stcg(reinterpret_cast<float4 *>(p.part_acc + (slot_of(q, from) * NR + rr) * D + d), o[j]);
-          if (d == 0) ml_of[rr] = make_float2(M[j], ls[j]);  // (others still read the part's)
-        }
+#pragma unroll 1
+      for (int k = 1; k < slices; k *= 2) {
+        // (a sum of two is the same in either order: both lanes alike)
+        const float Mo = __shfl_xor_sync(0xffffffffu, M, k), mn = fmaxf(M, Mo);
+        const float f = exp2_or_zero(M, mn == -INFINITY ? 0.f : mn);
+        M = mn;
+        ls *= f;
+        ls += __shfl_xor_sync(0xffffffffu, ls, k);
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, k);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, k);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, k);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
+      }
+      if (slice != 0) continue;
+      if (last) {
+        store_four<BF16>(out_row(q, rr) + d, o, ls > 0.f ? sfu_rcp(ls) : 0.f);
+      } else {
+        __stcg(reinterpret_cast<float4 *>(p.part_acc + (slot_of(q, from) * NR + rr) * D + d), o);
+        if (d == 0) ml_of[rr] = make_float2(M, ls);  // (others still read the part's)
       }
     }
   };
@@ -1002,10 +952,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
       if (!flag[4]) break;
       const int rows = min(p.rows_grp, q.r.ml * p.G - q.g * p.rows_grp);
       const int from = level == 0 ? group * g : 0, step = grouped && level == 1 ? g : 1;
-      if (n > 4)
-        merge(std::integral_constant<int, 1>{}, std::integral_constant<int, 12>{}, q, rows, from, n, step, level == 1);
-      else
-        merge(std::integral_constant<int, 3>{}, std::integral_constant<int, 4>{}, q, rows, from, n, step, level == 1);
+      merge(q, rows, from, n, step, level == 1);
       if (level == 0) {
         __syncthreads();
         if (tid < rows)
