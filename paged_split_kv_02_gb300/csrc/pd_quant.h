@@ -53,7 +53,6 @@ struct QuantAttnParams {
   int whole;         // 1: no unit is cut
   int min_share;     // the least share of a CTA
   int min_part;      // the fewest blocks of a part of an aligned unit
-  int align_slack;   // what parts of single units may be longer than equal shares
   FastDiv by_units, by_groups, by_heads, by_page, by_ctas;  // Hkv rg, rg, G, bpp, gridDim.x
   float *part_acc, *part_ml;  // [2 x CTAs][8 NT][D], [..][8 NT][2]
   int *counters;              // [units][unit_counters]: parts published, of a unit and of its groups
@@ -62,8 +61,10 @@ struct QuantAttnParams {
   unsigned int *status;
 };
 
-// What a unit counts in the line of blocks beside its blocks (its Q, its end).
-constexpr int kQuantUnitCost = 12;
+// What a unit counts in the line of blocks beside its blocks: its end, the last
+// round of its steps, its first references take a CTA 4 us (32 requests of 1..4
+// tokens, 32 / 8 heads at D = 128, 12 / 24 / 40 / 64: 76 / 74 / 66 / 69 us).
+constexpr int quant_unit_cost(int D) { return D == 64 ? 80 : D == 128 ? 40 : D == 256 ? 28 : 16; }
 // Sequences of one line at most (their lengths and places lie in shared memory).
 constexpr int kQuantSeqs = 448;
 constexpr int kQuantWarps = 8;

@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   constexpr int NR = 8 * NT;                  // rows of the CTA, padded
   constexpr int PASSES = quant_passes(D, NT), DC = D / PASSES, CPP = CPR / PASSES;
   constexpr int SWIZZLE = DC >= 32 ? 24 : DC - 8;  // of the columns of the warps' sums
+  constexpr int COST = quant_unit_cost(D);
   constexpr int SPC = 32 / TB;                // steps whose page ids a warp holds
   constexpr int NTHR = 32 * NW;
   constexpr int kPieces = kQuantPieces;       // pieces whose place is known at a time
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
 
   // ---- this CTA's share -------------------------------------------------------
   // A length of the line, from any place of a unit to any of another (a unit counts
-  // kQuantUnitCost beside its blocks); or, where units are few and it costs little, of a
+  // COST beside its blocks); or, where units are few and it costs little, of a
   // line on which every unit has a whole number of shares: no CTA then ends two units.
   // (whole: a CTA has a unit, there being no scratch for parts.)
   int U, N, unit0, n_pieces;
@@ -248,16 +249,16 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
   scan(sum, &N);
   U *= HR;  // units with blocks, and the blocks
   N *= HR;
-  int share = p.by_ctas.div(N + U * kQuantUnitCost + G - 1), even = 0;
+  int share = p.by_ctas.div(N + U * COST + G - 1), even = 0;
   if (2 * U <= G && U > 0) {
     // parts of s blocks take N / s + U CTAs at most; of one sequence, whose units are alike, no more than
     // G (approximate quotients, rounded up past their error)
     const int m = S == 1 ? U * div_near(G, U) : G - U;
-    const int s = max(p.min_part, (int)(1.f + 1.00001f * __fdividef((float)N, (float)m)));
-    if (s + kQuantUnitCost <= share + p.align_slack) even = s;
+    const int s = (int)(1.f + 1.00001f * __fdividef((float)N, (float)m));
+    if (s <= share + COST) even = max(s, p.min_part);
   }
   share = even > 0 ? even : max(share, p.min_share);
-  auto cost_of = [&](int nb) { return even > 0 ? (div_near(nb - 1, share) + 1) * share : nb + kQuantUnitCost; };
+  auto cost_of = [&](int nb) { return even > 0 ? (div_near(nb - 1, share) + 1) * share : nb + COST; };
   sum = 0;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i)
