@@ -69,8 +69,8 @@ constexpr int quant_unit_cost(int D) { return D == 64 ? 80 : D == 128 ? 40 : D =
 constexpr int kQuantSeqs = 448;
 constexpr int kQuantWarps = 8;
 #ifndef QTB
-#define QTB (D == 64 ? (NT <= 2 ? 4 : 2) : D == 128 ? 2 : 1)
-#define QNS (D == 512 ? 3 : 6)
+#define QTB (D == 64 ? (NT <= 2 ? 4 : 2) : D <= 256 ? 2 : 1)
+#define QNS (D >= 256 ? 3 : 6)
 #endif
 // 16-key blocks of a warp's step; slots of its ring, each K or V of a step;
 // n-tiles of 8 packed rows with their sums in registers.

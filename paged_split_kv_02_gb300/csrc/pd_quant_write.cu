@@ -12,15 +12,21 @@
 // The rotation rounds each product and the sum (no fused multiply-add), so that a
 // code, which sits on a rounding, does not depend on how a compiler pairs them.
 //
-// Memory-bound: every byte is read or written once but for the rescaled codes.
+// Memory-bound: every byte is read or written once but for the rescaled codes.  A
+// prompt of 16,384 tokens, 32 / 8 heads of 128: 74 us, 5.1 TB/s, 75 % of a copy's rate;
+// k and v alone take 34, their loads and codes 23 of them, the rotation the rest.  64
+// tokens, one a request: 4.1 us, 2.5 of them a launch.
 #include "pd_e4m3.cuh"
 #include "pd_quant.h"
 #include "pd_rope.cuh"
+
+#include <algorithm>
 
 namespace pd {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kCtas = 5;        // of an SM where tokens are many (the prompt above with 4 / 5 / 6: 78 / 74 / 76 us)
 constexpr int kMaxPairs = 256;  // rot_dim / 2 at head size 512
 constexpr int kLeast = -64;     // the exponent of the least scale
 
@@ -48,10 +54,9 @@ __device__ __forceinline__ void turn(float a, float b, float c, float s, float &
 }
 
 // The angles of token t's pairs to cs (cos, then sin), by n threads.
-__device__ __forceinline__ void load_angles(const QuantWriteParams &p, int t, float *cs, int me, int n,
-                                            bool report) {
+__device__ __forceinline__ void load_angles(const QuantWriteParams &p, int t, float *cs, int me, int n) {
   const int half = p.rot >> 1;
-  if (report && me < p.axes) {
+  if (me < p.axes) {
     const int pos = __ldg(p.positions + me * p.pos_stride + t);
     if (pos < 0 || pos >= p.max_pos) atomicOr(p.status, PD_DEV_BAD_POSITION);
   }
@@ -95,7 +100,7 @@ __device__ __forceinline__ void q_tokens(const QuantWriteParams &p, int t0, floa
     }
   };
   load(first, c0);
-  if (live && p.rot > 0) load_angles(p, t, cs, me, kGroup, true);
+  if (live && p.rot > 0) load_angles(p, t, cs, me, kGroup);
   if (live) {
     // dims past rot_dim
     constexpr int kW = 4;
@@ -172,10 +177,14 @@ template <int D, bool BF16, bool NEOX>
 __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, float *smem) {
   constexpr int WU = D > 128 ? D / 128 : 1;  // warps of a unit
   constexpr int SLOTS = kThreads / 32 / WU;  // units at a time
-  constexpr int CPR = D / 8;                 // 16-byte chunks of a row
-  constexpr int RPP = 32 * WU / CPR;         // rows that a unit's lanes hold at once
-  constexpr int NP = PD_SCALE_TOKENS / RPP;
-  __shared__ int slot_of[16 + 2 * PD_SCALE_TOKENS];  // of tokens t0 - 1 ..
+  // a thread has two 16-byte chunks of a row: of K under NeoX's rotation those that
+  // are rotated together, else neighbours
+  constexpr int LPR = D / 16;                // threads of a row
+  constexpr int RPP = 32 * WU / LPR;         // rows that a unit's threads have at once
+  constexpr int NP = PD_SCALE_TOKENS / RPP;  // rows of a thread
+  constexpr int kTokens = 2 * PD_SCALE_TOKENS - 1;      // of a CTA at most
+  __shared__ int slot_of[16 + 2 * PD_SCALE_TOKENS];     // of tokens t0 - 1 ..
+  __shared__ int row_of[PD_MAX_AXES * kTokens];         // the angles' rows of tokens t0 .., axis by axis
   __shared__ float top[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wi = cta / p.slices, slice = cta - wi * p.slices;
@@ -190,27 +199,32 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
     }
     slot_of[i] = s;
   }
+  const bool angles = u0 < p.Hkv && p.rot > 0;
+  if (angles) {
+    for (int i = tid; i < p.axes * kTokens; i += kThreads) {
+      const int axis = i / kTokens, t = t0 + i - axis * kTokens;
+      const int pos = t < p.T ? __ldg(p.positions + axis * p.pos_stride + t) : 0;
+      row_of[i] = min(max(pos, 0), p.max_pos - 1);
+      // (of q's tokens q's CTAs report)
+      if (p.q == nullptr && i - axis * kTokens < p.window && row_of[i] != pos) atomicOr(p.status, PD_DEV_BAD_POSITION);
+    }
+  }
   __syncthreads();
-  // the runs that begin here: a lane looks at a token
-  int n = 0;
+  // the runs that begin here: a lane has token t0 - 1 + lane (31 of them and the one before)
+  int n = 0;              // of the run that begins with token t0 + lane
   uint32_t written = 0;
   {
-    const int s = lane < p.window ? slot_of[lane + 1] : -1;
-    const int blk = s / PD_SCALE_TOKENS, before = slot_of[min(lane, p.window)];
-    if (s >= 0 && (before < 0 || before / PD_SCALE_TOKENS != blk)) {
-      int last = s;
-      written = 1u << (s & 15);
-      for (n = 1; n < PD_SCALE_TOKENS; ++n) {
-        // (lane + 1 + n <= window + 15)
-        const int next = slot_of[lane + 1 + n];
-        if (next < 0 || next / PD_SCALE_TOKENS != blk) break;
-        if (next <= last) {
-          if (slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
-          break;
-        }
-        last = next;
-        written |= 1u << (next & 15);
-      }
+    const int s = lane < p.window + 16 ? slot_of[lane] : -1, before = __shfl_up_sync(0xffffffffu, s, 1);
+    const bool same = s >= 0 && before >= 0 && s / PD_SCALE_TOKENS == before / PD_SCALE_TOKENS;
+    const uint32_t on = __ballot_sync(0xffffffffu, same && s > before);    // goes on with the token before
+    const uint32_t bad = __ballot_sync(0xffffffffu, same && s <= before);  // should
+    const uint32_t first = __ballot_sync(0xffffffffu, s >= 0 && !same) & ~1u;
+    // token t0 + lane is lane + 1 of the masks
+    if (lane < p.window && first >> (lane + 1) & 1u) {
+      const uint32_t after = lane < 30 ? on >> (lane + 2) : 0u;
+      n = min(__ffs(~after), PD_SCALE_TOKENS);  // (ones from there on, and itself)
+      for (int j = 0; j < n; ++j) written |= 1u << (slot_of[lane + 1 + j] & 15);
+      if (lane + 1 + n < 32 && bad >> (lane + 1 + n) & 1u && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
     }
   }
   const uint32_t begins = __ballot_sync(0xffffffffu, n > 0);
@@ -218,21 +232,43 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   const int n_runs = __popc(begins);
   const int lead0 = __ffs(begins) - 1, lead1 = 31 - __clz(begins);
   const int t_end = lead1 + __shfl_sync(0xffffffffu, n, lead1);
-  if (u0 < p.Hkv && p.rot > 0) {
-    // (a warp a token)
-    for (int j = lead0 + warp; j < t_end; j += kThreads / 32)
-      load_angles(p, t0 + j, smem + (j - lead0) * p.rot, lane, 32, p.q == nullptr);
+  const int half = p.rot >> 1;
+  if (angles) {
+    // (pairs of the tokens, eight of a thread at a time; half is 4 at least)
+    const int n = (t_end - lead0) * half;
+#pragma unroll 1
+    for (int i0 = tid; i0 < n; i0 += 8 * kThreads) {
+      float c[8], s[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kThreads, j = i / half, e = i - j * half;
+        if (i < n) {
+          const float *row = p.cos_sin + (int64_t)row_of[p.axis[e] * kTokens + lead0 + j] * p.cs_s0;
+          c[u] = __ldg(row + e);
+          s[u] = __ldg(row + half + e);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kThreads, j = i / half, e = i - j * half;
+        if (i < n) {
+          smem[j * p.rot + e] = c[u];
+          smem[j * p.rot + half + e] = s[u];
+        }
+      }
+    }
     __syncthreads();
   }
-  const int half = p.rot >> 1;
-  const int slot = warp / WU, ut = tid - slot * (32 * WU), ch = ut % CPR, r0 = ut / CPR;
+  const int slot = warp / WU, ut = tid - slot * (32 * WU), ch = ut % LPR, r0 = ut / LPR;
   const int work = n_runs * nu, rounds = (work + SLOTS - 1) / SLOTS;
 #pragma unroll 1
   for (int it = 0; it < rounds; ++it) {
     const int e = it * SLOTS + slot;
     const bool on = e < work;
     const int run = on ? e / nu : 0, u = u0 + (on ? e - run * nu : 0);
-    const int lead = __fns(begins, 0, run + 1);
+    uint32_t later = begins;
+    for (int i = 0; i < run; ++i) later &= later - 1;
+    const int lead = __ffs(later) - 1;
     const int rn = __shfl_sync(0xffffffffu, n, lead);
     const uint32_t mask = __shfl_sync(0xffffffffu, written, lead);
     const bool is_k = u < p.Hkv;
@@ -241,74 +277,80 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
     const int first_slot = slot_of[lead + 1];
     const int page = first_slot / p.P, sub = (first_slot - page * p.P) / PD_SCALE_TOKENS;
     float *scale_at = pool.scale + page * pool.s_page + sub * pool.s_blk + h * pool.s_head;
-    unsigned char *codes = pool.codes + page * pool.page + (int64_t)(sub * PD_SCALE_TOKENS) * pool.tok +
-                           h * pool.head + 8 * ch;
+    unsigned char *codes = pool.codes + page * pool.page + (int64_t)(sub * PD_SCALE_TOKENS) * pool.tok + h * pool.head;
+    const int64_t row = is_k ? p.k_s0 : p.v_s0;
     const unsigned short *src = is_k ? static_cast<const unsigned short *>(p.k) + (int64_t)h * p.k_s1
                                      : static_cast<const unsigned short *>(p.v) + (int64_t)h * p.v_s1;
-    const int64_t row = is_k ? p.k_s0 : p.v_s0;
-    const int t = t0 + lead;
-    const bool turned = is_k && 8 * ch < p.rot;
-    float x[NP][8];
-    float a = 0.f, old = 0.f;
+    src += (int64_t)(t0 + lead) * row;
+    // the chunks' first dims
+    const bool pair = NEOX && is_k && 16 * ch < p.rot;
+    const int da = pair ? 8 * ch : 16 * ch, db = pair ? 8 * ch + half : 16 * ch + 8;
+    // its values in fp32, K's rotated
+    float x[NP][2][8];
+    float old = 0.f, a = 0.f;
     if (on) {
       old = *scale_at;
-      uint4 w[NP], o[NP];
-      const int other = NEOX ? (8 * ch < half ? 8 * ch + half : 8 * ch - half) : 0;
+      uint4 wa[NP], wb[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int j = r0 + RPP * i;
-        w[i] = o[i] = make_uint4(0u, 0u, 0u, 0u);
+        wa[i] = wb[i] = make_uint4(0u, 0u, 0u, 0u);
         if (j < rn) {
-          w[i] = __ldg(reinterpret_cast<const uint4 *>(src + (t + j) * row + 8 * ch));
-          if (NEOX && turned) o[i] = __ldg(reinterpret_cast<const uint4 *>(src + (t + j) * row + other));
+          wa[i] = __ldg(reinterpret_cast<const uint4 *>(src + j * row + da));
+          wb[i] = __ldg(reinterpret_cast<const uint4 *>(src + j * row + db));
         }
       }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const int j = r0 + RPP * i;
-        unpack8<BF16>(w[i], x[i]);
-        if (turned && j < rn) {
-          const float *cs = smem + (lead - lead0 + j) * p.rot;
+        unpack8<BF16>(wa[i], x[i][0]);
+        unpack8<BF16>(wb[i], x[i][1]);
+      }
+      if (is_k && p.rot > 0) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (r0 + RPP * i >= rn) continue;
+          const float *cs = smem + (lead - lead0 + r0 + RPP * i) * p.rot + 8 * ch;
+          float(&y)[8] = x[i][0], (&z)[8] = x[i][1];
           if constexpr (NEOX) {
-            float y[8];
-            unpack8<BF16>(o[i], y);
-            const bool low = 8 * ch < half;
-            const float *c = cs + (low ? 8 * ch : 8 * ch - half);
+            if (!pair) continue;
 #pragma unroll
-            for (int e4 = 0; e4 < 8; e4 += 4) {
-              const float4 co = *reinterpret_cast<const float4 *>(c + e4);
-              const float4 si = *reinterpret_cast<const float4 *>(c + half + e4);
-              const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                float lo, hi;
-                if (low) {
-                  turn(x[i][e4 + z], y[e4 + z], cc[z], ss[z], lo, hi);
-                  x[i][e4 + z] = lo;
-                } else {
-                  turn(y[e4 + z], x[i][e4 + z], cc[z], ss[z], lo, hi);
-                  x[i][e4 + z] = hi;
-                }
-              }
+            for (int e = 0; e < 8; e += 4) {
+              const float4 co = *reinterpret_cast<const float4 *>(cs + e);
+              const float4 si = *reinterpret_cast<const float4 *>(cs + half + e);
+              turn(y[e], z[e], co.x, si.x, y[e], z[e]);
+              turn(y[e + 1], z[e + 1], co.y, si.y, y[e + 1], z[e + 1]);
+              turn(y[e + 2], z[e + 2], co.z, si.z, y[e + 2], z[e + 2]);
+              turn(y[e + 3], z[e + 3], co.w, si.w, y[e + 3], z[e + 3]);
             }
           } else {
-            const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * ch);
-            const float4 si = *reinterpret_cast<const float4 *>(cs + half + 4 * ch);
-            const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              float lo, hi;
-              turn(x[i][2 * z], x[i][2 * z + 1], cc[z], ss[z], lo, hi);
-              x[i][2 * z] = lo;
-              x[i][2 * z + 1] = hi;
+            for (int k = 0; k < 2; ++k) {
+              if (16 * ch + 8 * k >= p.rot) break;
+              float(&v)[8] = x[i][k];
+              const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * k);
+              const float4 si = *reinterpret_cast<const float4 *>(cs + half + 4 * k);
+              turn(v[0], v[1], co.x, si.x, v[0], v[1]);
+              turn(v[2], v[3], co.y, si.y, v[2], v[3]);
+              turn(v[4], v[5], co.z, si.z, v[4], v[5]);
+              turn(v[6], v[7], co.w, si.w, v[6], v[7]);
             }
           }
         }
+      }
+      // (fmaxf leaves NaN out)
 #pragma unroll
-        for (int e8 = 0; e8 < 8; ++e8) {
-          const float m = fabsf(x[i][e8]);
-          a = fmaxf(a, m < INFINITY ? m : 0.f);  // (of finite values)
-        }
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a = fmaxf(a, fmaxf(fabsf(x[i][0][e]), fabsf(x[i][1][e])));
+      if (a == INFINITY) {
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float m = fabsf(x[i][e >> 3][e & 7]);
+            a = fmaxf(a, m < INFINITY ? m : 0.f);  // (of finite values)
+          }
       }
     }
     uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(a));  // (>= 0: ordered as integers)
@@ -329,16 +371,30 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
     const float now = had && !grown ? old : need;
     const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0;
     const float inv = 1.f / now;
+    if (!pow2) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[i][e >> 3][e & 7] = __fdiv_rn(x[i][e >> 3][e & 7], now);
+    }
+    const float by = pow2 ? inv : 1.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int j = r0 + RPP * i;
       if (j >= rn) continue;
-      float c[8];
+      uint32_t c[4];
 #pragma unroll
-      for (int e8 = 0; e8 < 8; ++e8) c[e8] = pow2 ? x[i][e8] * inv : __fdiv_rn(x[i][e8], now);
-      const int off = slot_of[lead + 1 + j] & 15;
-      *reinterpret_cast<uint2 *>(codes + off * pool.tok) =
-          make_uint2(codes4(c[0], c[1], c[2], c[3]), codes4(c[4], c[5], c[6], c[7]));
+      for (int k = 0; k < 4; ++k) {
+        const float *v = &x[i][k >> 1][(k & 1) * 4];
+        c[k] = codes4(v[0] * by, v[1] * by, v[2] * by, v[3] * by);
+      }
+      unsigned char *to = codes + (slot_of[lead + 1 + j] & 15) * pool.tok;
+      if (pair) {
+        *reinterpret_cast<uint2 *>(to + da) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2 *>(to + db) = make_uint2(c[2], c[3]);
+      } else {
+        *reinterpret_cast<uint4 *>(to + da) = make_uint4(c[0], c[1], c[2], c[3]);
+      }
     }
     if (grown) {
       // the block's other codes, to the new scale
@@ -347,13 +403,16 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
       for (int i = 0; i < NP; ++i) {
         const int off = r0 + RPP * i;
         if (mask >> off & 1u) continue;
-        uint2 *at = reinterpret_cast<uint2 *>(codes + off * pool.tok);
-        const uint2 w = *at;
-        float y[4], z[4];
-        floats4(w.x, y);
-        floats4(w.y, z);
-        *at = make_uint2(codes4(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio),
-                         codes4(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio));
+        uint4 *at = reinterpret_cast<uint4 *>(codes + off * pool.tok + 16 * ch);
+        uint4 w = *at;
+        uint32_t *words[4] = {&w.x, &w.y, &w.z, &w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float y[4];
+          floats4(*words[k], y);
+          *words[k] = codes4(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
+        }
+        *at = w;
       }
     }
     __syncwarp();  // (every lane has the old scale)
@@ -362,7 +421,7 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
 }
 
 template <int D, bool BF16, bool NEOX, bool FEW>
-__global__ void __launch_bounds__(kThreads) pd_quant_write(const __grid_constant__ QuantWriteParams p) {
+__global__ void __launch_bounds__(kThreads, FEW ? 1 : kCtas) pd_quant_write(const __grid_constant__ QuantWriteParams p) {
   extern __shared__ __align__(16) float smem_f[];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -372,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) pd_quant_write(const __grid_constant
   else if (FEW)
     q_tokens<D, BF16, NEOX, kThreads, 4>(p, b - p.kv_ctas, smem_f);
   else
-    q_tokens<D, BF16, NEOX, kThreads / 2, 1>(p, 2 * (b - p.kv_ctas), smem_f);
+    q_tokens<D, BF16, NEOX, kThreads / 2, 2>(p, 2 * (b - p.kv_ctas), smem_f);
 }
 
 template <int D>
@@ -497,9 +556,11 @@ extern "C" PD_API int paged_rope_quant_cache_write(
   p.window = 1;
   while (p.window < most && T >= 4LL * num_sms * p.window) p.window *= 2;
   const int slots = head_size > 256 ? 1 : head_size > 128 ? 2 : 4;  // units of a CTA at a time
-  p.units = p.window > 4 ? 2 * slots : slots;
-  p.slices = (2 * num_kv_heads + p.units - 1) / p.units;
   const int64_t windows = (T + p.window - 1) / p.window;
+  // a CTA does one round of units, or where those are more CTAs than the SMs hold K (or V) of all heads (its
+  // slots and angles are read once)
+  p.units = windows * ((2 * num_kv_heads + slots - 1) / slots) > 10LL * num_sms ? std::max(slots, num_kv_heads) : slots;
+  p.slices = (2 * num_kv_heads + p.units - 1) / p.units;
   const bool few = T * 4 < (int64_t)num_sms * 32;
   const int64_t q_ctas = q ? (few ? T : (T + 1) / 2) : 0;
   if (windows * p.slices + q_ctas > INT32_MAX) return PD_EINVAL;
