@@ -116,8 +116,8 @@ PD_API int paged_quant_cache_read(const pd_tensor *k_cache, const pd_tensor *v_c
  *     out = softmax_k(scale * q . (k_scale k_code)) . (v_scale v_code)
  * in fp32 (the softmax weights are rounded to 16 bits for the second product),
  * rounded to q's type; 0 where no key is visible.  Scales of visible keys are
- * positive and finite, 2^-64 to 2^64 (any such numbers, not powers of two alone);
- * keys and values that some row sees are finite.  What no row sees may be
+ * positive, 2^-64 to 2^32 (any such numbers, not powers of two alone; values up to
+ * 448 x 2^32); keys and values that some row sees are finite.  What no row sees may be
  * anything.
  *   q, out       [S * max_query_len, Hq, D], or [T, Hq, D] with query_start
  *   block_table, seq_lens, query_start (or NULL), window, sinks, scale: as in
@@ -139,7 +139,7 @@ PD_API int paged_decode_attn_quant(const pd_tensor *q, const pd_tensor *k_cache,
  * row_groups groups, grid_x CTAs (grid_y > 1: so many runs of sequences, each
  * with its own grid_x), merge = 1 where shares may cut a unit (0: the scratch
  * holds too few parts, every (sequence, kv head, row group) is one CTA's),
- * key_groups warps that take alternate blocks, scratch_needed. */
+ * key_groups warps that take alternate steps of blocks, scratch_needed. */
 PD_API int paged_decode_plan_quant(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
                                    int page_size, int max_query_len, int window, int sinks,
                                    int block_table_width, int num_sms, const pd_scratch *scratch,

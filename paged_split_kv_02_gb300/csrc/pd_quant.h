@@ -68,14 +68,13 @@ constexpr int quant_unit_cost(int D) { return D == 64 ? 80 : D == 128 ? 40 : D =
 // Sequences of one line at most (their lengths and places lie in shared memory).
 constexpr int kQuantSeqs = 448;
 constexpr int kQuantWarps = 8;
-#ifndef QTB
-#define QTB (D == 64 ? (NT <= 2 ? 4 : 2) : D <= 256 ? 2 : 1)
-#define QNS (D >= 256 ? 3 : 6)
-#endif
-// 16-key blocks of a warp's step; slots of its ring, each K or V of a step;
-// n-tiles of 8 packed rows with their sums in registers.
-constexpr int quant_step_blocks(int D, int NT) { return QTB; }
-constexpr int quant_slots(int D, int NT) { return QNS; }
+// 16-key blocks of a warp's step; slots of its ring, each K or V of a step; n-tiles of
+// 8 packed rows with their sums in registers.  The slots take the shared memory that
+// there is; 64 requests of 4,096 tokens, 8 kv heads (2 at D = 256), in us: at D = 64 steps
+// of 1 / 2 / 4 blocks 85 / 70 / 60 (with 32 rows, 16 requests: 37 / 36 / 40), at 128 of 1 / 2 /
+// 4 104 / 89 / 91, with 3 slots for 6 of 2 blocks 93, at 256 of 1 / 2 54 / 53.
+constexpr int quant_step_blocks(int D, int NT) { return D == 64 ? (NT <= 2 ? 4 : 2) : D <= 256 ? 2 : 1; }
+constexpr int quant_slots(int D, int NT) { return D >= 256 ? 3 : 6; }
 constexpr int quant_max_tiles(int D) { return D == 64 ? 4 : 512 / D; }
 constexpr int quant_slot_bytes(int D, int NT) { return quant_step_blocks(D, NT) * 16 * D + 32; }
 // passes over the columns when a CTA's warps add their sums, each in one slot
