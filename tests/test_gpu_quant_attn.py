@@ -274,3 +274,42 @@ def test_a_batch_without_requests_zeroes_its_padding():
     run(dataclasses.replace(qc, case=none), 0, None, out=out)
     torch.cuda.synchronize()
     assert float(out.abs().sum()) == 0.0
+
+
+@pytest.mark.parametrize("D,M", [(64, 4), (128, 1), (512, 2)])
+def test_pages_shared_and_pages_before_a_window(D, M):
+    # two requests begin with the same pages; pages that a window has left are gone from the table
+    case = _case([700, 500, 90], D=D, heads=(8, 2), M=M)
+    table, pool = case.block_table.clone(), case.k_cache.shape[0]
+    table[1, :20] = table[0, :20]
+    assert int(table.max()) < pool
+    _checked(dataclasses.replace(case, block_table=table))
+    for window, sinks in ((100, 0), (100, 20)):
+        cut = table.clone()
+        for s, L in enumerate((700, 500, 90)):
+            first = max(0, L - M + 1 - window) // 16
+            cut[s, -(-sinks // 16):first] = -1
+        qc = quant_case(dataclasses.replace(case, window=window, block_table=table))
+        out = run(dataclasses.replace(qc, case=dataclasses.replace(qc.case, block_table=cut)), sinks, _scratch(case))
+        torch.cuda.synchronize()
+        near(qc, out, sinks)
+
+
+def test_two_streams_at_once():
+    # calls on two streams, each with scratch of its own
+    case = _case([2000, 30, 900], heads=(16, 2), M=2)
+    qc = quant_case(case)
+    outs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    scratch = [_scratch(case) for _ in streams]
+    tensors = [case.q.cuda(), case.block_table.cuda(), case.seq_lens.cuda()]
+    torch.cuda.synchronize()
+    for _ in range(15):
+        for st, sc in zip(streams, scratch):
+            out = torch.zeros_like(tensors[0])
+            st.wait_stream(torch.cuda.current_stream())
+            pd.paged_decode_attn_quant(tensors[0], qc.k, qc.v, qc.ks, qc.vs, tensors[1], tensors[2], out, 16, 2, 128, 16,
+                                       2, 0, 0, case.scale, case.layout, sc, stream=st)
+            outs.append(out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    near(qc, outs[0])

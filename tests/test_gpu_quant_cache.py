@@ -266,6 +266,76 @@ def test_bad_slots_and_positions():
     assert write(list(range(6)), [0, 1, 2, 3, 4, 8]) == pd.DEV_BAD_POSITION
 
 
+def _far(codes, layout, pages):
+    """The same pool, small, and as the last pages of one of 5 GiB."""
+    used = codes.shape[0]
+    big = torch.empty((pages,) + tuple(codes.shape[1:]), dtype=torch.uint8, device="cuda")
+    big[pages - used:] = codes.view(torch.uint8)
+    return big.view(E4M3)
+
+
+def test_offsets_past_32_bits():
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    D, H, P, used = 128, 2, 16, 6
+    pages = (5 << 30) // (P * H * D)
+    c = Cache(8, used, P, H, D, W.HND)
+    codes0, scale0 = [x.copy() for x in c.codes], [x.copy() for x in c.scale]
+    k, v = (_far(t, W.HND, pages) for t in (c.k, c.v))
+    ks, vs = (torch.empty((pages, 1, 2 * 600), device="cuda")[..., ::600] for _ in range(2))
+    for big, s in ((ks, c.ks), (vs, c.vs)):
+        big[pages - used:] = s
+    slots = np.array([0, 1, 2, 30, 31, 80, 81, 82])
+    x = torch.from_numpy(np.random.default_rng(1).standard_normal((2, 8, H, D))).bfloat16()
+    pd.paged_rope_quant_cache_write(None, x[0].cuda(), x[1].cuda(), None, _i32(slots + (pages - used) * P), None, None,
+                                    None, k, v, ks, vs, 0, H, D, 0, P, W.HND)
+    k_out, v_out = (torch.zeros((pages, H, P, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = np.arange(pages - used, pages)[None]
+    pd.paged_quant_cache_read(k, v, ks, vs, _i32(table), _i32([used * P]), _i32(table), k_out, v_out, H, D, P, W.HND)
+    torch.cuda.synchronize()
+    for j, (codes, s, out) in enumerate(((k, ks, k_out), (v, vs, v_out))):
+        Q.store(x[j].double().numpy(), slots, codes0[j], scale0[j])
+        assert np.array_equal(Q.by_token(codes[pages - used:], W.HND), codes0[j])
+        assert np.array_equal(s[pages - used:].cpu().numpy(), scale0[j])
+        want = torch.from_numpy(Q.dequantised(codes0[j], scale0[j])).bfloat16().permute(0, 2, 1, 3)
+        assert torch.equal(out[pages - used:].cpu(), want)
+
+
+def test_write_from_one_projection_and_strided_scales():
+    # q, k, v as views of one tensor of rows, rotated in place; pools and scales as views of wider ones
+    g = np.random.default_rng(12)
+    T, Hq, H, D, P = 37, 8, 2, 128, 32
+    qkv = torch.from_numpy(g.standard_normal((T, Hq + 2 * H, D))).half()
+    dev = qkv.cuda()
+    q, k, v = dev[:, :Hq], dev[:, Hq:Hq + H], dev[:, Hq + H:]
+    c = Cache(12, 4, P, H, D, W.NHD)
+    codes0, scale0 = [x.copy() for x in c.codes], [x.copy() for x in c.scale]
+    wide = [torch.full((8, P, H + 3, D + 16), 0x41, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pools = [w[::2, :, 1:1 + H, 16:] for w in wide]
+    for a, b in zip(pools, (c.k, c.v)):
+        a.copy_(b.view(torch.uint8))
+    ks, vs = (torch.stack([s, s.new_full(s.shape, 5.0)], 1)[:, 0] for s in (c.ks, c.vs))
+    slots = np.arange(5, 5 + T)
+    pos = g.integers(0, 90, T).astype(np.int32)
+    table = W.rope_cos_sin_table(90, D)
+    pd.paged_rope_quant_cache_write(q, k, v, _i32(pos), _i32(slots), table.cuda(), None, q, *(a.view(E4M3) for a in pools),
+                                    ks, vs, Hq, H, D, D, P, W.NHD)
+    torch.cuda.synchronize()
+    x = qkv.double().numpy()
+    axis = pd.rope_pair_axis([D // 2])
+    turned = rope_axes(x, pos[None], table.double().numpy(), axis, D, True)
+    slack = 2.0 ** -22 * (np.abs(x) + np.abs(np.roll(x, D // 2, -1)))
+    got = q.double().cpu().numpy()
+    off = np.abs(got - turned[:, :Hq])
+    assert (off <= 2.0 ** -11 * (np.abs(turned) + slack)[:, :Hq] + slack[:, :Hq] + 2.0 ** -25).all()
+    assert torch.equal(dev[:, Hq:].cpu(), qkv[:, Hq:])
+    c.k, c.v, c.ks, c.vs = (*(a.view(E4M3) for a in pools), ks, vs)
+    _check_write(c, slots, turned[:, Hq:Hq + H], x[:, Hq + H:], slack[:, Hq:Hq + H], codes0, scale0, False)
+    for w, a in zip(wide, pools):
+        a.fill_(0x41)
+        assert bool((w == 0x41).all())
+
+
 # ---------------------------------------------------------------------------
 # The read.
 
@@ -309,6 +379,29 @@ def test_read_pages(P, H):
 
 def test_read_many_requests():
     _read(1, torch.float16, 64, np.random.default_rng(1).integers(0, 90, 3000).tolist(), H=1)
+
+
+def test_read_shares_pages_and_is_captured():
+    # two requests with the same first pages, staged apart; a graph of it, on another stream
+    c = Cache(5, 9, 48, 2, 128, W.HND)
+    table = np.array([[7, 3, 1, -1], [7, 3, 8, 0]])
+    to = np.array([[0, 4, 2, 9], [1, 5, 3, 6]])
+    lens = [100, 150]
+    k, v = (torch.full((10, 2, 48, 128), 9.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    args = [_i32(a) for a in (table, lens, to)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            pd.paged_quant_cache_read(c.k, c.v, c.ks, c.vs, *args, k, v, 2, 128, 48, W.HND)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for x, codes, s in zip((k, v), c.codes, c.scale):
+        want = np.full((10, 48, 2, 128), 9.0)
+        Q.read(Q.dequantised(codes, s), table, lens, to, want)
+        assert torch.equal(x.permute(0, 2, 1, 3).cpu(), torch.from_numpy(want).half())
 
 
 def test_read_reports():
