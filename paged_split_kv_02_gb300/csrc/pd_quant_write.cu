@@ -13,9 +13,9 @@
 // code, which sits on a rounding, does not depend on how a compiler pairs them.
 //
 // Memory-bound: every byte is read or written once but for the rescaled codes.  A
-// prompt of 16,384 tokens, 32 / 8 heads of 128: 74 us, 5.1 TB/s, 75 % of a copy's rate;
-// k and v alone take 34, their loads and codes 23 of them, the rotation the rest.  64
-// tokens, one a request: 4.1 us, 2.5 of them a launch.
+// prompt of 16,384 tokens, 32 / 8 heads of 128: 71 us, 5.3 TB/s, 78 % of a copy's rate;
+// k and v alone take 29 (angles one float at a time, read with two-way bank conflicts:
+// 34), 23 without a rotation.  64 tokens, one a request: 4.4 us, 2.5 of them a launch.
 #include "pd_e4m3.cuh"
 #include "pd_quant.h"
 #include "pd_rope.cuh"
@@ -26,7 +26,7 @@ namespace pd {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kCtas = 5;        // of an SM where tokens are many (the prompt above with 4 / 5 / 6: 78 / 74 / 76 us)
+constexpr int kCtas = 5;        // of an SM where tokens are many (k and v of the prompt above with 5 / 6: 29 / 33 us)
 constexpr int kMaxPairs = 256;  // rot_dim / 2 at head size 512
 constexpr int kLeast = -64;     // the exponent of the least scale
 
@@ -45,7 +45,7 @@ struct QuantWriteParams {
   int window, slices, units;  // tokens of a k/v CTA, CTAs of a window, units of one
   int kv_ctas;                // k/v CTAs come first
   unsigned int *status;
-  uint8_t axis[kMaxPairs];
+  alignas(4) uint8_t axis[kMaxPairs];
 };
 
 __device__ __forceinline__ void turn(float a, float b, float c, float s, float &x, float &y) {
@@ -233,28 +233,39 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   const int lead0 = __ffs(begins) - 1, lead1 = 31 - __clz(begins);
   const int t_end = lead1 + __shfl_sync(0xffffffffu, n, lead1);
   const int half = p.rot >> 1;
+  // where pairs e .. e + 3 lie among a token's cosines (and sines): first the even fours, then the odd
+  // ones, so that the lanes of a row read side by side
+  auto angle_at = [&](int e) { return (e & 4 ? (half + 4) / 8 * 4 : 0) + (e >> 3) * 4; };
   if (angles) {
-    // (pairs of the tokens, eight of a thread at a time; half is 4 at least)
-    const int n = (t_end - lead0) * half;
+    // four pairs of a token at a time, four of those of a thread (half is a multiple of 4)
+    const int quads = half / 4, n = (t_end - lead0) * quads;
 #pragma unroll 1
-    for (int i0 = tid; i0 < n; i0 += 8 * kThreads) {
-      float c[8], s[8];
+    for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+      float4 c[4], s[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kThreads, j = i / half, e = i - j * half;
-        if (i < n) {
-          const float *row = p.cos_sin + (int64_t)row_of[p.axis[e] * kTokens + lead0 + j] * p.cs_s0;
-          c[u] = __ldg(row + e);
-          s[u] = __ldg(row + half + e);
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kThreads, j = i / quads, e = 4 * (i - j * quads);
+        if (i >= n) continue;
+        const uint32_t axes = *reinterpret_cast<const uint32_t *>(p.axis + e), a0 = axes & 0xffu;
+        auto row = [&](uint32_t axis) { return p.cos_sin + (int64_t)row_of[axis * kTokens + lead0 + j] * p.cs_s0; };
+        const float *r = row(a0);
+        if (axes == a0 * 0x01010101u) {
+          c[u] = __ldg(reinterpret_cast<const float4 *>(r + e));
+          s[u] = __ldg(reinterpret_cast<const float4 *>(r + half + e));
+        } else {
+          const float *r1 = row(axes >> 8 & 0xffu), *r2 = row(axes >> 16 & 0xffu), *r3 = row(axes >> 24);
+          c[u] = make_float4(__ldg(r + e), __ldg(r1 + e + 1), __ldg(r2 + e + 2), __ldg(r3 + e + 3));
+          s[u] = make_float4(__ldg(r + half + e), __ldg(r1 + half + e + 1), __ldg(r2 + half + e + 2),
+                             __ldg(r3 + half + e + 3));
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kThreads, j = i / half, e = i - j * half;
-        if (i < n) {
-          smem[j * p.rot + e] = c[u];
-          smem[j * p.rot + half + e] = s[u];
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kThreads, j = i / quads, e = 4 * (i - j * quads);
+        if (i >= n) continue;
+        float *to = smem + j * p.rot + angle_at(e);
+        *reinterpret_cast<float4 *>(to) = c[u];
+        *reinterpret_cast<float4 *>(to + half) = s[u];
       }
     }
     __syncthreads();
@@ -309,14 +320,14 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           if (r0 + RPP * i >= rn) continue;
-          const float *cs = smem + (lead - lead0 + r0 + RPP * i) * p.rot + 8 * ch;
+          const float *cs = smem + (lead - lead0 + r0 + RPP * i) * p.rot + 4 * ch;
           float(&y)[8] = x[i][0], (&z)[8] = x[i][1];
           if constexpr (NEOX) {
             if (!pair) continue;
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
-              const float4 co = *reinterpret_cast<const float4 *>(cs + e);
-              const float4 si = *reinterpret_cast<const float4 *>(cs + half + e);
+              const float4 co = *reinterpret_cast<const float4 *>(cs + angle_at(e));
+              const float4 si = *reinterpret_cast<const float4 *>(cs + half + angle_at(e));
               turn(y[e], z[e], co.x, si.x, y[e], z[e]);
               turn(y[e + 1], z[e + 1], co.y, si.y, y[e + 1], z[e + 1]);
               turn(y[e + 2], z[e + 2], co.z, si.z, y[e + 2], z[e + 2]);
@@ -327,8 +338,8 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
             for (int k = 0; k < 2; ++k) {
               if (16 * ch + 8 * k >= p.rot) break;
               float(&v)[8] = x[i][k];
-              const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * k);
-              const float4 si = *reinterpret_cast<const float4 *>(cs + half + 4 * k);
+              const float4 co = *reinterpret_cast<const float4 *>(cs + angle_at(4 * k));
+              const float4 si = *reinterpret_cast<const float4 *>(cs + half + angle_at(4 * k));
               turn(v[0], v[1], co.x, si.x, v[0], v[1]);
               turn(v[2], v[3], co.y, si.y, v[2], v[3]);
               turn(v[4], v[5], co.z, si.z, v[4], v[5]);
