@@ -1,6 +1,6 @@
 // The rotary embedding of q and k and the store of k and v into an 8-bit cache.
 //
-// Two kinds of CTAs.  Of q: a token, rotated as in pd_rope_axes.cu (the angles in
+// Two kinds of CTAs.  Of q: some tokens, rotated as in pd_rope_axes.cu (a token's angles in
 // shared memory once, a thread keeps one 16-byte chunk of dims and walks the heads).
 // Of k and v: the runs of tokens that begin in a few neighbouring tokens; a run
 // is the new tokens of one 16-token block, and a unit of work is a run's K or V
@@ -25,8 +25,10 @@
 namespace pd {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kLgThreads = 7, kThreads = 1 << kLgThreads;
 constexpr int kCtas = 5;        // of an SM where tokens are many (k and v of the prompt above with 5 / 6: 29 / 33 us)
+constexpr int kWindow = 64;     // tokens of a k/v CTA at most: 16 a warp
+constexpr int kAngleBytes = 40 << 10;  // of their angles
 constexpr int kMaxPairs = 256;  // rot_dim / 2 at head size 512
 constexpr int kLeast = -64;     // the exponent of the least scale
 
@@ -44,6 +46,7 @@ struct QuantWriteParams {
   int64_t num_slots;
   int window, slices, units;  // tokens of a k/v CTA, CTAs of a window, units of one
   int kv_ctas;                // k/v CTAs come first
+  int lg_group;               // log2 of the threads of a token of q
   unsigned int *status;
   alignas(4) uint8_t axis[kMaxPairs];
 };
@@ -68,12 +71,12 @@ __device__ __forceinline__ void load_angles(const QuantWriteParams &p, int t, fl
   }
 }
 
-// q of kThreads / kGroup tokens, kGroup threads each, kU heads in flight.
-template <int D, bool BF16, bool NEOX, int kGroup, int kU>
-__device__ __forceinline__ void q_tokens(const QuantWriteParams &p, int t0, float *smem) {
+// q of some tokens, 2^lg threads each, kU heads in flight.
+template <int D, bool BF16, bool NEOX, int kU>
+__device__ __forceinline__ void q_tokens(const QuantWriteParams &p, int t0, int lg, float *smem) {
   constexpr int kPairs = NEOX ? 8 : 4;  // pairs of a chunk
-  const int me = threadIdx.x % kGroup, t = t0 + threadIdx.x / kGroup;
-  float *cs = smem + (threadIdx.x / kGroup) * p.rot;
+  const int group = 1 << lg, me = threadIdx.x & (group - 1), t = t0 + (threadIdx.x >> lg);
+  float *cs = smem + (threadIdx.x >> lg) * p.rot;
   const int half = p.rot >> 1, chunks = half / kPairs;
   const bool live = t < p.T;
   // (coherent loads: q_out may be q, and a thread reads what it writes, before)
@@ -85,8 +88,8 @@ __device__ __forceinline__ void q_tokens(const QuantWriteParams &p, int t0, floa
     return reinterpret_cast<uint4 *>(static_cast<unsigned short *>(p.q_out) + (int64_t)t * p.qo_s0 +
                                      (int64_t)h * p.qo_s1 + d);
   };
-  const int wide = max(min(chunks, kGroup), 1);  // chunks taken at a time
-  const int h0 = me / wide, c0 = me - h0 * wide, hs = kGroup / wide;
+  const int wide = max(min(chunks, group), 1);  // chunks taken at a time
+  const int h0 = me / wide, c0 = me - h0 * wide, hs = group / wide;
   const int first = live && chunks > 0 && h0 < hs ? h0 : p.Hq;
   uint4 w1[kU], w2[kU];
   auto load = [&](int hh, int c) {
@@ -100,23 +103,23 @@ __device__ __forceinline__ void q_tokens(const QuantWriteParams &p, int t0, floa
     }
   };
   load(first, c0);
-  if (live && p.rot > 0) load_angles(p, t, cs, me, kGroup);
+  if (live && p.rot > 0) load_angles(p, t, cs, me, group);
   if (live) {
     // dims past rot_dim
     constexpr int kW = 4;
     const int pass = (D - p.rot) / 8, n = p.Hq * pass;
 #pragma unroll 1
-    for (int i0 = me; i0 < n; i0 += kW * kGroup) {
+    for (int i0 = me; i0 < n; i0 += kW * group) {
       uint4 w[kW];
 #pragma unroll
       for (int u = 0; u < kW; ++u) {
-        const int i = i0 + u * kGroup;
+        const int i = i0 + u * group;
         w[u] = make_uint4(0u, 0u, 0u, 0u);
         if (i < n) w[u] = *src(i / pass, p.rot + 8 * (i % pass));
       }
 #pragma unroll
       for (int u = 0; u < kW; ++u) {
-        const int i = i0 + u * kGroup;
+        const int i = i0 + u * group;
         if (i < n) *dst(i / pass, p.rot + 8 * (i % pass)) = w[u];
       }
     }
@@ -173,7 +176,8 @@ __device__ __forceinline__ float least_scale(float a) {
   return __uint_as_float((uint32_t)(max(e, kLeast) + 127) << 23);
 }
 
-template <int D, bool BF16, bool NEOX>
+// (FEW: its runs stay in registers, of 16 tokens at most; 0.2 us of a small call)
+template <int D, bool BF16, bool NEOX, bool FEW>
 __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, float *smem) {
   constexpr int WU = D > 128 ? D / 128 : 1;  // warps of a unit
   constexpr int SLOTS = kThreads / 32 / WU;  // units at a time
@@ -182,9 +186,13 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   constexpr int LPR = D / 16;                // threads of a row
   constexpr int RPP = 32 * WU / LPR;         // rows that a unit's threads have at once
   constexpr int NP = PD_SCALE_TOKENS / RPP;  // rows of a thread
-  constexpr int kTokens = 2 * PD_SCALE_TOKENS - 1;      // of a CTA at most
-  __shared__ int slot_of[16 + 2 * PD_SCALE_TOKENS];     // of tokens t0 - 1 ..
-  __shared__ int row_of[PD_MAX_AXES * kTokens];         // the angles' rows of tokens t0 .., axis by axis
+  constexpr int kTokens = kWindow + PD_SCALE_TOKENS - 1;  // of a CTA at most
+  __shared__ int slot_of[1 + kTokens];                     // of tokens t0 - 1 ..
+  __shared__ int row_of[PD_MAX_AXES * kTokens];            // the angles' rows of tokens t0 .., axis by axis
+  // the runs, in order: a warp's at 16 times its number; first token, tokens and the slots of
+  // the block that are written
+  __shared__ int run_count[kThreads / 32], run_lead[kWindow], run_n[kWindow];
+  __shared__ uint32_t run_mask[kWindow];
   __shared__ float top[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wi = cta / p.slices, slice = cta - wi * p.slices;
@@ -201,37 +209,67 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   }
   const bool angles = u0 < p.Hkv && p.rot > 0;
   if (angles) {
-    for (int i = tid; i < p.axes * kTokens; i += kThreads) {
-      const int axis = i / kTokens, t = t0 + i - axis * kTokens;
-      const int pos = t < p.T ? __ldg(p.positions + axis * p.pos_stride + t) : 0;
-      row_of[i] = min(max(pos, 0), p.max_pos - 1);
+    const int lg = p.window > PD_SCALE_TOKENS ? 7 : 5, near = p.window + PD_SCALE_TOKENS - 1;
+    for (int i = tid; i < p.axes << lg; i += kThreads) {
+      const int axis = i >> lg, j = i & ((1 << lg) - 1), t = t0 + j;
+      if (j >= near) continue;
+      const int pos = t < p.T ? __ldg(p.positions + axis * p.pos_stride + t) : 0, row = min(max(pos, 0), p.max_pos - 1);
+      row_of[axis * kTokens + j] = row;
       // (of q's tokens q's CTAs report)
-      if (p.q == nullptr && i - axis * kTokens < p.window && row_of[i] != pos) atomicOr(p.status, PD_DEV_BAD_POSITION);
+      if (p.q == nullptr && j < p.window && row != pos) atomicOr(p.status, PD_DEV_BAD_POSITION);
     }
   }
   __syncthreads();
-  // the runs that begin here: a lane has token t0 - 1 + lane (31 of them and the one before)
-  int n = 0;              // of the run that begins with token t0 + lane
-  uint32_t written = 0;
+  // the runs that begin here: warp w has those of tokens 16 w .. (up to 16 tokens every warp has
+  // them all, and waits for none), a lane token 16 w - 1 + lane: 31 of them and the one before
+  const bool wide = !FEW && p.window > PD_SCALE_TOKENS;
+  int n = 0;              // of the run that begins with token first16 + lane
+  uint32_t written = 0, begins;
+  int n_runs = 0, lead0 = 0, t_end = 0;
   {
-    const int s = lane < p.window + 16 ? slot_of[lane] : -1, before = __shfl_up_sync(0xffffffffu, s, 1);
-    const bool same = s >= 0 && before >= 0 && s / PD_SCALE_TOKENS == before / PD_SCALE_TOKENS;
-    const uint32_t on = __ballot_sync(0xffffffffu, same && s > before);    // goes on with the token before
-    const uint32_t bad = __ballot_sync(0xffffffffu, same && s <= before);  // should
-    const uint32_t first = __ballot_sync(0xffffffffu, s >= 0 && !same) & ~1u;
-    // token t0 + lane is lane + 1 of the masks
-    if (lane < p.window && first >> (lane + 1) & 1u) {
-      const uint32_t after = lane < 30 ? on >> (lane + 2) : 0u;
-      n = min(__ffs(~after), PD_SCALE_TOKENS);  // (ones from there on, and itself)
-      for (int j = 0; j < n; ++j) written |= 1u << (slot_of[lane + 1 + j] & 15);
-      if (lane + 1 + n < 32 && bad >> (lane + 1 + n) & 1u && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
+    const int first16 = wide ? warp * PD_SCALE_TOKENS : 0, own = min(p.window - first16, PD_SCALE_TOKENS);
+    if (own > 0) {
+      const int s = lane < own + 16 ? slot_of[first16 + lane] : -1, before = __shfl_up_sync(0xffffffffu, s, 1);
+      const bool same = s >= 0 && before >= 0 && s / PD_SCALE_TOKENS == before / PD_SCALE_TOKENS;
+      const uint32_t on = __ballot_sync(0xffffffffu, same && s > before);    // goes on with the token before
+      const uint32_t bad = __ballot_sync(0xffffffffu, same && s <= before);  // should
+      const uint32_t first = __ballot_sync(0xffffffffu, s >= 0 && !same) & ~1u;
+      // token first16 + lane is lane + 1 of the masks
+      if (lane < own && first >> (lane + 1) & 1u) {
+        const uint32_t after = lane < 30 ? on >> (lane + 2) : 0u;
+        n = min(__ffs(~after), PD_SCALE_TOKENS);  // (ones from there on, and itself)
+        for (int j = 0; j < n; ++j) written |= 1u << (slot_of[first16 + lane + 1 + j] & 15);
+        if (lane + 1 + n < 32 && bad >> (lane + 1 + n) & 1u && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
+      }
     }
+    begins = __ballot_sync(0xffffffffu, n > 0);
+    if (!FEW && n > 0) {
+      const int at = first16 + __popc(begins & ((1u << lane) - 1));
+      run_lead[at] = first16 + lane;
+      run_n[at] = n;
+      run_mask[at] = written;
+    }
+    if (!FEW && lane == 0) run_count[first16 / PD_SCALE_TOKENS] = __popc(begins);
   }
-  const uint32_t begins = __ballot_sync(0xffffffffu, n > 0);
-  if (begins == 0) return;  // (every warp alike)
-  const int n_runs = __popc(begins);
-  const int lead0 = __ffs(begins) - 1, lead1 = 31 - __clz(begins);
-  const int t_end = lead1 + __shfl_sync(0xffffffffu, n, lead1);
+  if constexpr (FEW) {
+    if (begins == 0) return;  // (every warp alike)
+    n_runs = __popc(begins);
+    lead0 = __ffs(begins) - 1;
+    const int last = 31 - __clz(begins);
+    t_end = last + __shfl_sync(0xffffffffu, n, last);
+  } else {
+    if (wide) __syncthreads();
+    else __syncwarp();
+    for (int w = 0; w < (wide ? kThreads / 32 : 1); ++w) {
+      const int c = run_count[w], at = w * PD_SCALE_TOKENS;
+      if (c > 0) {
+        if (n_runs == 0) lead0 = run_lead[at];
+        t_end = run_lead[at + c - 1] + run_n[at + c - 1];
+      }
+      n_runs += c;
+    }
+    if (n_runs == 0) return;
+  }
   const int half = p.rot >> 1;
   // where pairs e .. e + 3 lie among a token's cosines (and sines): first the even fours, then the odd
   // ones, so that the lanes of a row read side by side
@@ -276,12 +314,25 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   for (int it = 0; it < rounds; ++it) {
     const int e = it * SLOTS + slot;
     const bool on = e < work;
-    const int run = on ? e / nu : 0, u = u0 + (on ? e - run * nu : 0);
-    uint32_t later = begins;
-    for (int i = 0; i < run; ++i) later &= later - 1;
-    const int lead = __ffs(later) - 1;
-    const int rn = __shfl_sync(0xffffffffu, n, lead);
-    const uint32_t mask = __shfl_sync(0xffffffffu, written, lead);
+    int run = on ? e / nu : 0;
+    const int u = u0 + (on ? e - run * nu : 0);
+    int lead, rn;
+    uint32_t mask;
+    if constexpr (FEW) {
+      uint32_t later = begins;
+      for (int i = 0; i < run; ++i) later &= later - 1;
+      lead = __ffs(later) - 1;
+      rn = __shfl_sync(0xffffffffu, n, lead);
+      mask = __shfl_sync(0xffffffffu, written, lead);
+    } else {
+      // (its place: its warp's 16 and its number among them)
+      int at = 0;
+      while (run >= run_count[at]) run -= run_count[at++];
+      at = at * PD_SCALE_TOKENS + run;
+      lead = run_lead[at];
+      rn = run_n[at];
+      mask = run_mask[at];
+    }
     const bool is_k = u < p.Hkv;
     const int h = is_k ? u : u - p.Hkv;
     const QuantPool &pool = is_k ? p.kc : p.vc;
@@ -438,11 +489,9 @@ __global__ void __launch_bounds__(kThreads, FEW ? 1 : kCtas) pd_quant_write(cons
   grid_dependents_launch();
   const int b = blockIdx.x;
   if (b < p.kv_ctas)
-    kv_runs<D, BF16, NEOX>(p, b, smem_f);
-  else if (FEW)
-    q_tokens<D, BF16, NEOX, kThreads, 4>(p, b - p.kv_ctas, smem_f);
+    kv_runs<D, BF16, NEOX, FEW>(p, b, smem_f);
   else
-    q_tokens<D, BF16, NEOX, kThreads / 2, 2>(p, 2 * (b - p.kv_ctas), smem_f);
+    q_tokens<D, BF16, NEOX, FEW ? 4 : 2>(p, (b - p.kv_ctas) << (kLgThreads - p.lg_group), p.lg_group, smem_f);
 }
 
 template <int D>
@@ -561,21 +610,34 @@ extern "C" PD_API int paged_rope_quant_cache_write(
   p.rot = rot_dim;
   p.P = page_size;
   p.num_slots = k_cache->shape[0] * (int64_t)page_size;
-  // Tokens of a k/v CTA: 16 of a prompt (a block or two), fewer while that leaves
-  // SMs without one; the angles of its tokens and 15 more lie in shared memory.
-  const int most = head_size == 512 ? 4 : head_size == 256 ? 8 : 16;
-  p.window = 1;
-  while (p.window < most && T >= 4LL * num_sms * p.window) p.window *= 2;
-  const int slots = head_size > 256 ? 1 : head_size > 128 ? 2 : 4;  // units of a CTA at a time
-  const int64_t windows = (T + p.window - 1) / p.window;
-  // a CTA does one round of units, or where those are more CTAs than the SMs hold K (or V) of all heads (its
-  // slots and angles are read once)
-  p.units = windows * ((2 * num_kv_heads + slots - 1) / slots) > 10LL * num_sms ? std::max(slots, num_kv_heads) : slots;
-  p.slices = (2 * num_kv_heads + p.units - 1) / p.units;
   const bool few = T * 4 < (int64_t)num_sms * 32;
-  const int64_t q_ctas = q ? (few ? T : (T + 1) / 2) : 0;
-  if (windows * p.slices + q_ctas > INT32_MAX) return PD_EINVAL;
-  p.kv_ctas = (int)(windows * p.slices);
+  // Tokens of a k/v CTA, and units: one round of units, and as few tokens as leave at most 10 CTAs
+  // an SM, up to a block's 16, or with few heads as many as make two rounds of units, and up to what
+  // the angles (of them and 15 more) find room for, five CTAs an SM.  Where those are still more CTAs,
+  // K (or V) of all heads, whose slots and angles are read once.  (110,000 tokens of prompts, 8 / 1
+  // heads of 128: 122 us with 16 tokens, 112 with 64; 900 of prompts, 32 / 8 heads of 512: 34 us with 2
+  // tokens and 8 units, 23 with 16 and one.)
+  const int slots = head_size > 256 ? 1 : head_size > 128 ? 2 : 4;  // units of a CTA at a time
+  const int64_t ctas_most = 10LL * num_sms;
+  p.units = slots;
+  auto slices = [&] { return (2 * num_kv_heads + p.units - 1) / p.units; };
+  auto windows = [&] { return (T + p.window - 1) / p.window; };
+  for (p.window = 1; p.window < (few ? PD_SCALE_TOKENS : kWindow) && windows() * slices() > ctas_most; p.window *= 2) {
+    if (p.window >= PD_SCALE_TOKENS && p.window / PD_SCALE_TOKENS * num_kv_heads >= slots) break;
+    if ((2 * p.window + PD_SCALE_TOKENS - 1) * rot_dim * 4 > kAngleBytes) break;
+  }
+  if (windows() * slices() > ctas_most) p.units = (num_kv_heads + slots - 1) / slots * slots;
+  p.slices = slices();
+  // Threads of a token of q: all while tokens are few, else as many as have 8 chunks of 16 bytes
+  // each, from 8 to 64, and 4 CTAs an SM (131,072 tokens, 8 / 1 heads of 128: 224 us with 64, 147
+  // with 16).
+  p.lg_group = kLgThreads;
+  while (!few && p.lg_group > 3 && (p.lg_group == kLgThreads || (int64_t)num_q_heads * head_size < 64 << p.lg_group) &&
+         T << p.lg_group > (int64_t)num_sms * 4 * kThreads)
+    --p.lg_group;
+  const int64_t q_ctas = q ? ((T << p.lg_group) + kThreads - 1) >> kLgThreads : 0;
+  if (windows() * p.slices + q_ctas > INT32_MAX) return PD_EINVAL;
+  p.kv_ctas = (int)(windows() * p.slices);
   const int ctas = p.kv_ctas + (int)q_ctas;
   const int smem = (p.window + PD_SCALE_TOKENS - 1) * rot_dim * 4;
   const bool bf16 = k->dtype == PD_BF16;

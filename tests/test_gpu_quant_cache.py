@@ -177,6 +177,17 @@ def test_write_many_short_runs(D):
            heads=(1, 1))
 
 
+@pytest.mark.parametrize("D,H,rot,axes,neox", [(64, 1, 64, 1, True), (64, 2, 0, 1, True), (128, 1, 96, 4, False),
+                                               (256, 1, 16, 1, True), (512, 1, 8, 2, False)])
+def test_write_few_heads_of_many_tokens(D, H, rot, axes, neox):
+    # windows of up to 64 tokens a CTA: runs of every length in them, at every place
+    g = np.random.default_rng(D)
+    T, runs = 55_000 if D == 64 else 27_000 if D == 128 else 14_000, []
+    while sum(n for _, n in runs) < T:
+        runs.append((int(g.integers(0, 40)), int(g.choice([1, 2, 15, 16, 17, 63, 64, 65, 300, 1000]))))
+    _write(D + H, torch.bfloat16, D, runs, rot=rot, neox=neox, axes=axes, heads=(1 if H == 1 else 2, H), q=D == 64)
+
+
 def test_write_extremes():
     inf, nan = float("inf"), float("nan")
 
