@@ -9,6 +9,7 @@ namespace pd {
 namespace {
 
 constexpr int kSmemLimit = 232448;  // dynamic shared memory of a CTA at most
+constexpr int64_t kFewBytes = 24 << 20;  // of a batch's keys and values, once a row group
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -23,17 +24,32 @@ struct QuantPlan {
 int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks, int bt_width,
               int num_sms, const pd_scratch *scratch, QuantPlan *out) {
   const int64_t R = (int64_t)(Hq / Hkv) * M;
-  const int64_t rg = cdiv(R, 8 * quant_max_tiles(D));
+  int64_t nb_max = cdiv((int64_t)bt_width * P, kBlockKeys);
+  if (window > 0)
+    nb_max = std::min<int64_t>(nb_max, cdiv((int64_t)window + M - 1, kBlockKeys) + 1 +
+                                           cdiv(sinks, kBlockKeys));
+  // Rows of a CTA: as many as fit, so that the cache goes through the SMs as seldom as can be; but
+  // where units are few, fewer, as a step and a unit's end are long with many rows.  Down to 16 rows while
+  // a unit can have two CTAs (32 rows of 8 kv heads, D = 128, one request of 4,096 / 32,768 keys: 22 /
+  // 37 us with 32, 15 / 34 with 16; 64 requests of 4,096, though, 167 and 200), to 8 where the reads are few
+  // too (16 rows: 300 / 4,096 / 32,768 keys 11.1 / 14.3 / 24.9 us with 16, 9.3 / 12.4 / 29.2
+  // with 8), or the units very few at D = 256 (2 kv heads, 30,000 keys: 28.5 and 21.5; 10 requests of
+  // 8,000: 25.9 and 30.1).
+  int tiles = 1;
+  while (tiles < quant_max_tiles(D) && 8 * tiles < R) tiles *= 2;
+  for (int t = tiles / 2; t >= 1; t /= 2) {
+    const int64_t u = (int64_t)S * Hkv * cdiv(R, 8 * t);
+    if (2 * u > num_sms || !scratch || scratch->counter_slots < u) break;
+    if (t == 1 && u * nb_max * (kBlockKeys * 2 * D) > kFewBytes && (D < 256 || 8 * u > num_sms)) break;
+    tiles = t;
+  }
+  const int64_t rg = cdiv(R, 8 * tiles);
   const int rows = (int)cdiv(R, rg);
   int NT = 1;
   while (8 * NT < rows) NT *= 2;
   const int NR = 8 * NT;
   const int64_t HR = Hkv * rg;
   if (HR > 65535) return PD_EINVAL;  // (units of a sequence)
-  int64_t nb_max = cdiv((int64_t)bt_width * P, kBlockKeys);
-  if (window > 0)
-    nb_max = std::min<int64_t>(nb_max, cdiv((int64_t)window + M - 1, kBlockKeys) + 1 +
-                                           cdiv(sinks, kBlockKeys));
   // runs of sequences whose line's places fit an int
   const int64_t per_seq = (nb_max + quant_unit_cost(D)) * HR;
   const int64_t fit = (int64_t)(INT32_MAX / 4) / per_seq;

@@ -313,3 +313,28 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(o, outs[0]) for o in outs)
     near(qc, outs[0])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("heads,M", [((8, 2), 8), ((16, 2), 3), ((8, 2), 3), ((24, 2), 8), ((4, 2), 8)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 20)])
+def test_many_rows_of_many_requests(D, heads, M, window, sinks):
+    # (few units take fewer rows a CTA: these have all that fit, in cut and in whole units)
+    rng = np.random.default_rng(D + M)
+    lens = rng.integers(0, 120, 50).tolist()
+    lens[7], lens[31] = 900, 700
+    case = _case(lens, D=D, heads=heads, M=M, window=window)
+    R = heads[0] // heads[1] * M
+    full = min(-(-R // 8), 4 if D == 64 else 512 // D)
+    plan = pd.paged_decode_plan_quant(50, *heads, D, 16, M, window, sinks, case.block_table.shape[1], 152, _scratch(case))
+    assert plan["n_tiles"] >= full
+    rows = [(int(t), int(t) % heads[0]) for t in rng.integers(0, 50 * M, 150)] + [(7 * M, 0), (32 * M - 1, heads[0] - 1)]
+    _checked(case, sinks, rows=rows)
+
+
+@pytest.mark.parametrize("D,M", [(64, 8), (128, 8), (128, 4), (256, 4)])
+@pytest.mark.parametrize("L", [300, 9000, 40000])
+def test_rows_of_a_few_long_requests(D, M, L):
+    # the rows a CTA are the plan's choice, by the table's width
+    case = _case([L], D=D, heads=(8, 2), M=M)
+    _checked(case, rows=[(t, h) for t in range(M) for h in (0, 3, 7)], splits=256)

@@ -166,6 +166,24 @@ def test_plan(S, Hq, Hkv, D, M, width, splits, window):
     assert pd.paged_decode_plan_quant(1, 32, 8, 128, 16, 1, 0, 0, 2048, 152)["merge"] == 0
 
 
+def test_plan_rows_of_a_cta():
+    def tiles(S, Hq, Hkv, D, M, keys, scratch=True):
+        sd = pd.PdScratch()
+        sd.data, sd.counter_slots = 1 << 30, S * Hkv * pd.COUNTERS_PER_PAIR
+        sd.bytes = pd.paged_decode_scratch_bytes(S, Hq, Hkv, D, M, 256)
+        return pd.paged_decode_plan_quant(S, Hq, Hkv, D, 16, M, 0, 0, keys // 16, 152,
+                                          scratch_desc=sd if scratch else None)["n_tiles"]
+
+    # as many rows as there are, up to what fits, for many units or without scratch; fewer for few
+    assert tiles(64, 32, 8, 128, 8, 4096) == 4 and tiles(64, 32, 8, 128, 1, 4096) == 1
+    assert tiles(1, 32, 8, 128, 8, 320, scratch=False) == 4
+    assert tiles(1, 32, 8, 128, 8, 320) == 1 and tiles(1, 32, 8, 128, 8, 32768) == 2
+    assert tiles(1, 32, 8, 128, 4, 32768) == 2 and tiles(1, 32, 8, 128, 4, 4096) == 1
+    assert tiles(1, 16, 2, 256, 2, 32768) == 1 and tiles(10, 16, 2, 256, 2, 8000) == 2
+    # (rows past the counters of the scratch)
+    assert tiles(1, 512, 1, 128, 8, 4096) == 4
+
+
 def test_plan_refusals():
     ok = [2, 8, 2, 128, 16, 1, 0, 0, 10, 152]
     for at, value, rc in [(0, 0, -1), (1, 7, -1), (2, 0, -1), (3, 80, -3), (4, 8, -1), (5, 9, -4), (6, -1, -1), (7, -1, -1),
