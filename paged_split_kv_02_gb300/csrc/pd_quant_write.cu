@@ -239,8 +239,9 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
         const uint32_t after = lane < 30 ? on >> (lane + 2) : 0u;
         n = min(__ffs(~after), PD_SCALE_TOKENS);  // (ones from there on, and itself)
         for (int j = 0; j < n; ++j) written |= 1u << (slot_of[first16 + lane + 1 + j] & 15);
-        if (lane + 1 + n < 32 && bad >> (lane + 1 + n) & 1u && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
       }
+      // (each token by the CTA, or the warp, that it is one of, whichever has the run before it)
+      if (lane < own && bad >> (lane + 1) & 1u && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
     }
     begins = __ballot_sync(0xffffffffu, n > 0);
     if (!FEW && n > 0) {
