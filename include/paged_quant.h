@@ -41,6 +41,8 @@ extern "C" {
 #define PD_E4M3 4
 
 #define PD_SCALE_TOKENS 16 /* tokens of a page that share a scale */
+#define PD_RUN_DISTANCE 96 /* tokens before a run of a block's new tokens that
+                              are looked through for another run of it */
 
 /* ---- The write ----
  *
@@ -71,11 +73,15 @@ extern "C" {
  *   slot_mapping  [T] int32: the cache slots, distinct, or -1 (padding: q is
  *                 rotated, nothing is stored).  The tokens of one block stand next
  *                 to one another, their slots ascending, as paged_batch_tables
- *                 lays them out; a call writes a block in one such run.
+ *                 lays them out; a call writes a block in one such run.  (Two runs
+ *                 of a block further apart than PD_RUN_DISTANCE tokens are not
+ *                 seen: what the block then holds is undefined until its first
+ *                 token is written again.)
  *   rot_dim       0, or as in paged_rope_cache_write
  * Reported: a position outside the table (clamped) PD_DEV_BAD_POSITION; a slot
- * past the pool, or in a run one that does not ascend (it and the rest of the
- * run are not written): PD_DEV_BAD_SLOT. */
+ * past the pool, in a run one that does not ascend (it and the rest of the run
+ * are not written), or a run whose block one of the PD_RUN_DISTANCE tokens before
+ * it has a slot of (it is not written): PD_DEV_BAD_SLOT. */
 PD_API int paged_rope_quant_cache_write(const pd_tensor *q, const pd_tensor *k, const pd_tensor *v,
                                         const pd_tensor *positions, const pd_tensor *slot_mapping,
                                         const pd_tensor *cos_sin_cache, const uint8_t *pair_axis,

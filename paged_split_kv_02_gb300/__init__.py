@@ -66,6 +66,7 @@ DEV_BAD_SCRATCH, DEV_BAD_POSITION, DEV_BAD_SLOT, DEV_BAD_WORK = 0x10, 0x20, 0x40
 DEV_NO_PAGE = 0x100
 MAX_AXES = 8  # PD_MAX_AXES
 SCALE_TOKENS = 16  # PD_SCALE_TOKENS
+RUN_DISTANCE = 96  # PD_RUN_DISTANCE
 COUNTERS_PER_PAIR = 16  # PD_COUNTERS_PER_PAIR
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",

@@ -28,6 +28,7 @@ namespace {
 constexpr int kLgThreads = 7, kThreads = 1 << kLgThreads;
 constexpr int kCtas = 5;        // of an SM where tokens are many (k and v of the prompt above with 5 / 6: 29 / 33 us)
 constexpr int kWindow = 64;     // tokens of a k/v CTA at most: 16 a warp
+constexpr int kLook = PD_RUN_DISTANCE;  // tokens before a run among which its block may not be
 constexpr int kAngleBytes = 40 << 10;  // of their angles
 constexpr int kMaxPairs = 256;  // rot_dim / 2 at head size 512
 constexpr int kLeast = -64;     // the exponent of the least scale
@@ -187,7 +188,10 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   constexpr int RPP = 32 * WU / LPR;         // rows that a unit's threads have at once
   constexpr int NP = PD_SCALE_TOKENS / RPP;  // rows of a thread
   constexpr int kTokens = kWindow + PD_SCALE_TOKENS - 1;  // of a CTA at most
-  __shared__ int slot_of[1 + kTokens];                     // of tokens t0 - 1 ..
+  // (a CTA of 16 tokens, or 1, loads its slots and those before them in one go)
+  static_assert(kLook + 2 * PD_SCALE_TOKENS <= kThreads, "slots a thread each");
+  __shared__ int slots_at[kLook + kTokens];                // of tokens t0 - kLook ..
+  const int *const slot_of = slots_at + kLook;             // of tokens t0 ..
   __shared__ int row_of[PD_MAX_AXES * kTokens];            // the angles' rows of tokens t0 .., axis by axis
   // the runs, in order: a warp's at 16 times its number; first token, tokens and the slots of
   // the block that are written
@@ -198,14 +202,14 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   const int wi = cta / p.slices, slice = cta - wi * p.slices;
   const int t0 = wi * p.window;
   const int u0 = slice * p.units, nu = min(p.units, 2 * p.Hkv - u0);
-  for (int i = tid; i < p.window + 16; i += kThreads) {
-    const int t = t0 - 1 + i;
+  for (int i = tid; i < kLook + p.window + PD_SCALE_TOKENS - 1; i += kThreads) {
+    const int t = t0 - kLook + i;
     int s = t >= 0 && t < p.T ? __ldg(p.slots + t) : -1;
     if (s >= 0 && s >= p.num_slots) {
       if (slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
       s = -1;
     }
-    slot_of[i] = s;
+    slots_at[i] = s;
   }
   const bool angles = u0 < p.Hkv && p.rot > 0;
   if (angles) {
@@ -229,7 +233,7 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
   {
     const int first16 = wide ? warp * PD_SCALE_TOKENS : 0, own = min(p.window - first16, PD_SCALE_TOKENS);
     if (own > 0) {
-      const int s = lane < own + 16 ? slot_of[first16 + lane] : -1, before = __shfl_up_sync(0xffffffffu, s, 1);
+      const int s = lane < own + 16 ? slot_of[first16 - 1 + lane] : -1, before = __shfl_up_sync(0xffffffffu, s, 1);
       const bool same = s >= 0 && before >= 0 && s / PD_SCALE_TOKENS == before / PD_SCALE_TOKENS;
       const uint32_t on = __ballot_sync(0xffffffffu, same && s > before);    // goes on with the token before
       const uint32_t bad = __ballot_sync(0xffffffffu, same && s <= before);  // should
@@ -238,12 +242,25 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
       if (lane < own && first >> (lane + 1) & 1u) {
         const uint32_t after = lane < 30 ? on >> (lane + 2) : 0u;
         n = min(__ffs(~after), PD_SCALE_TOKENS);  // (ones from there on, and itself)
-        for (int j = 0; j < n; ++j) written |= 1u << (slot_of[first16 + lane + 1 + j] & 15);
+        for (int j = 0; j < n; ++j) written |= 1u << (slot_of[first16 + lane + j] & 15);
       }
       // (each token by the CTA, or the warp, that it is one of, whichever has the run before it)
       if (lane < own && bad >> (lane + 1) & 1u && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
     }
     begins = __ballot_sync(0xffffffffu, n > 0);
+    // a run whose block an earlier one has is left out: two units would write the block at once
+#pragma unroll 1
+    for (uint32_t later = begins; later; later &= later - 1) {
+      const int lead = __ffs(later) - 1, at = first16 + lead - 1 - lane;
+      const uint32_t block = (uint32_t)slot_of[first16 + lead] & ~(uint32_t)(PD_SCALE_TOKENS - 1);
+      bool again = false;
+#pragma unroll
+      for (int i = 0; i < kLook; i += 32) again |= (uint32_t)slot_of[at - i] - block < PD_SCALE_TOKENS;
+      if (!__any_sync(0xffffffffu, again)) continue;
+      if (lane == lead) n = 0;
+      if (lane == 0 && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
+      begins &= ~(1u << lead);
+    }
     if (!FEW && n > 0) {
       const int at = first16 + __popc(begins & ((1u << lane) - 1));
       run_lead[at] = first16 + lane;
@@ -337,7 +354,7 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
     const bool is_k = u < p.Hkv;
     const int h = is_k ? u : u - p.Hkv;
     const QuantPool &pool = is_k ? p.kc : p.vc;
-    const int first_slot = slot_of[lead + 1];
+    const int first_slot = slot_of[lead];
     const int page = first_slot / p.P, sub = (first_slot - page * p.P) / PD_SCALE_TOKENS;
     float *scale_at = pool.scale + page * pool.s_page + sub * pool.s_blk + h * pool.s_head;
     unsigned char *codes = pool.codes + page * pool.page + (int64_t)(sub * PD_SCALE_TOKENS) * pool.tok + h * pool.head;
@@ -451,7 +468,7 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
         const float *v = &x[i][k >> 1][(k & 1) * 4];
         c[k] = codes4(v[0] * by, v[1] * by, v[2] * by, v[3] * by);
       }
-      unsigned char *to = codes + (slot_of[lead + 1 + j] & 15) * pool.tok;
+      unsigned char *to = codes + (slot_of[lead + j] & 15) * pool.tok;
       if (pair) {
         *reinterpret_cast<uint2 *>(to + da) = make_uint2(c[0], c[1]);
         *reinterpret_cast<uint2 *>(to + db) = make_uint2(c[2], c[3]);

@@ -59,3 +59,24 @@ def test_a_whole_run_and_the_next_blocks(T, H):
     for at in (0, 1, 14, 15, 16, 20):
         slots = list(range(16, 36))
         _check(T, H, at, slots, slots, 0)
+
+
+@pytest.mark.parametrize("T,H", SIZES)
+def test_a_block_in_two_runs(T, H):
+    # the first one is written; beside it, with padding or another block between, and as far away as is looked
+    cases = [([16, 17, -1, 18], [16, 17, -1, -1]), ([0, 16, 1], [0, 16, -1]), ([35, 70, 32, 33, 20], [35, 70, -1, -1, 20]),
+             ([5, 3, 40, 6], [5, -1, 40, -1]), ([7, 20, 9, 21, 10], [7, 20, -1, -1, -1])]
+    for gap in (2, 16, 17, 33, 64, 80, pd.RUN_DISTANCE):
+        between = [-1] * (gap - 1)
+        cases.append(([16] + between + [17, 18, 50], [16] + between + [-1, -1, 50]))
+    for at in (0, 1, 14, 16, 31, 47, 63):
+        for slots, kept in cases:
+            if at + len(slots) <= T:
+                _check(T, H, at, slots, kept, pd.DEV_BAD_SLOT)
+
+
+@pytest.mark.parametrize("T,H", SIZES)
+def test_one_run_each_of_many_blocks(T, H):
+    for at in (0, 5, 16):
+        slots = [20, 3, -1, 40, 41, -1, 64, 100, 101, 150]
+        _check(T, H, at, slots, slots, 0)
