@@ -34,4 +34,22 @@ __device__ __forceinline__ void floats4(uint32_t w, float (&x)[4]) {
   x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
 
+// Products and quotients that are rounded again, to 16 or 8 bits: towards zero, and the last bit set
+// where something was cut off.  A value so marked lies on the exact one's side of every number of two
+// bits less, so that the second rounding gives what the exact value would (of results that are
+// normal in fp32, and of infinities and NaN).
+__device__ __forceinline__ float marked(float x, float cut) {
+  return cut != 0.f && fabsf(x) < INFINITY ? __uint_as_float(__float_as_uint(x) | 1u) : x;
+}
+__device__ __forceinline__ float times_marked(float a, float b) {
+  const float x = __fmul_rz(a, b);
+  return marked(x, fmaf(a, b, -x));  // (what was cut off is a float)
+}
+__device__ __forceinline__ float over_marked(float a, float b) {
+  const float x = __fdiv_rz(a, b);
+  return marked(x, fmaf(-x, b, a));  // (so is the remainder)
+}
+
+__device__ __forceinline__ bool power_of_two(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }
+
 }  // namespace pd

@@ -101,13 +101,19 @@ __global__ void __launch_bounds__(kThreads) pd_quant_read(const __grid_constant_
         if (!to[u]) continue;
         const uint32_t words[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
         uint32_t out[8];
+        auto values = [&](auto product) {
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          float x[4];
-          floats4(words[z], x);
-          out[2 * z] = Elem<BF16>::from2(x[0] * f[u], x[1] * f[u]);
-          out[2 * z + 1] = Elem<BF16>::from2(x[2] * f[u], x[3] * f[u]);
-        }
+          for (int z = 0; z < 4; ++z) {
+            float x[4];
+            floats4(words[z], x);
+            out[2 * z] = Elem<BF16>::from2(product(x[0]), product(x[1]));
+            out[2 * z + 1] = Elem<BF16>::from2(product(x[2]), product(x[3]));
+          }
+        };
+        if (power_of_two(f[u]))
+          values([&](float x) { return x * f[u]; });
+        else
+          values([&](float x) { return times_marked(x, f[u]); });  // (4 bits x 24 do not fit fp32)
         uint4 *at = reinterpret_cast<uint4 *>(to[u]);
         at[0] = make_uint4(out[0], out[1], out[2], out[3]);
         at[1] = make_uint4(out[4], out[5], out[6], out[7]);
