@@ -449,13 +449,13 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
     const bool had = old > 0.f && old < INFINITY && !(mask & 1u);
     const bool grown = had && need > old;
     const float now = had && !grown ? old : need;
-    const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0;
+    const bool pow2 = power_of_two(now);
     const float inv = 1.f / now;
     if (!pow2) {
 #pragma unroll
       for (int i = 0; i < NP; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[i][e >> 3][e & 7] = __fdiv_rn(x[i][e >> 3][e & 7], now);
+        for (int e = 0; e < 16; ++e) x[i][e >> 3][e & 7] = over_marked(x[i][e >> 3][e & 7], now);
     }
     const float by = pow2 ? inv : 1.f;
 #pragma unroll
@@ -477,7 +477,7 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
       }
     }
     if (grown) {
-      // the block's other codes, to the new scale
+      // the block's other codes, to the new scale (a power of two: the ratio is exact, or too small to count)
       const float ratio = __fdiv_rn(old, now);
 #pragma unroll 1
       for (int i = 0; i < NP; ++i) {
@@ -490,7 +490,8 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
         for (int k = 0; k < 4; ++k) {
           float y[4];
           floats4(*words[k], y);
-          *words[k] = codes4(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
+          *words[k] = codes4(times_marked(y[0], ratio), times_marked(y[1], ratio), times_marked(y[2], ratio),
+                             times_marked(y[3], ratio));
         }
         *at = w;
       }
