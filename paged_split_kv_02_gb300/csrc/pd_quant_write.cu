@@ -248,19 +248,6 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
       if (lane < own && bad >> (lane + 1) & 1u && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
     }
     begins = __ballot_sync(0xffffffffu, n > 0);
-    // a run whose block an earlier one has is left out: two units would write the block at once
-#pragma unroll 1
-    for (uint32_t later = begins; later; later &= later - 1) {
-      const int lead = __ffs(later) - 1, at = first16 + lead - 1 - lane;
-      const uint32_t block = (uint32_t)slot_of[first16 + lead] & ~(uint32_t)(PD_SCALE_TOKENS - 1);
-      bool again = false;
-#pragma unroll
-      for (int i = 0; i < kLook; i += 32) again |= (uint32_t)slot_of[at - i] - block < PD_SCALE_TOKENS;
-      if (!__any_sync(0xffffffffu, again)) continue;
-      if (lane == lead) n = 0;
-      if (lane == 0 && slice == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
-      begins &= ~(1u << lead);
-    }
     if (!FEW && n > 0) {
       const int at = first16 + __popc(begins & ((1u << lane) - 1));
       run_lead[at] = first16 + lane;
@@ -368,6 +355,7 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
     // its values in fp32, K's rotated
     float x[NP][2][8];
     float old = 0.f, a = 0.f;
+    bool again = false;
     if (on) {
       old = *scale_at;
       uint4 wa[NP], wb[NP];
@@ -380,6 +368,13 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
           wb[i] = __ldg(reinterpret_cast<const uint4 *>(src + j * row + db));
         }
       }
+      // a run whose block one of the tokens before it has is left out: two units would write the block at
+      // once (looked at here, while the rows are on their way)
+      const uint32_t block = (uint32_t)first_slot & ~(uint32_t)(PD_SCALE_TOKENS - 1);
+#pragma unroll
+      for (int i = 0; i < kLook; i += 32) again |= (uint32_t)slot_of[lead - 1 - lane - i] - block < PD_SCALE_TOKENS;
+      again = __any_sync(0xffffffffu, again);
+      if (again && u == 0 && lane == 0) atomicOr(p.status, PD_DEV_BAD_SLOT);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         unpack8<BF16>(wa[i], x[i][0]);
@@ -444,7 +439,7 @@ __device__ __forceinline__ void kv_runs(const QuantWriteParams &p, int cta, floa
     } else {
       a = __uint_as_float(bits);
     }
-    if (!on) continue;  // (whole units)
+    if (!on || again) continue;  // (whole units)
     const float need = least_scale(a);
     const bool had = old > 0.f && old < INFINITY && !(mask & 1u);
     const bool grown = had && need > old;
