@@ -40,6 +40,8 @@ extern "C" {
  * mantissa bits, bias 7, largest 448, no infinities, NaN = 0x7f. */
 #define PD_E4M3 4
 
+#define PD_DEV_BAD_SCALE 0x200u /* paged_decode_attn_quant: the scale of a block with
+                                   visible keys outside 2^-64 .. 2^32 */
 #define PD_SCALE_TOKENS 16 /* tokens of a page that share a scale */
 #define PD_RUN_DISTANCE 96 /* tokens before a run of a block's new tokens that
                               are looked through for another run of it */
@@ -123,8 +125,9 @@ PD_API int paged_quant_cache_read(const pd_tensor *k_cache, const pd_tensor *v_c
  * in fp32 (the softmax weights are rounded to 16 bits for the second product),
  * rounded to q's type; 0 where no key is visible.  Scales of visible keys are
  * positive, 2^-64 to 2^32 (any such numbers, not powers of two alone; values up to
- * 448 x 2^32); keys and values that some row sees are finite.  What no row sees may be
- * anything.
+ * 448 x 2^32, where the write takes any that its input holds); others are reported
+ * as PD_DEV_BAD_SCALE, and the rows that see their keys are undefined.  Keys and
+ * values that some row sees are finite.  What no row sees may be anything.
  *   q, out       [S * max_query_len, Hq, D], or [T, Hq, D] with query_start
  *   block_table, seq_lens, query_start (or NULL), window, sinks, scale: as in
  *                paged_decode_attn_sinks

@@ -63,7 +63,7 @@ STATUS_NAMES = {
 }
 DEV_WAIT_TIMEOUT, DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_BAD_QSTART = 0x1, 0x2, 0x4, 0x8
 DEV_BAD_SCRATCH, DEV_BAD_POSITION, DEV_BAD_SLOT, DEV_BAD_WORK = 0x10, 0x20, 0x40, 0x80
-DEV_NO_PAGE = 0x100
+DEV_NO_PAGE, DEV_BAD_SCALE = 0x100, 0x200
 MAX_AXES = 8  # PD_MAX_AXES
 SCALE_TOKENS = 16  # PD_SCALE_TOKENS
 RUN_DISTANCE = 96  # PD_RUN_DISTANCE

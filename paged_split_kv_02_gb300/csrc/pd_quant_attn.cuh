@@ -47,6 +47,11 @@ namespace pd {
 // would pass 2^15 (a half's largest is 2^16), to where the largest is 2^7, so it
 // moves rarely and P loses bits of its 11 below 2^-21 of the largest alone.
 constexpr float kQuantTop = 7.f, kQuantMost = 15.f;
+// 2^-64 and 2^32 as bits, the range of the scales: what is not a positive number of
+// it (NaN and infinity too) lies past it as a number without a sign.  The largest of
+// a piece is kept, two instructions a block, and looked at when the piece ends: 0 to
+// 1.6 % of a call (a test in each step 1 to 7, one of each run of steps 0 to 5).
+constexpr uint32_t kQuantLeast = (127u - 64) << 23, kQuantLargest = (127u + 32) << 23;
 
 // 4- and 16-byte copies global -> shared by address, and this thread's groups.
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void *src) {
@@ -437,12 +442,17 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
         }
       }
       if (!is_v) {
-        // a lane a scale: K's and V's of a block side by side
+        // a lane a scale: K's and V's of a block side by side (of one that is not there: 1, which is
+        // in the range)
         const int from = at * TB + (lane >> 1) % TB;
         const int64_t there = __shfl_sync(0xffffffffu, k_at, from);
         const int64_t ks = __shfl_sync(0xffffffffu, ks_at, from), vs = __shfl_sync(0xffffffffu, vs_at, from);
-        if (lane < 2 * TB && there >= 0)
-          copy_async4(slot + TB * BLOCK + lane * 4, lane & 1 ? p.v.scale + vs : p.k.scale + ks);
+        if (lane < 2 * TB) {
+          if (there >= 0)
+            copy_async4(slot + TB * BLOCK + lane * 4, lane & 1 ? p.v.scale + vs : p.k.scale + ks);
+          else
+            reinterpret_cast<float *>(ring + in_slot * SLOT + TB * BLOCK)[lane] = 1.f;
+        }
       } else {
         ++at;
         if (look) {
@@ -584,6 +594,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
       }
     }
     bool settled = false;  // every row has its reference
+    uint32_t past = 0;     // how far scales lie past their range, as numbers
     uint32_t pb[TB][NT][2];
     if (k < 0) {
 #pragma unroll 1
@@ -658,6 +669,8 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
         const float2 kv = scales[b];
+        past = __viaddmax_u32(__float_as_uint(kv.x), 0u - kQuantLeast, past);
+        past = __viaddmax_u32(__float_as_uint(kv.y), 0u - kQuantLeast, past);
         const float lg = __log2f(kv.y);
         inv[b] = sfu_rcp(kv.y);
 #pragma unroll
@@ -803,6 +816,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps, 1) pd_quant_decode(const __g
         ml_of[(8 * n + 2 * lane + 1) * NW + warp] = make_float2(l[n][1] > 0.f ? mu[n][1] : -INFINITY, l[n][1]);
       }
     }
+    if (past > kQuantLargest - kQuantLeast && lane == 0) atomicOr(p.status, PD_DEV_BAD_SCALE);
     if (lane == 0) free_slot[warp] = (warp * NS + in_slot) * SLOT;
     const bool cut = q.parts > 1;
     __syncwarp();  // (every lane has read the slot)
