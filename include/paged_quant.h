@@ -59,11 +59,16 @@ extern "C" {
  *                                   finite number counts as 0)
  *     code  = x / scale rounded to the nearest code, ties to even
  * and where an old scale grew, the block's other codes are rounded to the new
- * one (code x old / new): each keeps its value to half a step of the new scale.
- * A value is then at most 2^-4 of itself off, or 2^-10 x scale where it is below
- * 2^-6 x scale.  Scales are powers of two, so x / scale is exact and a call's
- * result does not depend on how its sums are ordered.  Infinities are stored
- * as 448 x scale and NaN as NaN; neither counts in a.
+ * one (code x old / new): a value is half a step of the new scale off what it was
+ * held as.  A value that is written is at most 2^-4 of itself off, or 2^-10 x scale
+ * where it is below 2^-6 x scale; each time that its block's scale grows after that
+ * adds 2^-10 x the new scale at most, all of them together less than 2^-9 x the last
+ * one.  (Scales are powers of two, so x / scale is exact, a code that stays above 2^-6
+ * keeps its bits, and a call's result does not depend on how its sums are ordered.
+ * Of an old scale that is none, each growth is a rounding of its own.)  A scale never
+ * shrinks before its block starts anew: a draft token that is taken back leaves it
+ * as it made it.  Infinities are stored as 448 x scale and NaN as NaN; neither counts
+ * in a.
  *
  *   q, q_out      [T, Hq, D] fp16/bf16, or both NULL: k and v alone (num_q_heads
  *                 is then ignored); q_out may be q itself
