@@ -106,7 +106,8 @@ PD_API int paged_rope_quant_cache_write(const pd_tensor *q, const pd_tensor *k, 
  * which paged_prefill_attn (or any call on a 16-bit pool) takes with out_table
  * as its block table.  A negative entry of either table leaves the page out
  * (pages before a window; pages staged earlier), and the slots past a request's
- * last token are left as they were.
+ * last token are left as they were.  Every entry of the tables is looked at: a
+ * call over tables far wider than the requests takes longer.
  *   block_table, out_table  [S, W] int32
  *   seq_lens                [S] int32
  *   k_out, v_out            fp16/bf16 pools [num_out_blocks, ...] in the same
@@ -139,7 +140,9 @@ PD_API int paged_quant_cache_read(const pd_tensor *k_cache, const pd_tensor *v_c
  *   scratch      paged_decode_scratch_bytes / _init, as for paged_decode_attn;
  *                NULL or a small one: fewer CTAs share the keys
  * The launch runs one wave of CTAs that take equal shares of all requests'
- * keys; paged_decode_plan_quant gives its numbers (path 7). */
+ * keys (past 448 requests a wave for each 448 of them); paged_decode_plan_quant gives
+ * its numbers (path 7).  How many rows a CTA takes is chosen by the table's
+ * width: the lengths are on the device. */
 PD_API int paged_decode_attn_quant(const pd_tensor *q, const pd_tensor *k_cache,
                                    const pd_tensor *v_cache, const pd_tensor *k_scale,
                                    const pd_tensor *v_scale, const pd_tensor *block_table,

@@ -34,7 +34,9 @@ int make_plan(int S, int Hq, int Hkv, int D, int P, int M, int window, int sinks
   // 37 us with 32, 15 / 34 with 16; 64 requests of 4,096, though, 167 and 200), to 8 where the reads are few
   // too (16 rows: 300 / 4,096 / 32,768 keys 11.1 / 14.3 / 24.9 us with 16, 9.3 / 12.4 / 29.2
   // with 8), or the units very few at D = 256 (2 kv heads, 30,000 keys: 28.5 and 21.5; 10 requests of
-  // 8,000: 25.9 and 30.1).
+  // 8,000: 25.9 and 30.1).  All of these with tables as wide as the requests: the width is what the host
+  // knows, so that a short request in a wide table gets the rows of a long one (300 keys of 16 rows: 9.4
+  // us with 19 pages, 11.0 with 512 or more).  The 24 MB lie between measured 17 and 134.
   int tiles = 1;
   while (tiles < quant_max_tiles(D) && 8 * tiles < R) tiles *= 2;
   for (int t = tiles / 2; t >= 1; t /= 2) {
