@@ -65,10 +65,9 @@ extern "C" {
  * adds 2^-10 x the new scale at most, all of them together less than 2^-9 x the last
  * one.  (Scales are powers of two, so x / scale is exact, a code that stays above 2^-6
  * keeps its bits, and a call's result does not depend on how its sums are ordered.
- * Of an old scale that is none, each growth is a rounding of its own.)  A scale never
- * shrinks before its block starts anew: a draft token that is taken back leaves it
- * as it made it.  Infinities are stored as 448 x scale and NaN as NaN; neither counts
- * in a.
+ * The growth of an old scale that is none rounds every code.)  A scale never shrinks
+ * before its block starts anew: a draft token that is taken back leaves it as it made
+ * it.  Infinities are stored as 448 x scale and NaN as NaN; neither counts in a.
  *
  *   q, q_out      [T, Hq, D] fp16/bf16, or both NULL: k and v alone (num_q_heads
  *                 is then ignored); q_out may be q itself
